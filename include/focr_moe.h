@@ -429,6 +429,136 @@ focr_status focr_rswa_decode(const float* q, const float* k_new, const float* v_
                              const int32_t* n_gen, int32_t B, float* out, void* workspace, size_t ws_bytes,
                              void* stream);
 
+/* ------------------------------------------------------------------ speculative decode step
+ * Operators of a decode step that scores several drafted tokens per sequence over a quantised R-SWA cache:
+ * rotate q and k, write rows into the cache, attend from a tree of drafted nodes, turn the lm_head's logits into
+ * probabilities, verify the drafts, commit the accepted ones to the ring.  Source of the geometry: franken_ocr README,
+ * "Design Philosophy" and "Architecture" (R-SWA), frankenocr.pages.dev, "One forward pass", steps 6 and 7, and
+ * "Four bits, one shared scale" (the codes).  The pages fix none of these formulas; each call states its own.
+ * Every call is asynchronous on `stream`, needs no workspace, holds no state between calls and gives the same bits
+ * for the same inputs.  Calls may overlap as long as no buffer that one of them writes is used by another.
+ */
+#define FOCR_HEADS_MAX 128          /* most heads (query or kv) of these calls */
+#define FOCR_TREE_NODES_MAX 64      /* most drafted nodes x query heads per kv head */
+#define FOCR_KV_N_MAX 32768         /* most tokens per sequence of one focr_kv_write */
+#define FOCR_V_MAX 1048576          /* largest vocabulary of focr_token_probs / focr_spec_verify */
+
+/*
+ * focr_qk_norm_rope -- per-head norms (optional) and position rotation of q and k in one pass.
+ * For each head row x[128] of token t:
+ *     y = x / sqrt(mean(x^2) + eps) * gamma        with FOCR_QK_NORM (gamma NULL: ones), else y = x;
+ *     angle_i = pos[t] * theta^(-2i / rot_dim), i < rot_dim / 2 (formed in fp64);
+ *     (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin) for the pair (a, b) = (i, i + rot_dim / 2), or
+ *     (2i, 2i + 1) with FOCR_ROPE_INTERLEAVED;  dims >= rot_dim pass through.
+ *   q, k, q_out, k_out: DEVICE fp32, token t's row at ptr + t * ld, its heads x 128 values contiguous; ld is in
+ *     floats, at least heads * 128 and a multiple of 4 (so q and k may be columns of a fused projection's rows).
+ *     An output may be its own input (same pointer and ld); any other shared element is refused.
+ *   heads_k may be 0 (k, k_out ignored).  pos: DEVICE int32 [T], any value.  gamma_q, gamma_k: DEVICE fp32 [128] or
+ *   NULL.  1 <= T <= FOCR_T_MAX; rot_dim even in [2, 128]; theta > 0.  Float pointers 16-byte aligned.
+ * Errors: FOCR_ERR_INVALID_ARG, FOCR_ERR_UNSUPPORTED (rot_dim), FOCR_ERR_CUDA.
+ */
+#define FOCR_QK_NORM 1
+#define FOCR_ROPE_INTERLEAVED 2
+focr_status focr_qk_norm_rope(const float* q, int64_t ldq, int32_t heads_q, const float* k, int64_t ldk,
+                              int32_t heads_k, const int32_t* pos, int32_t T, const float* gamma_q,
+                              const float* gamma_k, float eps, double theta, int32_t rot_dim, int32_t flags,
+                              float* q_out, int64_t ldqo, float* k_out, int64_t ldko, void* stream);
+
+/*
+ * A quantised key/value cache, caller-owned: the reference blocks or the rings of B sequences.
+ *   k, v: DEVICE codes [B][heads][cap][128] int8 (FOCR_W_INT8), or [B][heads][cap][64] bytes of two nibbles
+ *     (FOCR_W_INT4; element 2j in bits 0-3, 2j + 1 in bits 4-7), 16-byte aligned;
+ *   k_scale, v_scale: DEVICE fp32 [B][heads][cap].
+ *   A row's values are scale * code.  1 <= B <= FOCR_RSWA_B_MAX, heads <= FOCR_HEADS_MAX, cap <= FOCR_RSWA_RCAP_MAX.
+ */
+typedef struct focr_kv_cache {
+    void* k;
+    float* k_scale;
+    void* v;
+    float* v_scale;
+    int32_t type;    /* FOCR_W_INT8 or FOCR_W_INT4 */
+    int32_t B, heads, cap;
+} focr_kv_cache;
+
+/*
+ * focr_kv_write -- quantise rows of K and V and write them into a cache.
+ *   s = fp32(max|x|) / Q (one fp32 division; Q = 127 int8, 7 int4), q = round-half-even(fp32(x / s)) clamped to
+ *   [-127, 127] or [-8, 7]; s = 0: q = 0.  Inputs must be finite.
+ *   k, v: DEVICE fp32, row r at ptr + r * ld (ld in floats, >= heads * 128, a multiple of 4), 0 <= r < n_rows.
+ *   For sequence b and i < count[b]: source row r = (row0 ? row0[b] : b * n_max) + (index ? index[b * n_max + i] : i)
+ *   goes to slot start[b] + i, or (start[b] + i) mod cap with FOCR_KV_WRAP.  With more tokens than slots the last
+ *   cap tokens are written.  The same source row may be given twice.
+ *   row0, count, start: DEVICE int32 [B]; index: DEVICE int32 [B][n_max] or NULL (entries i >= count[b] are not read).
+ *   A sequence whose count is outside [0, n_max], whose start is negative, or whose rows do not fit (without
+ *   FOCR_KV_WRAP) writes nothing; a token whose source row is outside [0, n_rows) is left out.  Rows that no token
+ *   goes to keep their contents.
+ * Errors: FOCR_ERR_INVALID_ARG, FOCR_ERR_UNSUPPORTED (type), FOCR_ERR_CUDA.
+ */
+#define FOCR_KV_WRAP 1
+focr_status focr_kv_write(const focr_kv_cache* c, const float* k, int64_t ldk, const float* v, int64_t ldv,
+                          int64_t n_rows, const int32_t* row0, const int32_t* count, const int32_t* index,
+                          int32_t n_max, const int32_t* start, int32_t flags, void* stream);
+
+/*
+ * focr_kv_read -- the fp32 values of rows 0 .. len[b] - 1 of each sequence: k_out, v_out DEVICE fp32
+ * [B][heads][cap][128] (the layout focr_rswa_decode takes), 16-byte aligned.  Rows >= len[b] of the outputs are left
+ * as they were, as are all rows of a sequence whose len is outside [0, cap].
+ */
+focr_status focr_kv_read(const focr_kv_cache* c, const int32_t* len, float* k_out, float* v_out, void* stream);
+
+/*
+ * focr_rswa_tree -- R-SWA attention of a tree of drafted tokens over a quantised reference block and ring; with one
+ * node the single-token form.  Node i < n_nodes[b] of sequence b has parent[b][i] in [-1, i) (-1: the last committed
+ * token) and depth d (0 for a child of the last committed token).  With n = n_gen[b] committed generated tokens
+ * (positions 0 .. n - 1, token p in ring slot p mod 128) it stands at position n + d and sees the reference rows
+ * 0 .. ref_len[b] - 1, the ring's tokens max(0, n - 128, n + d - 127) .. n - 1, its ancestors and itself:
+ *     out = sum_j softmax_j(q . k_j / sqrt(128)) v_j;   query head x reads kv head x / (heads_q / heads).
+ * The ring is not written: focr_kv_write with FOCR_KV_WRAP commits accepted nodes.
+ *   q, out: DEVICE fp32 [B][N][heads_q][128]; k_new, v_new: DEVICE fp32 [B][N][heads][128] (heads of the caches),
+ *   finite for live nodes; 16-byte aligned.  parent: DEVICE int32 [B][N] or NULL (a chain: parent of i is i - 1).
+ *   n_nodes: DEVICE int32 [B] or NULL (N each).  ref_len, n_gen: DEVICE int32 [B].
+ *   ref and ring: caches of B sequences, the same heads and type; ring->cap = 128.
+ *   1 <= N, N * heads_q / heads <= FOCR_TREE_NODES_MAX.
+ *   Rows of nodes >= n_nodes[b] are left as they were.  A sequence with ref_len outside [0, ref->cap], n_gen < 0,
+ *   n_nodes outside [0, N] or a bad parent of a live node gets NaN (in all N rows if n_nodes is the bad value).
+ * Errors: FOCR_ERR_INVALID_ARG, FOCR_ERR_UNSUPPORTED (types, ring size, heads), FOCR_ERR_CUDA.
+ */
+focr_status focr_rswa_tree(const float* q, const float* k_new, const float* v_new, int32_t B, int32_t N,
+                           int32_t heads_q, const focr_kv_cache* ref, const int32_t* ref_len,
+                           const focr_kv_cache* ring, const int32_t* n_gen, const int32_t* parent,
+                           const int32_t* n_nodes, float* out, void* stream);
+
+/*
+ * focr_token_probs -- probs[t] = softmax(logits[t] / temperature), DEVICE fp32 [T][V], fp32 arithmetic.  probs may be
+ * logits.  A logit of -inf has probability 0; a row without a finite maximum is NaN.
+ * 1 <= T <= FOCR_T_MAX, 1 <= V <= FOCR_V_MAX, temperature > 0.
+ */
+focr_status focr_token_probs(const float* logits, int32_t T, int32_t V, float temperature, float* probs, void* stream);
+
+/*
+ * focr_spec_verify -- verify a tree of drafted tokens against the target's probabilities, keeping the target's
+ * distribution (siblings must be independent draws from the draft's distribution behind their parent).
+ *   target: DEVICE fp32 [B][N + 1][V]; row 0 is the distribution behind the last committed token, row i + 1 the one
+ *     behind node i.  draft: DEVICE fp32 [B][N][V], row r the distribution that the children of row r's token were
+ *     drawn from (row 0: behind the last committed token, row i + 1: behind node i), or NULL: the drafts were chosen,
+ *     not drawn.  Probabilities are finite and not negative; only rows that the walk reaches are read.
+ *   tokens: DEVICE int32 [B][N], in [0, V); parent, n_nodes: as for focr_rswa_tree.
+ *   u: DEVICE fp32 [B][N + 1] uniforms in [0, 1): u[i] tests node i, u[N] samples the next token.
+ * The nodes are tried in index order: node i is tried if its parent is the last accepted node cur (the root at
+ * first).  With p, q the rows behind cur, W(t) = max(p(t) - c q(t), 0), c = 0 and M = 1 at first:
+ *     accept iff u_i * q(x_i) * M < W(x_i): cur = i, c = 0, M = 1;   else c += M, M = sum_t W(t).
+ *   Without a draft W = p: accept iff u_i * M < W(x_i); else M -= W(x_i), W(x_i) = 0.
+ * next_token = the smallest t with W(t) > 0 and sum_{t' <= t} W(t') > u_N * sum W, W behind the last accepted node
+ * (if W is zero everywhere, p; if rounding leaves no such t, the last t with W(t) > 0).  All in fp64.
+ *   n_accept: DEVICE int32 [B]; path: DEVICE int32 [B][N], the accepted nodes in order, then -1;
+ *   next_token: DEVICE int32 [B].  A sequence with n_nodes outside [0, N], a bad parent or a bad token of a live node
+ *   gets n_accept = next_token = -1 and a path of -1.
+ * 1 <= B <= FOCR_RSWA_B_MAX, 1 <= N <= FOCR_TREE_NODES_MAX, 1 <= V <= FOCR_V_MAX.
+ */
+focr_status focr_spec_verify(const float* target, const float* draft, int32_t V, const int32_t* tokens,
+                             const int32_t* parent, const int32_t* n_nodes, const float* u, int32_t B, int32_t N,
+                             int32_t* n_accept, int32_t* path, int32_t* next_token, void* stream);
+
 /*
  * focr_tc_selftest -- diagnostic: one tensor-core tile through the library's tcgen05 primitives
  * (the ones the T > 8 grouped kernel uses), to check them against a host GEMM.

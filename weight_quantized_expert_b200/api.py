@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import typing
 
 import numpy as np
 
@@ -35,7 +36,8 @@ EXPORTED = (
     "focr_dense_mlp_free", "focr_dense_mlp_export_quantized", "focr_dense_mlp_forward", "focr_tc_selftest",
     "focr_decode_step_workspace_bytes", "focr_decode_step", "focr_w8a8_pack", "focr_w8a8_free",
     "focr_w8a8_export", "focr_w8a8_quantize_x", "focr_w8a8_workspace_bytes", "focr_w8a8_gemv", "focr_w8a8_check",
-    "focr_lm_head_check", "focr_rswa_workspace_bytes", "focr_rswa_decode",
+    "focr_lm_head_check", "focr_rswa_workspace_bytes", "focr_rswa_decode", "focr_qk_norm_rope", "focr_kv_write",
+    "focr_kv_read", "focr_rswa_tree", "focr_token_probs", "focr_spec_verify",
 )
 FWD_RESIDUAL = 1
 FWD_DETERMINISTIC = 2
@@ -67,6 +69,12 @@ _lock = threading.Lock()
 class DecodeModelDesc(ctypes.Structure):
     _fields_ = [("dense", ctypes.c_void_p), ("moe", ctypes.POINTER(ctypes.c_void_p)), ("n_moe", ctypes.c_int32),
                 ("gamma", ctypes.POINTER(ctypes.c_void_p)), ("eps", ctypes.c_float), ("head", ctypes.c_void_p)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("type", ctypes.c_int32), ("B", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("cap", ctypes.c_int32)]
 
 
 def lib():
@@ -115,6 +123,14 @@ def lib():
                 "focr_lm_head_check": (i32, [P, P]),
                 "focr_rswa_workspace_bytes": (sz, [i32, i32]),
                 "focr_rswa_decode": (i32, [P, P, P, P, P, P, i32, P, P, P, i32, P, P, sz, P]),
+                "focr_qk_norm_rope": (i32, [P, i64, i32, P, i64, i32, P, i32, P, P, ctypes.c_float, ctypes.c_double,
+                                            i32, i32, P, i64, P, i64, P]),
+                "focr_kv_write": (i32, [ctypes.POINTER(KVCacheDesc), P, i64, P, i64, i64, P, P, P, i32, P, i32, P]),
+                "focr_kv_read": (i32, [ctypes.POINTER(KVCacheDesc), P, P, P, P]),
+                "focr_rswa_tree": (i32, [P, P, P, i32, i32, i32, ctypes.POINTER(KVCacheDesc), P,
+                                         ctypes.POINTER(KVCacheDesc), P, P, P, P, P]),
+                "focr_token_probs": (i32, [P, i32, i32, ctypes.c_float, P, P]),
+                "focr_spec_verify": (i32, [P, P, i32, P, P, P, P, i32, i32, P, P, P, P]),
                 "focr_last_error": (ctypes.c_char_p, []),
                 "focr_version": (ctypes.c_char_p, []),
             }
@@ -406,6 +422,210 @@ def focr_rswa_decode(q, k_new, v_new, k_ref, v_ref, ref_len, k_ring, v_ring, n_g
                                   _ptr(k_ring), _ptr(v_ring), _ptr(n_gen), B, _ptr(out), _ptr(workspace),
                                   workspace.numel(), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- speculative decode step
+
+QK_NORM, ROPE_INTERLEAVED, KV_WRAP = 1, 2, 1
+
+
+def _require(ok, msg: str):
+    if not ok:
+        raise FocrError(1, msg)
+
+
+def _same_device(dev, dtype, **tensors):
+    """Every given tensor (None: absent) is on `dev`, has `dtype` and is contiguous."""
+    for name, t in tensors.items():
+        if t is not None and not (t.device == dev and t.dtype == dtype and t.is_contiguous()):
+            raise FocrError(1, f"{name}: a contiguous {dtype} tensor on {dev} is needed, "
+                               f"got {t.dtype} on {t.device}, strides {t.stride()}")
+
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with `dev` current; stream None: the current stream of `dev`."""
+    import torch
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
+
+
+def _new(make, dev, stream):
+    """A tensor made by `make`, in the memory pool of the stream it is going to be written on."""
+    import torch
+    if stream is None:
+        return make()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def focr_qk_norm_rope(q, k, pos, gamma_q=None, gamma_k=None, eps: float = 1e-6, theta: float = 10000.0,
+                      rot_dim: int = 128, interleaved: bool = False, norm: bool = False, q_out=None, k_out=None,
+                      stream=None):
+    """Per-head norms (norm=True) and rotation of q [T, heads_q, 128] and k [T, heads_k, 128] (or None) at pos [T] int32.
+    Tokens may be strided (columns of a fused projection).  q_out / k_out may be q / k.  Returns (q_out, k_out)."""
+    import torch
+    dev = q.device
+    _require(q.is_cuda and pos.dtype == torch.int32 and pos.shape == (q.shape[0],), "q on a GPU and pos int32 [T] are needed")
+    _same_device(dev, torch.int32, pos=pos)
+    _same_device(dev, torch.float32, gamma_q=gamma_q, gamma_k=gamma_k)
+    for g in (gamma_q, gamma_k):
+        _require(g is None or g.shape == (RSWA_DIM,), "gamma must be [128]")
+    if q_out is None:
+        q_out = _new(lambda: torch.empty(q.shape, dtype=q.dtype, device=dev), dev, stream)
+    if k is not None and k_out is None:
+        k_out = _new(lambda: torch.empty(k.shape, dtype=k.dtype, device=dev), dev, stream)
+    for x, like in ((q, q), (q_out, q), (k, k), (k_out, k)):
+        if like is not None:
+            _require(x.dim() == 3 and x.shape == like.shape and x.shape[0] == q.shape[0] and x.shape[2] == RSWA_DIM
+                     and x.dtype == torch.float32 and x.device == dev and x.stride(2) == 1
+                     and (x.stride(1) == RSWA_DIM or x.shape[1] == 1),
+                     "q, k and their outputs are fp32 [T, heads, 128] on one GPU with contiguous heads")
+    T, hq = q.shape[0], q.shape[1]
+    hk = 0 if k is None else k.shape[1]
+    ld = [0 if x is None else (x.stride(0) if T > 1 else x.shape[1] * RSWA_DIM) for x in (q, k, q_out, k_out)]
+    flags = (QK_NORM if norm else 0) | (ROPE_INTERLEAVED if interleaved else 0)
+    _call(lib().focr_qk_norm_rope, dev, stream, _ptr(q), ld[0], hq, _ptr(k), ld[1], hk, _ptr(pos), T, _ptr(gamma_q),
+          _ptr(gamma_k), float(eps), float(theta), int(rot_dim), flags, _ptr(q_out), ld[2], _ptr(k_out), ld[3])
+    return q_out, k_out
+
+
+class KVCache(typing.NamedTuple):
+    """A quantised key/value cache: codes int8 [B, heads, cap, 128] or uint8 [B, heads, cap, 64] (two nibbles a byte)
+    and scales fp32 [B, heads, cap].  The calls below take any tuple of these four."""
+    k: "torch.Tensor"
+    k_scale: "torch.Tensor"
+    v: "torch.Tensor"
+    v_scale: "torch.Tensor"
+
+
+def new_kv_cache(B: int, heads: int, cap: int, wtype: int = W_INT8, device="cuda") -> KVCache:
+    """A zero-filled cache of int8 or int4 rows."""
+    import torch
+    _require(wtype in (W_INT8, W_INT4), "a cache holds int8 or int4 rows")
+    shape = (B, heads, cap, RSWA_DIM if wtype == W_INT8 else RSWA_DIM // 2)
+    dt = torch.int8 if wtype == W_INT8 else torch.uint8
+    k, v = (torch.zeros(shape, dtype=dt, device=device) for _ in range(2))
+    return KVCache(k, torch.zeros(shape[:3], device=device), v, torch.zeros(shape[:3], device=device))
+
+
+def _kv_desc(cache, dev, name: str = "cache") -> KVCacheDesc:
+    import torch
+    k, ks, v, vs = cache
+    int8 = k.dtype == torch.int8
+    _require(k.dim() == 4 and k.shape[3] == (RSWA_DIM if int8 else RSWA_DIM // 2) and v.shape == k.shape
+             and ks.shape == k.shape[:3] and vs.shape == k.shape[:3],
+             f"{name}: codes [B, heads, cap, 128] int8 or [B, heads, cap, 64] uint8 and scales [B, heads, cap]")
+    _same_device(dev, torch.int8 if int8 else torch.uint8, k=k, v=v)
+    _same_device(dev, torch.float32, k_scale=ks, v_scale=vs)
+    B, heads, cap, _ = k.shape
+    return KVCacheDesc(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), W_INT8 if int8 else W_INT4, B, heads, cap)
+
+
+def focr_kv_write(cache, k, v, count, start, row0=None, index=None, n_max: int | None = None, wrap: bool = False,
+                  stream=None):
+    """Quantise rows of k, v [rows, heads, 128] (rows may be strided) into the cache: sequence b's i-th token, source row
+    (row0[b] or b * n_max) + (index[b, i] or i), goes to slot start[b] + i (mod cap with wrap=True).  n_max: the most
+    tokens of a sequence (default: the columns of index, else rows // B)."""
+    import torch
+    dev = k.device
+    _require(k.is_cuda, "k must be on a GPU")
+    desc = _kv_desc(cache, dev)
+    B, heads = desc.B, desc.heads
+    for x in (k, v):
+        _require(x.dim() == 3 and x.shape == k.shape and x.shape[1:] == (heads, RSWA_DIM) and x.dtype == torch.float32
+                 and x.device == dev and x.stride(2) == 1 and (x.stride(1) == RSWA_DIM or heads == 1),
+                 "k and v are fp32 [rows, heads, 128] on the cache's GPU with contiguous heads")
+    if n_max is None:
+        n_max = index.shape[1] if index is not None else max(1, k.shape[0] // B)
+    _same_device(dev, torch.int32, count=count, start=start, row0=row0, index=index)
+    _require(all(t is None or t.shape == (B,) for t in (count, start, row0)) and
+             (index is None or index.shape == (B, n_max)), "count, start and row0 are [B], index is [B, n_max]")
+    ld = [x.stride(0) if x.shape[0] > 1 else heads * RSWA_DIM for x in (k, v)]
+    _call(lib().focr_kv_write, dev, stream, ctypes.byref(desc), _ptr(k), ld[0], _ptr(v), ld[1], k.shape[0], _ptr(row0),
+          _ptr(count), _ptr(index), int(n_max), _ptr(start), KV_WRAP if wrap else 0)
+    return cache
+
+
+def focr_kv_read(cache, length, k_out=None, v_out=None, stream=None):
+    """(k_out, v_out) fp32 [B, heads, cap, 128]: the values of rows < length[b]; other rows keep what the outputs held
+    (zero where they are made here)."""
+    import torch
+    dev = cache[0].device
+    _require(cache[0].is_cuda, "the cache must be on a GPU")
+    desc = _kv_desc(cache, dev)
+    shape = (desc.B, desc.heads, desc.cap, RSWA_DIM)
+    k_out, v_out = (_new(lambda: torch.zeros(shape, device=dev), dev, stream) if o is None else o for o in (k_out, v_out))
+    _require(k_out.shape == shape and v_out.shape == shape and length.shape == (desc.B,),
+             "outputs are [B, heads, cap, 128], length is [B]")
+    _same_device(dev, torch.float32, k_out=k_out, v_out=v_out)
+    _same_device(dev, torch.int32, length=length)
+    _call(lib().focr_kv_read, dev, stream, ctypes.byref(desc), _ptr(length), _ptr(k_out), _ptr(v_out))
+    return k_out, v_out
+
+
+def focr_rswa_tree(q, k_new, v_new, ref, ref_len, ring, n_gen, parent=None, n_nodes=None, out=None, stream=None):
+    """out [B, N, heads_q, 128]: R-SWA attention of N drafted nodes per sequence (N = 1: one token) over the quantised
+    caches `ref` and `ring`; parent [B, N] (None: a chain), n_nodes [B] (None: N each).  Rows of nodes >= n_nodes keep
+    what `out` held (zero where it is made here)."""
+    import torch
+    dev = q.device
+    _require(q.is_cuda and q.dim() == 4, "q must be [B, N, heads_q, 128] on a GPU")
+    dref, dring = _kv_desc(ref, dev, "ref"), _kv_desc(ring, dev, "ring")
+    B, N, hq, _ = q.shape
+    if out is None:
+        out = _new(lambda: torch.zeros(q.shape, device=dev), dev, stream)
+    _require(q.shape[3] == RSWA_DIM and k_new.shape == (B, N, dref.heads, RSWA_DIM) and v_new.shape == k_new.shape
+             and out.shape == q.shape, "q, out [B, N, heads_q, 128] and k_new, v_new [B, N, heads, 128] are needed")
+    _same_device(dev, torch.float32, q=q, k_new=k_new, v_new=v_new, out=out)
+    _same_device(dev, torch.int32, ref_len=ref_len, n_gen=n_gen, parent=parent, n_nodes=n_nodes)
+    _require(ref_len.shape == (B,) and n_gen.shape == (B,) and (n_nodes is None or n_nodes.shape == (B,))
+             and (parent is None or parent.shape == (B, N)), "ref_len, n_gen, n_nodes are [B], parent is [B, N]")
+    _call(lib().focr_rswa_tree, dev, stream, _ptr(q), _ptr(k_new), _ptr(v_new), B, N, hq, ctypes.byref(dref),
+          _ptr(ref_len), ctypes.byref(dring), _ptr(n_gen), _ptr(parent), _ptr(n_nodes), _ptr(out))
+    return out
+
+
+def focr_token_probs(logits, temperature: float = 1.0, out=None, stream=None):
+    """softmax(logits / temperature) over the last dimension of fp32 logits [..., V]; out may be logits."""
+    import torch
+    dev = logits.device
+    _require(logits.is_cuda and logits.dim() >= 1, "logits must be on a GPU")
+    if out is None:
+        out = _new(lambda: torch.empty(logits.shape, device=dev), dev, stream)
+    _require(out.shape == logits.shape, "out must have the shape of logits")
+    _same_device(dev, torch.float32, logits=logits, out=out)
+    V = logits.shape[-1]
+    _call(lib().focr_token_probs, dev, stream, _ptr(logits), logits.numel() // max(1, V), V, float(temperature), _ptr(out))
+    return out
+
+
+def focr_spec_verify(target_probs, draft_probs, tokens, parent, n_nodes, u, n_accept=None, path=None, next_token=None,
+                     stream=None):
+    """Verify drafted trees: target_probs [B, N + 1, V], draft_probs [B, N, V] or None (chosen drafts), tokens [B, N],
+    parent [B, N] (None: a chain), n_nodes [B] (None: N each), u [B, N + 1].
+    Returns (n_accept [B], path [B, N], next_token [B]), int32."""
+    import torch
+    dev = target_probs.device
+    _require(target_probs.is_cuda and target_probs.dim() == 3, "target_probs must be [B, N + 1, V] on a GPU")
+    B, N, V = target_probs.shape[0], target_probs.shape[1] - 1, target_probs.shape[2]
+    n_accept, path, next_token = (
+        _new(lambda s=s: torch.empty(s, dtype=torch.int32, device=dev), dev, stream) if o is None else o
+        for o, s in ((n_accept, (B,)), (path, (B, N)), (next_token, (B,))))
+    _require(tokens.shape == (B, N) and u.shape == (B, N + 1) and (draft_probs is None or draft_probs.shape == (B, N, V))
+             and (parent is None or parent.shape == (B, N)) and (n_nodes is None or n_nodes.shape == (B,))
+             and n_accept.shape == (B,) and path.shape == (B, N) and next_token.shape == (B,),
+             "tokens, parent, path are [B, N], u is [B, N + 1], draft_probs is [B, N, V], n_nodes, n_accept, next_token are [B]")
+    _same_device(dev, torch.float32, target_probs=target_probs, draft_probs=draft_probs, u=u)
+    _same_device(dev, torch.int32, tokens=tokens, parent=parent, n_nodes=n_nodes, n_accept=n_accept, path=path,
+                 next_token=next_token)
+    _call(lib().focr_spec_verify, dev, stream, _ptr(target_probs), _ptr(draft_probs), V, _ptr(tokens), _ptr(parent),
+          _ptr(n_nodes), _ptr(u), B, N, _ptr(n_accept), _ptr(path), _ptr(next_token))
+    return n_accept, path, next_token
 
 
 def focr_rmsnorm(x, gamma=None, eps: float = 1e-6, out=None, stream=None):
