@@ -10,145 +10,568 @@
 //       out = sum_j softmax_j(q . k_j / sqrt(128)) v_j,   k_j = ks_j * kc_j,  v_j = vs_j * vc_j (codes and scales).
 //   Query head x reads kv head x / (heads_q / heads_kv).  In terms of a slot's age a = (n - 1 - slot) mod 128 the
 //   window is a < min(n, 127 - d), which needs no sum that could overflow.
+//
+// Both products run on the integer tensor cores (mma.sync m16n8k32, exact s32 sums) with the cache's codes as they
+// lie in memory: nothing is dequantised.  A "column" is one query head of one node.
+//   scores    A query row is written as three 8-bit digits of a fixed-point number, q = (max|q| / 8323072) * (65536 d2
+//             + 256 d1 + d0), d2 signed, so it is off by half a step of 2^-23 max|q|.  Three products of the digits
+//             with the key codes give the exact integer dot; the key's scale, the query's step and log2(e) / sqrt(128)
+//             follow in fp32.
+//   softmax   online over blocks of 64 keys, base 2, per warp.
+//   values    out needs sum_j e_j vs_j vc_j.  The weights of a block, relative to the block's largest score and
+//             largest value scale, are written as three unsigned digits (step 2^-24); the three integer sums over the
+//             64 keys are exact, join in fp32 and are added to the fp32 accumulator with the block's factor.
+//   No sum can wrap or leave a float's exact integers: |sum| <= 128 * 128 * 255 < 2^22, so accumulators start at the
+//   bit pattern of 1.5 * 2^23 and are read back as floats by one subtraction.
+// Drafted keys and values stay fp32 and are few: a warp takes a column and walks its line on the CUDA cores.
+//
+// Work split: a cluster of S CTAs (four warps each) has one kv head of one sequence and up to 16 columns; its warps
+// take the 64-key blocks in turn (reference rows, then the ring), each with its own copies in flight (cp.async into
+// its part of shared memory: the next block's K loads while P V runs, its V while Q K runs).  Warps join in shared
+// memory, CTAs through distributed shared memory.  Bound by memory: 264 B (int8) or 136 B (int4) a key and head.
 #include <math.h>
 
 #include "abi_util.h"
 #include "common.cuh"
 #include "kv_cache.h"
+#include "launch_state.h"
 
 namespace focr {
 namespace {
 
 constexpr int RD = FOCR_RSWA_DIM, RW = FOCR_RSWA_RING;
 constexpr int TREE_MAX = FOCR_TREE_NODES_MAX;
+constexpr int COLS = 16;                        // columns of a CTA: the rows of one MMA tile
+constexpr int BLK = 64;                         // keys of a block
+constexpr int WARPS = 4, PT = 32 * WARPS;
+constexpr int PAD = RD + 8;                     // floats per row of a warp's partial output: no bank conflicts
+constexpr float LOG2E = 1.4426950408889634f;
 constexpr float SCALE = 0.08838834764831845f;   // 1 / sqrt(128)
+constexpr float Q_TOP = 8323072.f;              // 127 * 2^16: the largest fixed-point query value
+constexpr float P_TOP = 16711680.f;             // 255 * 2^16: the largest fixed-point weight
+constexpr float MAGIC = 12582912.f;             // 1.5 * 2^23
+constexpr int MAGIC_BITS = 0x4B400000;
+constexpr float NONE = -1e30f;                  // running maximum of a column that has seen no key
+constexpr float TINY = 1e-30f;                  // magnitudes below this share its step
 
 struct TreeParams {
     const float *q, *k_new, *v_new;
     KvView ref, ring;
     const int32_t *ref_len, *n_gen, *parent, *n_nodes;
     float* out;
-    int N, hq, hk, G;
+    int N, hq, hk, G, S, groups;   // S: CTAs of a cluster; groups: column groups of 16 per kv head
 };
 
-// 16 codes of a row, from dim 16 * sub, as floats
-__device__ __forceinline__ void load16(const uint8_t* codes, size_t row, int type, int sub, float (&x)[16]) {
-    if (type == FOCR_W_INT8) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(codes + row * RD) + sub);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = (float)(int8_t)(u[j / 4] >> 8 * (j % 4));
-    } else {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes + row * (RD / 2)) + sub);
-        const uint32_t u[2] = {w.x, w.y};
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = (float)((int)(u[j / 8] << (28 - 4 * (j % 8))) >> 28);
-    }
+template <bool INT4>
+struct Stage {   // a warp's part of shared memory: one block of keys; later its partial output
+    static constexpr int ROW = INT4 ? RD / 2 : RD;
+    static constexpr int V = BLK * ROW, KS = 2 * BLK * ROW, VS = KS + 4 * BLK, LOADS = VS + 4 * BLK;
+    static constexpr int BYTES = LOADS > COLS * PAD * 4 ? LOADS : COLS * PAD * 4;
+};
+
+struct Shared {
+    uint4 qf[4 * 3][32];               // query digits as A fragments: [k-step * 3 + digit][lane]
+    float part[COLS][RD];              // the drafted keys' part, then the CTA's
+    float part_m[COLS], part_l[COLS];
+    float warp_m[WARPS][COLS], warp_l[WARPS][COLS];
+    float step[COLS];                  // a score in units of log2 is (integer dot) * key scale * step
+    int ages[COLS];                    // ring slots younger than this are seen (0 for a column without a node)
+    unsigned long long line[TREE_MAX];
+    int par[TREE_MAX];
+    int bad;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// d += a (16 x 32) * b (32 x 8); A_S8: a is signed and b too (query top digit x codes); else a is unsigned digits
+template <bool A_S8>
+__device__ __forceinline__ void mma(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (A_S8)
+        asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 65536 d2 + 256 d1 + d0 of three accumulators that started at MAGIC_BITS
+__device__ __forceinline__ float join(int d2, int d1, int d0) {
+    const float f2 = __int_as_float(d2) - MAGIC, f1 = __int_as_float(d1) - MAGIC, f0 = __int_as_float(d0) - MAGIC;
+    return fmaf(f2, 65536.f, fmaf(f1, 256.f, f0));
+}
+// bytes of four words, transposed: o[i] = byte i of a, b, c, d
+__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&o)[4]) {
+    const uint32_t t0 = __byte_perm(a, b, 0x5140), t1 = __byte_perm(c, d, 0x5140);
+    const uint32_t t2 = __byte_perm(a, b, 0x7362), t3 = __byte_perm(c, d, 0x7362);
+    o[0] = __byte_perm(t0, t1, 0x5410), o[1] = __byte_perm(t0, t1, 0x7632);
+    o[2] = __byte_perm(t2, t3, 0x5410), o[3] = __byte_perm(t2, t3, 0x7632);
 }
 
-constexpr int PT = 128, GROUPS = PT / 8;
+// Shared-memory offset of 16-byte chunk j of row r; the swizzles spread the chunks that eight lanes read together
+// (K: rows 2i and 2i + 1; V: rows 0, 2, 4, 6) over all banks.
+template <bool INT4>
+__device__ __forceinline__ int k_off(int r, int j) {
+    return INT4 ? r * 64 + j * 16 : r * 128 + ((j ^ ((r & 1) << 2)) << 4);
+}
+template <bool INT4>
+__device__ __forceinline__ int v_off(int r, int j) {
+    const int x = ((r >> 1) & 3) << 1;
+    return INT4 ? (r >> 1) * 128 + ((((r & 1) << 2 | j) ^ x) << 4) : r * 128 + ((j ^ x) << 4);
+}
 
-__global__ void __launch_bounds__(PT) rswa_tree_kernel(const __grid_constant__ TreeParams p) {
-    __shared__ float sm_m[GROUPS], sm_l[GROUPS];
-    __shared__ __align__(16) float sm_acc[GROUPS][RD];
-    __shared__ int sm_par[TREE_MAX];
-    __shared__ int sm_bad;
-    const int b = blockIdx.x / p.hk, h = blockIdx.x % p.hk, node = blockIdx.y / p.G, x = h * p.G + blockIdx.y % p.G;
-    const int tid = threadIdx.x, g = tid >> 3, sub = tid & 7;
+struct Block {   // where a block's rows are
+    const uint8_t *k, *v;
+    const float *ks, *vs;
+    int rows;        // rows that hold a key; later ones are read from the last such row and masked
+    int ring_slot;   // first ring slot, or -1 for reference rows
+};
+
+template <bool INT4>
+__device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* src, int rows, bool is_v, int lane) {
+    constexpr int CH = INT4 ? 4 : 8, STEP = 32 / CH;
+    const int j = lane % CH;
+#pragma unroll
+    for (int i = 0; i < BLK / STEP; ++i) {
+        const int r = lane / CH + STEP * i;
+        cp16(dst + (is_v ? v_off<INT4>(r, j) : k_off<INT4>(r, j)), src + (size_t)min(r, rows - 1) * (CH * 16) + j * 16);
+    }
+}
+__device__ __forceinline__ void load_scales(uint32_t dst, const float* src, int rows, int lane) {
+    cp4(dst + 4 * lane, src + min(lane, rows - 1));
+    cp4(dst + 4 * (lane + 32), src + min(lane + 32, rows - 1));
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+
+// W16: more than eight columns, so both row halves of the MMA tiles are used.
+template <bool INT4, bool W16>
+__global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant__ TreeParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    using St = Stage<INT4>;
+    Shared& sh = *reinterpret_cast<Shared*>(smem + WARPS * St::BYTES);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, c = lane & 3;
+    const int rank = p.S > 1 ? (int)cluster_rank() : 0;
+    const int unit = blockIdx.x / p.S, group = unit % p.groups, pair = unit / p.groups, b = pair / p.hk, h = pair % p.hk;
+    const int col0 = group * COLS, cols = min(COLS, p.N * p.G - col0);
+    uint8_t* stage = smem + warp * St::BYTES;
+    const uint32_t st = smem_u32(stage);
+
     pdl_wait();
     const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b), L = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
-    if (tid == 0) sm_bad = R < 0 || R > p.ref.cap || n < 0 || L < 0 || L > p.N;
+    if (tid == 0) sh.bad = R < 0 || R > p.ref.cap || n < 0 || L < 0 || L > p.N;
     __syncthreads();
     if (tid < min(L, p.N)) {
         const int par = p.parent ? __ldg(p.parent + (size_t)b * p.N + tid) : tid - 1;
-        sm_par[tid] = par;
-        if (par < -1 || par >= tid) sm_bad = 1;
+        sh.par[tid] = par;
+        if (par < -1 || par >= tid) sh.bad = 1;
     }
     __syncthreads();
-    float* out = p.out + (((size_t)b * p.N + node) * p.hq + x) * RD;
-    if (sm_bad) {
-        if (node < (L < 0 || L > p.N ? p.N : L)) out[tid] = __int_as_float(0x7fc00000);   // NaN
+    if (sh.bad) {   // the whole cluster sees the same: nobody waits for it
+        const int live = L < 0 || L > p.N ? p.N : L;
+        for (int col = rank; col < cols; col += p.S) {
+            const int node = (col0 + col) / p.G;
+            if (node < live)
+                p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = __int_as_float(0x7fc00000);
+        }
         return;
     }
-    if (node >= L) return;
-    unsigned long long line = 0;   // the node and its ancestors
-    int depth = -1;
-    for (int j = node; j >= 0; j = sm_par[j]) {
-        line |= 1ull << j;
-        ++depth;
+    if (col0 / p.G >= L) return;   // no live node in this group, in any CTA of the cluster
+
+    // the warp's blocks: rank * WARPS + warp, then every S * WARPS-th
+    const int nref = (R + BLK - 1) / BLK, nring = (min(n, RW) + BLK - 1) / BLK, nblk = nref + nring;
+    const size_t ref0 = ((size_t)b * p.hk + h) * p.ref.cap, ring0 = ((size_t)b * p.hk + h) * RW;
+    auto block_at = [&](int i) {
+        Block x;
+        const bool ring = i >= nref;
+        const KvView& v = ring ? p.ring : p.ref;
+        const int first = (ring ? i - nref : i) * BLK;
+        const size_t row = (ring ? ring0 : ref0) + first;
+        x.k = v.k + row * St::ROW, x.v = v.v + row * St::ROW, x.ks = v.ks + row, x.vs = v.vs + row;
+        x.rows = min(BLK, (ring ? min(n, RW) : R) - first);
+        x.ring_slot = ring ? first : -1;
+        return x;
+    };
+    int blk = rank * WARPS + warp;
+    Block cur{};
+    if (blk < nblk) {
+        cur = block_at(blk);
+        load_codes<INT4>(st, cur.k, cur.rows, false, lane);
+        load_scales(st + St::KS, cur.ks, cur.rows, lane);
+        load_scales(st + St::VS, cur.vs, cur.rows, lane);
     }
-    float qv[16];
-    {
-        const float4* q4 = reinterpret_cast<const float4*>(p.q + (((size_t)b * p.N + node) * p.hq + x) * RD + 16 * sub);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 t = __ldg(q4 + i);
-            qv[4 * i] = t.x, qv[4 * i + 1] = t.y, qv[4 * i + 2] = t.z, qv[4 * i + 3] = t.w;
-        }
+    cp_commit();
+    if (blk < nblk) load_codes<INT4>(st + St::V, cur.v, cur.rows, true, lane);
+    cp_commit();
+
+    // ---- lines of the tree
+    if (tid < L) {
+        unsigned long long line = 0;
+        for (int j = tid; j >= 0; j = sh.par[j]) line |= 1ull << j;
+        sh.line[tid] = line;
     }
-    const int ages = min(n, RW - 1 - depth);
-    const size_t row0 = ((size_t)b * p.hk + h) * p.ref.cap, ring0 = ((size_t)b * p.hk + h) * RW;
-    float m = -INFINITY, l = 0.f, acc[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    const int nk = R + RW + L;
-    for (int jb = 0; jb < nk; jb += GROUPS) {
-        const int j = jb + g;
-        float kk[16], vv[16], ks = 0.f, vs = 0.f;
-        bool live = j < nk;
-        if (live && j < R) {
-            load16(p.ref.k, row0 + j, p.ref.type, sub, kk);
-            load16(p.ref.v, row0 + j, p.ref.type, sub, vv);
-            ks = __ldg(p.ref.ks + row0 + j), vs = __ldg(p.ref.vs + row0 + j);
-        } else if (live && j < R + RW) {
-            const int slot = j - R;
-            live = (unsigned)(n - 1 - slot) % RW < (unsigned)ages && n > 0;
-            if (live) {
-                load16(p.ring.k, ring0 + slot, p.ring.type, sub, kk);
-                load16(p.ring.v, ring0 + slot, p.ring.type, sub, vv);
-                ks = __ldg(p.ring.ks + ring0 + slot), vs = __ldg(p.ring.vs + ring0 + slot);
-            }
-        } else if (live) {
-            const int a = j - R - RW;
-            live = line >> a & 1;
-            if (live) {
-                const size_t r = (((size_t)b * p.N + a) * p.hk + h) * RD + 16 * sub;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) kk[i] = __ldg(p.k_new + r + i), vv[i] = __ldg(p.v_new + r + i);
-                ks = vs = 1.f;
-            }
-        }
-        float dot = 0.f;
-        if (live) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dot = fmaf(qv[i], kk[i], dot);
-        }
-        dot += __shfl_xor_sync(0xffffffffu, dot, 1);
-        dot += __shfl_xor_sync(0xffffffffu, dot, 2);
-        dot += __shfl_xor_sync(0xffffffffu, dot, 4);
-        if (!live) continue;
-        const float sc = dot * ks * SCALE, mn = fmaxf(m, sc);
-        const float corr = expf(m - mn), w = expf(sc - mn);
-        l = l * corr + w;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = acc[i] * corr + w * vs * vv[i];
-        m = mn;
-    }
-    if (sub == 0) sm_m[g] = m, sm_l[g] = l;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) sm_acc[g][16 * sub + i] = acc[i];
     __syncthreads();
-    float M = -INFINITY;
+    // ---- query digits and per-column constants; the drafted keys' part
+    for (int col = warp; col < COLS; col += WARPS) {
+        const int node = (col0 + col) / p.G, x = h * p.G + (col0 + col) % p.G;
+        const bool live = col < cols && node < L;
+        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live) q = __ldg(reinterpret_cast<const float4*>(p.q + (((size_t)b * p.N + node) * p.hq + x) * RD) + lane);
+        float a = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w)));
 #pragma unroll
-    for (int k = 0; k < GROUPS; ++k) M = fmaxf(M, sm_m[k]);
-    float Ls = 0.f, A = 0.f;
+        for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        a = fmaxf(a, TINY);
+        const float inv = Q_TOP / a;
+        const int f[4] = {__float2int_rn(q.x * inv), __float2int_rn(q.y * inv), __float2int_rn(q.z * inv), __float2int_rn(q.w * inv)};
+        const int tl = (col & 7) * 4, hi = col >> 3;
 #pragma unroll
-    for (int k = 0; k < GROUPS; ++k) {
-        const float e = expf(sm_m[k] - M);   // 0 for an empty group; the node itself is in one of them
-        Ls += sm_l[k] * e;
-        A += sm_acc[k][tid] * e;
+        for (int d = 0; d < 3; ++d) {
+            const uint32_t v0 = (f[0] >> 8 * d) & 255, v1 = (f[1] >> 8 * d) & 255, v2 = (f[2] >> 8 * d) & 255, v3 = (f[3] >> 8 * d) & 255;
+            if (INT4) {   // dims 32 c + 8 s + 2 i in the first word of a k-step, + 1 in the second
+                const int s = (lane >> 1) & 3, cc = lane >> 3;
+                uint16_t* w = reinterpret_cast<uint16_t*>(&sh.qf[s * 3 + d][tl + cc]);
+                w[2 * hi + (lane & 1)] = (uint16_t)(v0 | v2 << 8);
+                w[2 * (2 + hi) + (lane & 1)] = (uint16_t)(v1 | v3 << 8);
+            } else {      // dims 64 (s / 2) + 16 c + 8 (s % 2) + i, + 4 in the second
+                const int s = 2 * (lane >> 4) + ((lane >> 1) & 1), cc = (lane >> 2) & 3;
+                reinterpret_cast<uint32_t*>(&sh.qf[s * 3 + d][tl + cc])[2 * (lane & 1) + hi] = v0 | v1 << 8 | v2 << 16 | v3 << 24;
+            }
+        }
+        if (lane == 0) {
+            sh.step[col] = a / Q_TOP * (SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
+            sh.ages[col] = live ? min(n, RW - __popcll(sh.line[node])) : 0;
+        }
+        // a CTA of the cluster takes every S-th column's line
+        float m = NONE, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live && col % p.S == rank) {
+            const float k2 = SCALE * LOG2E;
+            const float4 qs = make_float4(q.x * k2, q.y * k2, q.z * k2, q.w * k2);
+            for (unsigned long long line = sh.line[node]; line; line &= line - 1) {
+                const size_t r = (((size_t)b * p.N + __ffsll(line) - 1) * p.hk + h) * (RD / 4) + lane;
+                const float4 kk = __ldg(reinterpret_cast<const float4*>(p.k_new) + r);
+                const float4 vv = __ldg(reinterpret_cast<const float4*>(p.v_new) + r);
+                float s = qs.x * kk.x + qs.y * kk.y + qs.z * kk.z + qs.w * kk.w;
+#pragma unroll
+                for (int i = 16; i >= 1; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+                const float mn = fmaxf(m, s), al = ex2(m - mn), w = ex2(s - mn);
+                l = l * al + w;
+                o.x = o.x * al + w * vv.x, o.y = o.y * al + w * vv.y, o.z = o.z * al + w * vv.z, o.w = o.w * al + w * vv.w;
+                m = mn;
+            }
+        }
+        reinterpret_cast<float4*>(sh.part[col])[lane] = o;
+        if (lane == 0) sh.part_m[col] = m, sh.part_l[col] = l;
     }
-    out[tid] = A / Ls;
+    __syncthreads();
+
+    // ---- the blocks.  Lane (gr, c) has columns gr and gr + 8 and, of each 8 keys, keys 2 c and 2 c + 1.
+    float O[16][W16 ? 4 : 2];
+#pragma unroll
+    for (int t = 0; t < 16; ++t)
+#pragma unroll
+        for (int j = 0; j < (W16 ? 4 : 2); ++j) O[t][j] = 0.f;
+    constexpr int HALVES = W16 ? 2 : 1;
+    float run_m[HALVES], run_l[HALVES], step[HALVES];
+    int ages[HALVES];
+#pragma unroll
+    for (int e = 0; e < HALVES; ++e) {
+        run_m[e] = NONE, run_l[e] = 0.f;
+        step[e] = sh.step[gr + 8 * e], ages[e] = sh.ages[gr + 8 * e];
+    }
+    for (; blk < nblk; blk += p.S * WARPS) {
+        cp_wait1();
+        __syncwarp();
+        // scores, without the column's step: T[j][..] for keys 8 j + 2 c, + 1
+        float T[8][W16 ? 4 : 2], vs[8][2];
+        const bool whole = cur.rows == BLK && cur.ring_slot < 0;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            int acc[4][3][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int d = 0; d < 3; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[j][d][i] = MAGIC_BITS;
+            uint32_t kb[4][8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 32 * half + 8 * j + gr;
+                if (INT4) {
+                    const uint4 w = lds128(stage + k_off<true>(r, c));
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kb[j][2 * i] = (u[i] << 4) & 0xF0F0F0F0u, kb[j][2 * i + 1] = u[i] & 0xF0F0F0F0u;
+                } else {
+                    const uint4 w0 = lds128(stage + k_off<false>(r, c)), w1 = lds128(stage + k_off<false>(r, c + 4));
+                    kb[j][0] = w0.x, kb[j][1] = w0.y, kb[j][2] = w0.z, kb[j][3] = w0.w;
+                    kb[j][4] = w1.x, kb[j][5] = w1.y, kb[j][6] = w1.z, kb[j][7] = w1.w;
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int d = 0; d < 3; ++d) {
+                    const uint4 q4 = lds128(&sh.qf[s * 3 + d][lane]);
+                    const uint32_t a[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (d == 2)
+                            mma<true>(acc[j][d], a, kb[j][2 * s], kb[j][2 * s + 1]);
+                        else
+                            mma<false>(acc[j][d], a, kb[j][2 * s], kb[j][2 * s + 1]);
+                    }
+                }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = 32 * half + 8 * j + 2 * c, jj = 4 * half + j;
+                float2 ks = *reinterpret_cast<const float2*>(stage + St::KS + 4 * key);
+                float2 v2 = *reinterpret_cast<const float2*>(stage + St::VS + 4 * key);
+                vs[jj][0] = v2.x, vs[jj][1] = v2.y;
+#pragma unroll
+                for (int i = 0; i < (W16 ? 4 : 2); ++i)
+                    T[jj][i] = join(acc[j][2][i], acc[j][1][i], acc[j][0][i]) * (i & 1 ? ks.y : ks.x);
+                if (!whole) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const bool in = key + i < cur.rows;
+                        if (!in) vs[jj][i] = 0.f;
+#pragma unroll
+                        for (int e = 0; e < HALVES; ++e) {
+                            const bool seen = in && (cur.ring_slot < 0 || ((n - 1 - cur.ring_slot - key - i) & (RW - 1)) < ages[e]);
+                            if (!seen) T[jj][2 * e + i] = -INFINITY;
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        // the next block's K and scales take this block's place
+        const int next = blk + p.S * WARPS;
+        Block nxt{};
+        if (next < nblk) {
+            nxt = block_at(next);
+            load_codes<INT4>(st, nxt.k, nxt.rows, false, lane);
+            load_scales(st + St::KS, nxt.ks, nxt.rows, lane);
+            load_scales(st + St::VS, nxt.vs, nxt.rows, lane);
+        }
+        cp_commit();
+        // softmax of the block: weights relative to its largest score and value scale, as digits
+        float vmax = TINY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) vmax = fmaxf(vmax, fmaxf(vs[j][0], vs[j][1]));
+        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
+        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+        const float vinv = P_TOP / vmax;
+        float alpha[HALVES], gain[HALVES];
+        uint32_t pd[2][3][4];   // digits as A fragments: [32 keys][digit]
+#pragma unroll
+        for (int j = 0; j < 8; ++j) vs[j][0] *= vinv, vs[j][1] *= vinv;
+#pragma unroll
+        for (int e = 0; e < HALVES; ++e) {
+            float tm = T[0][2 * e];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) tm = fmaxf(tm, fmaxf(T[j][2 * e], T[j][2 * e + 1]));
+            tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
+            tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
+            const bool any = tm != -INFINITY;
+            const float mb = any ? tm * step[e] : 0.f;
+            float sum = 0.f;
+            uint32_t u[8][2];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float w = ex2(fminf(fmaf(T[j][2 * e + i], step[e], -mb), 0.f));
+                    sum += w;
+                    u[j][i] = __float2uint_rn(w * vs[j][i]);
+                }
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int j = 4 * kk + 2 * g;
+                    const uint32_t t0 = __byte_perm(u[j][0], u[j][1], 0x5140), t1 = __byte_perm(u[j + 1][0], u[j + 1][1], 0x5140);
+                    const uint32_t t2 = __byte_perm(u[j][0], u[j][1], 0x0062), t3 = __byte_perm(u[j + 1][0], u[j + 1][1], 0x0062);
+                    // fragment words: (row gr, keys g = 0), (row gr + 8, g = 0), (gr, g = 1), (gr + 8, g = 1)
+                    pd[kk][0][2 * g + e] = __byte_perm(t0, t1, 0x5410);
+                    pd[kk][1][2 * g + e] = __byte_perm(t0, t1, 0x7632);
+                    pd[kk][2][2 * g + e] = __byte_perm(t2, t3, 0x5410);
+                }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            const float mn = any ? fmaxf(run_m[e], mb) : run_m[e];
+            alpha[e] = ex2(run_m[e] - mn);
+            const float beta = any ? ex2(mb - mn) : 0.f;
+            run_l[e] = run_l[e] * alpha[e] + beta * sum;
+            gain[e] = beta * vmax * ((INT4 ? 1.f / 16.f : 1.f) / P_TOP);
+            run_m[e] = mn;
+        }
+        if (!W16) {
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int d = 0; d < 3; ++d) pd[kk][d][1] = pd[kk][d][3] = 0u;
+        }
+        cp_wait1();
+        __syncwarp();
+        // values: dim 16 g + t of tile t, from the bytes of the lane's sixteen keys
+        uint32_t vb[2][16][2];
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int r0 = 32 * kk + 16 * g + 2 * c;
+                if (INT4) {
+                    uint2 w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + (i & 1) + 8 * (i >> 1);
+                        w[i] = *reinterpret_cast<const uint2*>(stage + St::V + v_off<true>(r, gr >> 1) + (gr & 1) * 8);
+                    }
+                    uint32_t o[4];
+                    transpose4(w[0].x, w[1].x, w[2].x, w[3].x, o);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vb[kk][2 * i][g] = (o[i] << 4) & 0xF0F0F0F0u, vb[kk][2 * i + 1][g] = o[i] & 0xF0F0F0F0u;
+                    transpose4(w[0].y, w[1].y, w[2].y, w[3].y, o);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vb[kk][8 + 2 * i][g] = (o[i] << 4) & 0xF0F0F0F0u, vb[kk][8 + 2 * i + 1][g] = o[i] & 0xF0F0F0F0u;
+                } else {
+                    uint4 w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = lds128(stage + St::V + v_off<false>(r0 + (i & 1) + 8 * (i >> 1), gr));
+                    uint32_t o[4];
+                    transpose4(w[0].x, w[1].x, w[2].x, w[3].x, o);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vb[kk][i][g] = o[i];
+                    transpose4(w[0].y, w[1].y, w[2].y, w[3].y, o);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vb[kk][4 + i][g] = o[i];
+                    transpose4(w[0].z, w[1].z, w[2].z, w[3].z, o);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vb[kk][8 + i][g] = o[i];
+                    transpose4(w[0].w, w[1].w, w[2].w, w[3].w, o);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vb[kk][12 + i][g] = o[i];
+                }
+            }
+        __syncwarp();
+        if (next < nblk) load_codes<INT4>(st + St::V, nxt.v, nxt.rows, true, lane);
+        cp_commit();
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            int acc[3][4];
+#pragma unroll
+            for (int d = 0; d < 3; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[d][i] = MAGIC_BITS;
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int d = 0; d < 3; ++d) mma<false>(acc[d], pd[kk][d], vb[kk][t][0], vb[kk][t][1]);
+#pragma unroll
+            for (int i = 0; i < (W16 ? 4 : 2); ++i)
+                O[t][i] = fmaf(O[t][i], alpha[i >> 1], gain[i >> 1] * join(acc[2][i], acc[1][i], acc[0][i]));
+        }
+        cur = nxt;
+    }
+    // ---- join the warps: partial outputs at [column][t * 8 + dim / 16], dim = 16 * (dim / 16) + t
+    cp_wait0();
+    __syncwarp();
+    {
+        float* po = reinterpret_cast<float*>(stage);
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+#pragma unroll
+            for (int e = 0; e < HALVES; ++e)
+                *reinterpret_cast<float2*>(po + (gr + 8 * e) * PAD + t * 8 + 2 * c) = make_float2(O[t][2 * e], O[t][2 * e + 1]);
+        if (c == 0) {
+#pragma unroll
+            for (int e = 0; e < HALVES; ++e) sh.warp_m[warp][gr + 8 * e] = run_m[e], sh.warp_l[warp][gr + 8 * e] = run_l[e];
+        }
+    }
+    __syncthreads();
+    for (int col = 0; col < cols; ++col) {
+        const float pm = sh.part_m[col];
+        float M = pm;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sh.warp_m[w][col]);
+        float f = ex2(pm - M), l = f * sh.part_l[col], o = f * sh.part[col][tid];
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const float g = ex2(sh.warp_m[w][col] - M);
+            l = fmaf(g, sh.warp_l[w][col], l);
+            o = fmaf(g, reinterpret_cast<const float*>(smem + w * St::BYTES)[col * PAD + (tid & 15) * 8 + (tid >> 4)], o);
+        }
+        if (p.S == 1) {
+            const int node = (col0 + col) / p.G;
+            if (node < L) p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = o / l;
+        } else {
+            sh.part[col][tid] = o;
+            __syncthreads();   // everybody has read the column's old maximum and sum
+            if (tid == 0) sh.part_m[col] = M, sh.part_l[col] = l;
+        }
+    }
+    if (p.S == 1) return;
+    // ---- join the CTAs of the cluster: each takes every S-th column
+    cluster_sync();
+    for (int col = rank; col < cols; col += p.S) {
+        const int node = (col0 + col) / p.G;
+        if (node >= L) continue;
+        float M = NONE, l = 0.f, o = 0.f;
+        for (int r = 0; r < p.S; ++r) M = fmaxf(M, ld_cluster(mapa_shared(&sh.part_m[col], r)));
+        for (int r = 0; r < p.S; ++r) {
+            const float f = ex2(ld_cluster(mapa_shared(&sh.part_m[col], r)) - M);
+            l = fmaf(f, ld_cluster(mapa_shared(&sh.part_l[col], r)), l);
+            o = fmaf(f, ld_cluster(mapa_shared(&sh.part[col][tid], r)), o);
+        }
+        p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = o / l;
+    }
+    cluster_sync();   // no CTA leaves while another reads its shared memory
+}
+
+template <bool INT4, bool W16>
+cudaError_t launch_tree(TreeParams& p, int B, cudaStream_t st) {
+    const void* fn = (const void*)rswa_tree_kernel<INT4, W16>;
+    const size_t smem = WARPS * Stage<INT4>::BYTES + sizeof(Shared);
+    cudaError_t e = once_per_device(fn, [&] {
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    });
+    if (e != cudaSuccess) return e;
+    p.groups = (p.N * p.G + COLS - 1) / COLS;
+    // enough CTAs for two per SM several times over, at least one block a warp
+    const int sms = device_sms() > 0 ? device_sms() : 148, units = B * p.hk * p.groups;
+    const int blocks = (p.ref.cap + BLK - 1) / BLK + RW / BLK;
+    p.S = 1;
+    while (p.S < 8 && units * p.S < 8 * sms && p.S * WARPS < blocks) p.S *= 2;
+    void* args[] = {&p};
+    return launch_kernel(fn, dim3((unsigned)(units * p.S)), dim3(PT), smem, p.S, args, st);
 }
 
 }  // namespace
@@ -185,8 +608,9 @@ extern "C" focr_status focr_rswa_tree(const float* q, const float* k_new, const 
         return report_error(FOCR_ERR_INVALID_ARG, "out overlaps an input");
     p.q = q, p.k_new = k_new, p.v_new = v_new, p.ref_len = ref_len, p.n_gen = n_gen, p.parent = parent, p.n_nodes = n_nodes;
     p.out = out, p.N = N, p.hq = heads_q, p.hk = ref->heads, p.G = G;
-    void* args[] = {&p};
-    return report_launch(launch_kernel((const void*)rswa_tree_kernel, dim3(B * p.hk, N * G), dim3(PT), 0, 1, args,
-                                       (cudaStream_t)stream),
-                         "rswa_tree_kernel");
+    const bool wide = N * G > 8, int4 = ref->type == FOCR_W_INT4;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = int4 ? (wide ? launch_tree<true, true>(p, B, st) : launch_tree<true, false>(p, B, st))
+                               : (wide ? launch_tree<false, true>(p, B, st) : launch_tree<false, false>(p, B, st));
+    return report_launch(e, "rswa_tree_kernel");
 }
