@@ -531,7 +531,7 @@ focr_status focr_rswa_tree(const float* q, const float* k_new, const float* v_ne
 /*
  * focr_token_probs -- probs[t] = softmax(logits[t] / temperature), DEVICE fp32 [T][V], fp32 arithmetic.  probs may be
  * logits.  A logit of -inf has probability 0; a row without a finite maximum is NaN.
- * 1 <= T <= FOCR_T_MAX, 1 <= V <= FOCR_V_MAX, temperature > 0.
+ * 1 <= T <= FOCR_T_MAX, 1 <= V <= FOCR_V_MAX, 1e-6 <= temperature <= 1e6.
  */
 focr_status focr_token_probs(const float* logits, int32_t T, int32_t V, float temperature, float* probs, void* stream);
 

@@ -103,7 +103,7 @@ def test_tree_refusals(bad, status, word):
 @pytest.mark.parametrize("args,word", [
     ((None, 1, 8, 1.0, at(1)), "NULL"), ((at(0), 0, 8, 1.0, at(1)), "T="), ((at(0), 1, 0, 1.0, at(1)), "V="),
     ((at(0), 1, (1 << 20) + 1, 1.0, at(1)), "V="), ((at(0), 1, 8, 0.0, at(1)), "temperature"),
-    ((at(0), 1, 8, float("nan"), at(1)), "temperature"), ((at(0), 1, 8, float("inf"), at(1)), "temperature"),
+    ((at(0), 1, 8, 1e-7, at(1)), "temperature"), ((at(0), 1, 8, float("nan"), at(1)), "temperature"), ((at(0), 1, 8, float("inf"), at(1)), "temperature"),
     ((at(0) + 2, 1, 8, 1.0, at(1)), "misaligned"), ((at(0), 1, 8, 1.0, at(0) + 4), "overlap"),
 ])
 def test_probs_refusals(args, word):

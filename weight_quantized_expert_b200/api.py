@@ -427,40 +427,69 @@ def focr_rswa_decode(q, k_new, v_new, k_ref, v_ref, ref_len, k_ring, v_ring, n_g
 # ---------------------------------------------------------------- speculative decode step
 
 QK_NORM, ROPE_INTERLEAVED, KV_WRAP = 1, 2, 1
+_torch = None
 
 
-def _require(ok, msg: str):
+def _tensor_lib():
+    """torch, and the library's handle: bound once (these calls take microseconds)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch, _lib or lib()
+
+
+def _need(ok, msg: str):
     if not ok:
         raise FocrError(1, msg)
 
 
-def _same_device(dev, dtype, **tensors):
-    """Every given tensor (None: absent) is on `dev`, has `dtype` and is contiguous."""
-    for name, t in tensors.items():
-        if t is not None and not (t.device == dev and t.dtype == dtype and t.is_contiguous()):
-            raise FocrError(1, f"{name}: a contiguous {dtype} tensor on {dev} is needed, "
-                               f"got {t.dtype} on {t.device}, strides {t.stride()}")
+def _need_tensor(name, t, dev: int, dtype, shape):
+    """t is a contiguous tensor of this dtype and shape on device `dev`."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise FocrError(1, f"{name}: a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev} is needed, "
+                           f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+    return t.data_ptr()
 
 
-def _call(fn, dev, stream, *args):
-    """fn(*args, stream) with `dev` current; stream None: the current stream of `dev`."""
-    import torch
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, _stream(stream)))
+def _need_rows(name, t, dev: int, shape):
+    """t is fp32 [rows, heads, 128] on device `dev` with contiguous heads; rows may be strided.  (pointer, row stride)"""
+    stride = t.stride()
+    if (t.get_device() != dev or t.dtype is not _torch.float32 or t.shape != shape or shape[2] != RSWA_DIM or stride[2] != 1
+            or (stride[1] != RSWA_DIM and shape[1] > 1)):
+        raise FocrError(1, f"{name}: fp32 {tuple(shape[:2]) + (RSWA_DIM,)} with contiguous heads on cuda:{dev} is needed, "
+                           f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {stride}")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * RSWA_DIM
+
+
+def _device_of(t, what: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise FocrError(1, f"{what} must be on a GPU")
+    return dev
+
+
+def _call(fn, dev: int, stream, *args):
+    """fn(*args, stream) with device `dev` current; stream None: the current stream of `dev`."""
+    st = _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if _torch.cuda.current_device() == dev:
+        status = fn(*args, st)
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)))
+        with _torch.cuda.device(dev):
+            status = fn(*args, st)
+    if status:
+        _check(status)
 
 
-def _new(make, dev, stream):
-    """A tensor made by `make`, in the memory pool of the stream it is going to be written on."""
-    import torch
+def _new(dev: int, stream, shape, dtype=None, zero=False):
+    """A tensor in the memory pool of the stream it is going to be written on."""
+    make = _torch.zeros if zero else _torch.empty
     if stream is None:
-        return make()
+        return make(shape, dtype=dtype or _torch.float32, device=dev)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    with torch.cuda.stream(stream):
-        return make()
+        stream = _torch.cuda.ExternalStream(int(stream), device=dev)
+    with _torch.cuda.stream(stream):
+        return make(shape, dtype=dtype or _torch.float32, device=dev)
 
 
 def focr_qk_norm_rope(q, k, pos, gamma_q=None, gamma_k=None, eps: float = 1e-6, theta: float = 10000.0,
@@ -468,29 +497,29 @@ def focr_qk_norm_rope(q, k, pos, gamma_q=None, gamma_k=None, eps: float = 1e-6, 
                       stream=None):
     """Per-head norms (norm=True) and rotation of q [T, heads_q, 128] and k [T, heads_k, 128] (or None) at pos [T] int32.
     Tokens may be strided (columns of a fused projection).  q_out / k_out may be q / k.  Returns (q_out, k_out)."""
-    import torch
-    dev = q.device
-    _require(q.is_cuda and pos.dtype == torch.int32 and pos.shape == (q.shape[0],), "q on a GPU and pos int32 [T] are needed")
-    _same_device(dev, torch.int32, pos=pos)
-    _same_device(dev, torch.float32, gamma_q=gamma_q, gamma_k=gamma_k)
-    for g in (gamma_q, gamma_k):
-        _require(g is None or g.shape == (RSWA_DIM,), "gamma must be [128]")
+    torch, L = _tensor_lib()
+    dev = _device_of(q, "q")
+    shape = q.shape
+    _need(len(shape) == 3, "q must be [T, heads, 128]")
+    T, hq = shape[0], shape[1]
     if q_out is None:
-        q_out = _new(lambda: torch.empty(q.shape, dtype=q.dtype, device=dev), dev, stream)
-    if k is not None and k_out is None:
-        k_out = _new(lambda: torch.empty(k.shape, dtype=k.dtype, device=dev), dev, stream)
-    for x, like in ((q, q), (q_out, q), (k, k), (k_out, k)):
-        if like is not None:
-            _require(x.dim() == 3 and x.shape == like.shape and x.shape[0] == q.shape[0] and x.shape[2] == RSWA_DIM
-                     and x.dtype == torch.float32 and x.device == dev and x.stride(2) == 1
-                     and (x.stride(1) == RSWA_DIM or x.shape[1] == 1),
-                     "q, k and their outputs are fp32 [T, heads, 128] on one GPU with contiguous heads")
-    T, hq = q.shape[0], q.shape[1]
-    hk = 0 if k is None else k.shape[1]
-    ld = [0 if x is None else (x.stride(0) if T > 1 else x.shape[1] * RSWA_DIM) for x in (q, k, q_out, k_out)]
-    flags = (QK_NORM if norm else 0) | (ROPE_INTERLEAVED if interleaved else 0)
-    _call(lib().focr_qk_norm_rope, dev, stream, _ptr(q), ld[0], hq, _ptr(k), ld[1], hk, _ptr(pos), T, _ptr(gamma_q),
-          _ptr(gamma_k), float(eps), float(theta), int(rot_dim), flags, _ptr(q_out), ld[2], _ptr(k_out), ld[3])
+        q_out = _new(dev, stream, shape)
+    qp, ldq = _need_rows("q", q, dev, shape)
+    qo, ldqo = _need_rows("q_out", q_out, dev, shape)
+    hk = kp = ldk = ko = ldko = 0
+    if k is not None:
+        shape = k.shape
+        _need(len(shape) == 3 and shape[0] == T, "k must be [T, heads, 128]")
+        hk = shape[1]
+        if k_out is None:
+            k_out = _new(dev, stream, shape)
+        kp, ldk = _need_rows("k", k, dev, shape)
+        ko, ldko = _need_rows("k_out", k_out, dev, shape)
+    one = (RSWA_DIM,)
+    _call(L.focr_qk_norm_rope, dev, stream, qp, ldq, hq, kp, ldk, hk, _need_tensor("pos", pos, dev, torch.int32, (T,)), T,
+          None if gamma_q is None else _need_tensor("gamma_q", gamma_q, dev, torch.float32, one),
+          None if gamma_k is None else _need_tensor("gamma_k", gamma_k, dev, torch.float32, one), eps, theta, rot_dim,
+          (QK_NORM if norm else 0) | (ROPE_INTERLEAVED if interleaved else 0), qo, ldqo, ko, ldko)
     return q_out, k_out
 
 
@@ -506,24 +535,23 @@ class KVCache(typing.NamedTuple):
 def new_kv_cache(B: int, heads: int, cap: int, wtype: int = W_INT8, device="cuda") -> KVCache:
     """A zero-filled cache of int8 or int4 rows."""
     import torch
-    _require(wtype in (W_INT8, W_INT4), "a cache holds int8 or int4 rows")
+    _need(wtype in (W_INT8, W_INT4), "a cache holds int8 or int4 rows")
     shape = (B, heads, cap, RSWA_DIM if wtype == W_INT8 else RSWA_DIM // 2)
     dt = torch.int8 if wtype == W_INT8 else torch.uint8
     k, v = (torch.zeros(shape, dtype=dt, device=device) for _ in range(2))
     return KVCache(k, torch.zeros(shape[:3], device=device), v, torch.zeros(shape[:3], device=device))
 
 
-def _kv_desc(cache, dev, name: str = "cache") -> KVCacheDesc:
-    import torch
+def _kv_desc(cache, dev: int, name: str = "cache") -> KVCacheDesc:
     k, ks, v, vs = cache
-    int8 = k.dtype == torch.int8
-    _require(k.dim() == 4 and k.shape[3] == (RSWA_DIM if int8 else RSWA_DIM // 2) and v.shape == k.shape
-             and ks.shape == k.shape[:3] and vs.shape == k.shape[:3],
-             f"{name}: codes [B, heads, cap, 128] int8 or [B, heads, cap, 64] uint8 and scales [B, heads, cap]")
-    _same_device(dev, torch.int8 if int8 else torch.uint8, k=k, v=v)
-    _same_device(dev, torch.float32, k_scale=ks, v_scale=vs)
-    B, heads, cap, _ = k.shape
-    return KVCacheDesc(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), W_INT8 if int8 else W_INT4, B, heads, cap)
+    shape, int8 = k.shape, k.dtype is _torch.int8
+    _need(len(shape) == 4 and shape[3] == (RSWA_DIM if int8 else RSWA_DIM // 2),
+          f"{name}: codes are [B, heads, cap, 128] int8 or [B, heads, cap, 64] uint8")
+    dtype = _torch.int8 if int8 else _torch.uint8
+    B, heads, cap = rows = shape[:3]
+    return KVCacheDesc(_need_tensor(name, k, dev, dtype, shape), _need_tensor(name, ks, dev, _torch.float32, rows),
+                       _need_tensor(name, v, dev, dtype, shape), _need_tensor(name, vs, dev, _torch.float32, rows),
+                       W_INT8 if int8 else W_INT4, B, heads, cap)
 
 
 def focr_kv_write(cache, k, v, count, start, row0=None, index=None, n_max: int | None = None, wrap: bool = False,
@@ -531,40 +559,35 @@ def focr_kv_write(cache, k, v, count, start, row0=None, index=None, n_max: int |
     """Quantise rows of k, v [rows, heads, 128] (rows may be strided) into the cache: sequence b's i-th token, source row
     (row0[b] or b * n_max) + (index[b, i] or i), goes to slot start[b] + i (mod cap with wrap=True).  n_max: the most
     tokens of a sequence (default: the columns of index, else rows // B)."""
-    import torch
-    dev = k.device
-    _require(k.is_cuda, "k must be on a GPU")
+    torch, L = _tensor_lib()
+    dev = _device_of(k, "k")
     desc = _kv_desc(cache, dev)
-    B, heads = desc.B, desc.heads
-    for x in (k, v):
-        _require(x.dim() == 3 and x.shape == k.shape and x.shape[1:] == (heads, RSWA_DIM) and x.dtype == torch.float32
-                 and x.device == dev and x.stride(2) == 1 and (x.stride(1) == RSWA_DIM or heads == 1),
-                 "k and v are fp32 [rows, heads, 128] on the cache's GPU with contiguous heads")
+    B, shape, i32 = desc.B, k.shape, torch.int32
+    _need(len(shape) == 3 and shape[1] == desc.heads, "k and v must be [rows, heads, 128] with the cache's heads")
+    kp, ldk = _need_rows("k", k, dev, shape)
+    vp, ldv = _need_rows("v", v, dev, shape)
     if n_max is None:
-        n_max = index.shape[1] if index is not None else max(1, k.shape[0] // B)
-    _same_device(dev, torch.int32, count=count, start=start, row0=row0, index=index)
-    _require(all(t is None or t.shape == (B,) for t in (count, start, row0)) and
-             (index is None or index.shape == (B, n_max)), "count, start and row0 are [B], index is [B, n_max]")
-    ld = [x.stride(0) if x.shape[0] > 1 else heads * RSWA_DIM for x in (k, v)]
-    _call(lib().focr_kv_write, dev, stream, ctypes.byref(desc), _ptr(k), ld[0], _ptr(v), ld[1], k.shape[0], _ptr(row0),
-          _ptr(count), _ptr(index), int(n_max), _ptr(start), KV_WRAP if wrap else 0)
+        n_max = index.shape[1] if index is not None else max(1, shape[0] // B)
+    _call(L.focr_kv_write, dev, stream, ctypes.byref(desc), kp, ldk, vp, ldv, shape[0],
+          None if row0 is None else _need_tensor("row0", row0, dev, i32, (B,)), _need_tensor("count", count, dev, i32, (B,)),
+          None if index is None else _need_tensor("index", index, dev, i32, (B, n_max)), n_max,
+          _need_tensor("start", start, dev, i32, (B,)), KV_WRAP if wrap else 0)
     return cache
 
 
 def focr_kv_read(cache, length, k_out=None, v_out=None, stream=None):
     """(k_out, v_out) fp32 [B, heads, cap, 128]: the values of rows < length[b]; other rows keep what the outputs held
     (zero where they are made here)."""
-    import torch
-    dev = cache[0].device
-    _require(cache[0].is_cuda, "the cache must be on a GPU")
+    torch, L = _tensor_lib()
+    dev = _device_of(cache[0], "the cache")
     desc = _kv_desc(cache, dev)
     shape = (desc.B, desc.heads, desc.cap, RSWA_DIM)
-    k_out, v_out = (_new(lambda: torch.zeros(shape, device=dev), dev, stream) if o is None else o for o in (k_out, v_out))
-    _require(k_out.shape == shape and v_out.shape == shape and length.shape == (desc.B,),
-             "outputs are [B, heads, cap, 128], length is [B]")
-    _same_device(dev, torch.float32, k_out=k_out, v_out=v_out)
-    _same_device(dev, torch.int32, length=length)
-    _call(lib().focr_kv_read, dev, stream, ctypes.byref(desc), _ptr(length), _ptr(k_out), _ptr(v_out))
+    if k_out is None:
+        k_out = _new(dev, stream, shape, zero=True)
+    if v_out is None:
+        v_out = _new(dev, stream, shape, zero=True)
+    _call(L.focr_kv_read, dev, stream, ctypes.byref(desc), _need_tensor("length", length, dev, torch.int32, (desc.B,)),
+          _need_tensor("k_out", k_out, dev, torch.float32, shape), _need_tensor("v_out", v_out, dev, torch.float32, shape))
     return k_out, v_out
 
 
@@ -572,35 +595,35 @@ def focr_rswa_tree(q, k_new, v_new, ref, ref_len, ring, n_gen, parent=None, n_no
     """out [B, N, heads_q, 128]: R-SWA attention of N drafted nodes per sequence (N = 1: one token) over the quantised
     caches `ref` and `ring`; parent [B, N] (None: a chain), n_nodes [B] (None: N each).  Rows of nodes >= n_nodes keep
     what `out` held (zero where it is made here)."""
-    import torch
-    dev = q.device
-    _require(q.is_cuda and q.dim() == 4, "q must be [B, N, heads_q, 128] on a GPU")
+    torch, L = _tensor_lib()
+    dev = _device_of(q, "q")
+    shape, f32, i32 = q.shape, torch.float32, torch.int32
+    _need(len(shape) == 4 and shape[3] == RSWA_DIM, "q must be [B, N, heads_q, 128]")
+    B, N, hq, _ = shape
     dref, dring = _kv_desc(ref, dev, "ref"), _kv_desc(ring, dev, "ring")
-    B, N, hq, _ = q.shape
     if out is None:
-        out = _new(lambda: torch.zeros(q.shape, device=dev), dev, stream)
-    _require(q.shape[3] == RSWA_DIM and k_new.shape == (B, N, dref.heads, RSWA_DIM) and v_new.shape == k_new.shape
-             and out.shape == q.shape, "q, out [B, N, heads_q, 128] and k_new, v_new [B, N, heads, 128] are needed")
-    _same_device(dev, torch.float32, q=q, k_new=k_new, v_new=v_new, out=out)
-    _same_device(dev, torch.int32, ref_len=ref_len, n_gen=n_gen, parent=parent, n_nodes=n_nodes)
-    _require(ref_len.shape == (B,) and n_gen.shape == (B,) and (n_nodes is None or n_nodes.shape == (B,))
-             and (parent is None or parent.shape == (B, N)), "ref_len, n_gen, n_nodes are [B], parent is [B, N]")
-    _call(lib().focr_rswa_tree, dev, stream, _ptr(q), _ptr(k_new), _ptr(v_new), B, N, hq, ctypes.byref(dref),
-          _ptr(ref_len), ctypes.byref(dring), _ptr(n_gen), _ptr(parent), _ptr(n_nodes), _ptr(out))
+        out = _new(dev, stream, shape, zero=True)
+    new = (B, N, dref.heads, RSWA_DIM)
+    _call(L.focr_rswa_tree, dev, stream, _need_tensor("q", q, dev, f32, shape), _need_tensor("k_new", k_new, dev, f32, new),
+          _need_tensor("v_new", v_new, dev, f32, new), B, N, hq, ctypes.byref(dref),
+          _need_tensor("ref_len", ref_len, dev, i32, (B,)), ctypes.byref(dring), _need_tensor("n_gen", n_gen, dev, i32, (B,)),
+          None if parent is None else _need_tensor("parent", parent, dev, i32, (B, N)),
+          None if n_nodes is None else _need_tensor("n_nodes", n_nodes, dev, i32, (B,)),
+          _need_tensor("out", out, dev, f32, shape))
     return out
 
 
 def focr_token_probs(logits, temperature: float = 1.0, out=None, stream=None):
     """softmax(logits / temperature) over the last dimension of fp32 logits [..., V]; out may be logits."""
-    import torch
-    dev = logits.device
-    _require(logits.is_cuda and logits.dim() >= 1, "logits must be on a GPU")
+    torch, L = _tensor_lib()
+    dev = _device_of(logits, "logits")
+    shape = logits.shape
+    _need(len(shape) >= 1, "logits must be [..., V]")
     if out is None:
-        out = _new(lambda: torch.empty(logits.shape, device=dev), dev, stream)
-    _require(out.shape == logits.shape, "out must have the shape of logits")
-    _same_device(dev, torch.float32, logits=logits, out=out)
-    V = logits.shape[-1]
-    _call(lib().focr_token_probs, dev, stream, _ptr(logits), logits.numel() // max(1, V), V, float(temperature), _ptr(out))
+        out = _new(dev, stream, shape)
+    V = shape[-1]
+    _call(L.focr_token_probs, dev, stream, _need_tensor("logits", logits, dev, torch.float32, shape),
+          logits.numel() // max(1, V), V, temperature, _need_tensor("out", out, dev, torch.float32, shape))
     return out
 
 
@@ -609,22 +632,24 @@ def focr_spec_verify(target_probs, draft_probs, tokens, parent, n_nodes, u, n_ac
     """Verify drafted trees: target_probs [B, N + 1, V], draft_probs [B, N, V] or None (chosen drafts), tokens [B, N],
     parent [B, N] (None: a chain), n_nodes [B] (None: N each), u [B, N + 1].
     Returns (n_accept [B], path [B, N], next_token [B]), int32."""
-    import torch
-    dev = target_probs.device
-    _require(target_probs.is_cuda and target_probs.dim() == 3, "target_probs must be [B, N + 1, V] on a GPU")
-    B, N, V = target_probs.shape[0], target_probs.shape[1] - 1, target_probs.shape[2]
-    n_accept, path, next_token = (
-        _new(lambda s=s: torch.empty(s, dtype=torch.int32, device=dev), dev, stream) if o is None else o
-        for o, s in ((n_accept, (B,)), (path, (B, N)), (next_token, (B,))))
-    _require(tokens.shape == (B, N) and u.shape == (B, N + 1) and (draft_probs is None or draft_probs.shape == (B, N, V))
-             and (parent is None or parent.shape == (B, N)) and (n_nodes is None or n_nodes.shape == (B,))
-             and n_accept.shape == (B,) and path.shape == (B, N) and next_token.shape == (B,),
-             "tokens, parent, path are [B, N], u is [B, N + 1], draft_probs is [B, N, V], n_nodes, n_accept, next_token are [B]")
-    _same_device(dev, torch.float32, target_probs=target_probs, draft_probs=draft_probs, u=u)
-    _same_device(dev, torch.int32, tokens=tokens, parent=parent, n_nodes=n_nodes, n_accept=n_accept, path=path,
-                 next_token=next_token)
-    _call(lib().focr_spec_verify, dev, stream, _ptr(target_probs), _ptr(draft_probs), V, _ptr(tokens), _ptr(parent),
-          _ptr(n_nodes), _ptr(u), B, N, _ptr(n_accept), _ptr(path), _ptr(next_token))
+    torch, L = _tensor_lib()
+    dev = _device_of(target_probs, "target_probs")
+    shape, f32, i32 = target_probs.shape, torch.float32, torch.int32
+    _need(len(shape) == 3, "target_probs must be [B, N + 1, V]")
+    B, N, V = shape[0], shape[1] - 1, shape[2]
+    if n_accept is None:
+        n_accept = _new(dev, stream, (B,), i32)
+    if path is None:
+        path = _new(dev, stream, (B, N), i32)
+    if next_token is None:
+        next_token = _new(dev, stream, (B,), i32)
+    _call(L.focr_spec_verify, dev, stream, _need_tensor("target_probs", target_probs, dev, f32, shape),
+          None if draft_probs is None else _need_tensor("draft_probs", draft_probs, dev, f32, (B, N, V)), V,
+          _need_tensor("tokens", tokens, dev, i32, (B, N)),
+          None if parent is None else _need_tensor("parent", parent, dev, i32, (B, N)),
+          None if n_nodes is None else _need_tensor("n_nodes", n_nodes, dev, i32, (B,)),
+          _need_tensor("u", u, dev, f32, (B, N + 1)), B, N, _need_tensor("n_accept", n_accept, dev, i32, (B,)),
+          _need_tensor("path", path, dev, i32, (B, N)), _need_tensor("next_token", next_token, dev, i32, (B,)))
     return n_accept, path, next_token
 
 

@@ -1,0 +1,31 @@
+// Thread-block clusters: rank, barrier and reads of another CTA's shared memory.
+#pragma once
+
+#include "common.cuh"
+
+namespace focr {
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
+}
+// the value of the same variable in the shared memory of the cluster's CTA `rank`
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ double ld_cluster(const double* p, uint32_t rank) {
+    double v;
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(p, rank)) : "memory");
+    return v;
+}
+
+}  // namespace focr

@@ -137,7 +137,10 @@ extern "C" focr_status focr_qk_norm_rope(const float* q, int64_t ldq, int32_t he
     p.q = q, p.k = k, p.q_out = q_out, p.k_out = k_out, p.gamma_q = gamma_q, p.gamma_k = gamma_k, p.pos = pos;
     p.ldq = ldq, p.ldk = ldk, p.ldqo = ldqo, p.ldko = ldko;
     p.T = T, p.hq = heads_q, p.hk = heads_k, p.rot = rot_dim, p.flags = flags, p.eps = eps;
-    for (int i = 0; i < RD / 2; ++i) p.rev[i] = i < rot_dim / 2 ? pow(theta, -2. * i / rot_dim) * 0.15915494309189535 : 0.;
+    // powers by repeated products (one pow a call): off by at most i x 2^-53, on angles that shrink with i
+    const double ratio = pow(theta, -2. / rot_dim);
+    double rev = 0.15915494309189535;   // 1 / (2 pi)
+    for (int i = 0; i < RD / 2; ++i, rev *= ratio) p.rev[i] = i < rot_dim / 2 ? rev : 0.;
     void* args[] = {&p};
     return report_launch(launch_kernel((const void*)qk_rope_kernel, dim3(T), dim3(RT), 0, 1, args, (cudaStream_t)stream),
                          "qk_rope_kernel");

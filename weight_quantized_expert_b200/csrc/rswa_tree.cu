@@ -32,6 +32,7 @@
 #include <math.h>
 
 #include "abi_util.h"
+#include "cluster.cuh"
 #include "common.cuh"
 #include "kv_cache.h"
 #include "launch_state.h"
@@ -153,20 +154,6 @@ __device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* src, int
 __device__ __forceinline__ void load_scales(uint32_t dst, const float* src, int rows, int lane) {
     cp4(dst + 4 * lane, src + min(lane, rows - 1));
     cp4(dst + 4 * (lane + 32), src + min(lane + 32, rows - 1));
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
 }
 
 // W16: more than eight columns, so both row halves of the MMA tiles are used.
@@ -545,11 +532,11 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         const int node = (col0 + col) / p.G;
         if (node >= L) continue;
         float M = NONE, l = 0.f, o = 0.f;
-        for (int r = 0; r < p.S; ++r) M = fmaxf(M, ld_cluster(mapa_shared(&sh.part_m[col], r)));
+        for (int r = 0; r < p.S; ++r) M = fmaxf(M, ld_cluster(&sh.part_m[col], r));
         for (int r = 0; r < p.S; ++r) {
-            const float f = ex2(ld_cluster(mapa_shared(&sh.part_m[col], r)) - M);
-            l = fmaf(f, ld_cluster(mapa_shared(&sh.part_l[col], r)), l);
-            o = fmaf(f, ld_cluster(mapa_shared(&sh.part[col][tid], r)), o);
+            const float f = ex2(ld_cluster(&sh.part_m[col], r) - M);
+            l = fmaf(f, ld_cluster(&sh.part_l[col], r), l);
+            o = fmaf(f, ld_cluster(&sh.part[col][tid], r), o);
         }
         p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = o / l;
     }

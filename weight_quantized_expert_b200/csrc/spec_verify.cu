@@ -14,57 +14,159 @@
 // rejection takes p(x) out of W and M.  The next token is the smallest t with sum_{t' <= t} W(t') > u_N sum W.
 // The answers are whole numbers next to borders, so all of it is in fp64 (products and differences of two fp32
 // values are exact or nearly so); sums run in a fixed order.
+//
+// Both are bound by memory (one row of V floats read and written; one row of p and q read per rejection), and by
+// latency for few rows.  A row belongs to a cluster of up to eight CTAs, which exchange one pair of numbers through
+// distributed shared memory; token_probs keeps its part of the row in registers, so the row is read once.  The
+// verification looks up p and q of all drafted tokens at once before it walks, so an accepted node costs no memory
+// latency; a rejection is one pass over the rows, spread over the cluster's warps.
 #include <math.h>
 
 #include "abi_util.h"
+#include "cluster.cuh"
 #include "common.cuh"
+#include "launch_state.h"
 
 namespace focr {
 namespace {
 
 constexpr int TREE_MAX = FOCR_TREE_NODES_MAX;
-constexpr int VT = 1024, VWARPS = VT / 32;
+constexpr int VT = 512, VWARPS = VT / 32;
+constexpr int CLUSTER_MAX = 8;
+
+// ------------------------------------------------------------------ probabilities
+
+constexpr int HELD = 8;   // groups of four values a thread keeps: 16,384 of a row per CTA
 
 struct ProbsParams {
     const float* logits;
     float* probs;
-    int V;
-    float temp;
+    int V, C;        // C: CTAs of a row
+    float temp, inv; // inv = 1 / temp
 };
 
-__global__ void __launch_bounds__(VT) token_probs_kernel(ProbsParams p) {
-    __shared__ float sm[VWARPS];
-    __shared__ double sum[VWARPS];
-    const int tid = threadIdx.x;
-    const float* x = p.logits + (size_t)blockIdx.x * p.V;
-    float* y = p.probs + (size_t)blockIdx.x * p.V;
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// exp((x - base) / temp): the quotient from the reciprocal and one correction (correctly rounded but for rare
+// halfway cases); -inf is held at a finite value, whose exponential is 0, so that the correction stays finite
+__device__ __forceinline__ float expo(float x, float base, const ProbsParams& p) {
+    const float t = max_nan(x - base, -1e30f);
+    const float q = t * p.inv;
+    return expf(fmaf(fmaf(-q, p.temp, t), p.inv, q));
+}
+
+// Group g of a thread: values 4 g' .. 4 g' + 3 (VEC: rows are 16-byte aligned) or four values VT apart.
+template <bool VEC>
+__device__ __forceinline__ float4 get4(const float* x, int g, int tid, int n, float none) {
+    if (VEC) {
+        const int i = 4 * (g * VT + tid);
+        return i < n ? *reinterpret_cast<const float4*>(x + i) : make_float4(none, none, none, none);
+    }
+    const int i = 4 * g * VT + tid;
+    return make_float4(i < n ? x[i] : none, i + VT < n ? x[i + VT] : none, i + 2 * VT < n ? x[i + 2 * VT] : none,
+                       i + 3 * VT < n ? x[i + 3 * VT] : none);
+}
+template <bool VEC>
+__device__ __forceinline__ void put4(float* y, int g, int tid, int n, float4 v) {
+    if (VEC) {
+        const int i = 4 * (g * VT + tid);
+        if (i < n) *reinterpret_cast<float4*>(y + i) = v;
+        return;
+    }
+    const int i = 4 * g * VT + tid;
+    if (i < n) y[i] = v.x;
+    if (i + VT < n) y[i + VT] = v.y;
+    if (i + 2 * VT < n) y[i + 2 * VT] = v.z;
+    if (i + 3 * VT < n) y[i + 3 * VT] = v.w;
+}
+__device__ __forceinline__ float max4(float m, float4 v) { return fmaxf(fmaxf(m, fmaxf(v.x, v.y)), fmaxf(v.z, v.w)); }
+
+template <bool VEC>
+__global__ void __launch_bounds__(VT, 2) token_probs_kernel(ProbsParams p) {
+    __shared__ float wm[VWARPS], cta_m;
+    __shared__ double ws[VWARPS], cta_s;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = p.C > 1 ? (int)cluster_rank() : 0;
+    const size_t row = blockIdx.x / p.C;
+    const int share = ((p.V + p.C - 1) / p.C + 3) & ~3, first = min(p.V, rank * share), n = min(share, p.V - first);
+    const float* x = p.logits + row * p.V + first;
+    float* y = p.probs + row * p.V + first;
+    const int groups = (n + 4 * VT - 1) / (4 * VT);
     pdl_wait();
+    // the part's maximum; the first HELD groups stay in registers
+    float4 v[HELD];
+#pragma unroll
+    for (int g = 0; g < HELD; ++g) v[g] = get4<VEC>(x, g, tid, n, -INFINITY);
     float m = -INFINITY;
-    for (int t = tid; t < p.V; t += VT) m = fmaxf(m, x[t]);
+#pragma unroll
+    for (int g = 0; g < HELD; ++g) m = max4(m, v[g]);
+    for (int g = HELD; g < groups; ++g) m = max4(m, get4<VEC>(x, g, tid, n, -INFINITY));
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((tid & 31) == 0) sm[tid >> 5] = m;
+    if (lane == 0) wm[warp] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < VWARPS; ++w) m = fmaxf(m, sm[w]);
-    double d = 0.;   // a row has up to a million terms
-    for (int t = tid; t < p.V; t += VT) d += (double)expf((x[t] - m) / p.temp);
+    for (int w = 0; w < VWARPS; ++w) m = fmaxf(m, wm[w]);
+    const float base = m == -INFINITY ? 0.f : m;   // a part of masked logits alone sums to 0
+    // exponentials relative to it, and their sum (fp32 in a thread's group of four, fp64 beyond)
+    double s = 0.;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if ((tid & 31) == 0) sum[tid >> 5] = d;
+    for (int g = 0; g < HELD; ++g) {
+        v[g] = make_float4(expo(v[g].x, base, p), expo(v[g].y, base, p), expo(v[g].z, base, p), expo(v[g].w, base, p));
+        s += (double)((v[g].x + v[g].y) + (v[g].z + v[g].w));
+    }
+    for (int g = HELD; g < groups; ++g) {
+        const float4 t = get4<VEC>(x, g, tid, n, -INFINITY);
+        s += (double)((expo(t.x, base, p) + expo(t.y, base, p)) + (expo(t.z, base, p) + expo(t.w, base, p)));
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) ws[warp] = s;
     __syncthreads();
-    d = 0.;
+    s = 0.;
 #pragma unroll
-    for (int w = 0; w < VWARPS; ++w) d += sum[w];
-    const float s = (float)d;
-    for (int t = tid; t < p.V; t += VT) y[t] = expf((x[t] - m) / p.temp) / s;
+    for (int w = 0; w < VWARPS; ++w) s += ws[w];
+    float M = m;
+    if (p.C > 1) {
+        if (tid == 0) cta_m = m, cta_s = s;
+        cluster_sync();
+        for (int r = 0; r < p.C; ++r) M = fmaxf(M, ld_cluster(&cta_m, r));
+        double total = 0.;
+        for (int r = 0; r < p.C; ++r) {
+            const float mr = ld_cluster(&cta_m, r);
+            total += ld_cluster(&cta_s, r) * (double)expo(mr == -INFINITY ? 0.f : mr, M, p);
+        }
+        s = total;
+        cluster_arrive();   // waited for before the CTA ends
+    }
+    // a row of -inf alone has no distribution
+    const float f = M == -INFINITY ? __int_as_float(0x7fc00000) : (float)((double)expo(base, M, p) / s);
+#pragma unroll
+    for (int g = 0; g < HELD; ++g) put4<VEC>(y, g, tid, n, make_float4(v[g].x * f, v[g].y * f, v[g].z * f, v[g].w * f));
+    for (int g = HELD; g < groups; ++g) {
+        const float4 t = get4<VEC>(x, g, tid, n, -INFINITY);
+        put4<VEC>(y, g, tid, n, make_float4(expo(t.x, base, p) * f, expo(t.y, base, p) * f, expo(t.z, base, p) * f, expo(t.w, base, p) * f));
+    }
+    if (p.C > 1) cluster_wait();
 }
+
+// ------------------------------------------------------------------ verification
 
 struct VerifyParams {
     const float *target, *draft, *u;
     const int32_t *tokens, *parent, *n_nodes;
     int32_t *n_accept, *path, *next;
-    int N, V;
+    int N, V, C, vec;
+};
+
+struct VerifyShared {
+    double p[TREE_MAX], q[TREE_MAX], u[TREE_MAX + 1];   // of each node's token behind its parent
+    int par[TREE_MAX], tok[TREE_MAX], gone[TREE_MAX];
+    double warp_sum[VWARPS], cta_sum[2];
+    int bad, next, last, cta_next, cta_last;
 };
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -75,122 +177,244 @@ __device__ __forceinline__ double warp_sum(double v) {
 
 // What is left of the target at token t (see the head of the file).
 struct Residual {
-    const float *p, *q;
+    const float *p, *q;   // q: nullptr while nothing is taken off
     double c;
-    const int* gone;   // rejected tokens of drafts without probabilities
+    const int* gone;      // rejected tokens of drafts without probabilities
     int n_gone;
-    __device__ double at(int t) const {
-        const double v = (double)__ldg(p + t);
-        if (q) return fmax(v - c * (double)__ldg(q + t), 0.);
+    __device__ bool is_gone(int t) const {
         for (int i = 0; i < n_gone; ++i)
-            if (gone[i] == t) return 0.;
-        return v;
+            if (gone[i] == t) return true;
+        return false;
+    }
+    __device__ static double left(float p, float q, double c) {
+        const double v = fma(-c, (double)q, (double)p);
+        return v > 0. ? v : 0.;
+    }
+    __device__ double at(int t) const {
+        if (q) return left(__ldg(p + t), __ldg(q + t), c);
+        return is_gone(t) ? 0. : (double)__ldg(p + t);
     }
 };
 
-// Sums of W over the warps' contiguous segments into `seg`, and the total, in every thread.
-__device__ double segment_sums(const Residual& w, int V, double* seg) {
+constexpr int TILE = 128;   // tokens a warp takes at a time
+constexpr int BATCH = 4;    // tiles in flight
+
+// The lane's share of one tile's sum of W.  vec: four neighbours of an aligned row, else four tokens 32 apart.
+__device__ __forceinline__ void tile_load(const float* x, int tile, int lane, int V, bool vec, float (&o)[4]) {
+    if (vec) {
+        const int t = tile * TILE + 4 * lane;
+        const float4 v = t < V ? __ldg(reinterpret_cast<const float4*>(x + t)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = tile * TILE + 32 * j + lane;
+            o[j] = t < V ? __ldg(x + t) : 0.f;
+        }
+    }
+}
+// Sums of W over tiles t0 .. t0 + BATCH - 1 below t1 (this lane's shares).
+__device__ __forceinline__ void batch_sums(const Residual& w, int t0, int t1, int lane, int V, bool vec, bool any_gone,
+                                           double (&s)[BATCH]) {
+    float p[BATCH][4], q[BATCH][4];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+        const int tile = t0 + i < t1 ? t0 + i : V;   // behind the row: zeros
+        tile_load(w.p, tile, lane, V, vec, p[i]);
+        if (w.q) tile_load(w.q, tile, lane, V, vec, q[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+        double d = 0.;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (w.q)
+                d += Residual::left(p[i][j], q[i][j], w.c);
+            else if (!any_gone || !w.is_gone((t0 + i) * TILE + (vec ? 4 * lane + j : 32 * j + lane)))
+                d += (double)p[i][j];
+        }
+        s[i] = d;
+    }
+}
+
+// sum of W in every thread of the cluster; the warp's and the CTAs' parts stay in shared memory
+__device__ double row_sum(const Residual& w, const VerifyParams& p, VerifyShared& sh, int rank, int t0, int t1, int& turn) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int len = (V + VWARPS - 1) / VWARPS, t0 = warp * len, t1 = min(V, t0 + len);
+    bool any_gone = false;
+    if (!w.q)
+        for (int i = 0; i < w.n_gone; ++i) any_gone |= w.gone[i] / TILE >= t0 && w.gone[i] / TILE < t1;
     double s = 0.;
-    for (int t = t0 + lane; t < t1; t += 32) s += w.at(t);
+    for (int t = t0; t < t1; t += BATCH) {
+        double part[BATCH];
+        batch_sums(w, t, t1, lane, p.V, p.vec, any_gone, part);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) s += part[i];
+    }
     s = warp_sum(s);
-    __syncthreads();
-    if (lane == 0) seg[warp] = s;
+    __syncthreads();   // the sums of the pass before have been read
+    if (lane == 0) sh.warp_sum[warp] = s;
     __syncthreads();
     double total = 0.;
-    for (int i = 0; i < VWARPS; ++i) total += seg[i];
+#pragma unroll
+    for (int i = 0; i < VWARPS; ++i) total += sh.warp_sum[i];
+    if (p.C == 1) return total;
+    // two places in turn: a CTA may write its next sum while another still reads this one
+    turn ^= 1;
+    if (threadIdx.x == 0) sh.cta_sum[turn] = total;
+    cluster_sync();
+    total = 0.;
+    for (int r = 0; r < p.C; ++r) total += ld_cluster(&sh.cta_sum[turn], r);
     return total;
 }
 
-__global__ void __launch_bounds__(VT) spec_verify_kernel(VerifyParams p) {
-    __shared__ double seg[VWARPS];
-    __shared__ int gone[TREE_MAX];
-    __shared__ int sm_bad, sm_next, sm_last;
-    const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, N = p.N, V = p.V;
+__global__ void __launch_bounds__(VT, 1) spec_verify_kernel(VerifyParams p) {
+    __shared__ VerifyShared sh;
+    const int rank = p.C > 1 ? (int)cluster_rank() : 0, b = blockIdx.x / p.C;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, N = p.N, V = p.V;
+    const float *P = p.target + (size_t)b * (N + 1) * V, *Q = p.draft ? p.draft + (size_t)b * N * V : nullptr;
     pdl_wait();
     const int L = p.n_nodes ? __ldg(p.n_nodes + b) : N;
     if (tid == 0) {
-        sm_bad = L < 0 || L > N;
-        sm_next = V;
-        sm_last = -1;
+        sh.bad = L < 0 || L > N;
+        sh.next = V;
+        sh.last = -1;
     }
     __syncthreads();
     if (tid < min(L, N)) {
         const int par = p.parent ? __ldg(p.parent + (size_t)b * N + tid) : tid - 1;
         const int x = __ldg(p.tokens + (size_t)b * N + tid);
-        if (par < -1 || par >= tid || x < 0 || x >= V) sm_bad = 1;
+        if (par < -1 || par >= tid || x < 0 || x >= V) {
+            sh.bad = 1;
+        } else {
+            const size_t at = (size_t)(par + 1) * V + x;
+            sh.par[tid] = par;
+            sh.tok[tid] = x;
+            sh.p[tid] = (double)__ldg(P + at);
+            sh.q[tid] = Q ? (double)__ldg(Q + at) : 1.;
+            sh.u[tid] = (double)__ldg(p.u + (size_t)b * (N + 1) + tid);
+        }
     }
+    if (tid == TREE_MAX) sh.u[TREE_MAX] = (double)__ldg(p.u + (size_t)b * (N + 1) + N);
     __syncthreads();
     int32_t* path = p.path + (size_t)b * N;
-    if (sm_bad) {
-        if (tid < N) path[tid] = -1;
-        if (tid == 0) p.n_accept[b] = p.next[b] = -1;
+    if (sh.bad) {   // the whole cluster sees the same
+        if (rank == 0) {
+            if (tid < N) path[tid] = -1;
+            if (tid == 0) p.n_accept[b] = p.next[b] = -1;
+        }
         return;
     }
-    const float *P = p.target + (size_t)b * (N + 1) * V, *Q = p.draft ? p.draft + (size_t)b * N * V : nullptr;
-    int cur = -1, taken = 0;
+    // this warp's tiles
+    const int tiles = (V + TILE - 1) / TILE, per = (tiles + p.C * VWARPS - 1) / (p.C * VWARPS);
+    const int t0 = min(tiles, (rank * VWARPS + warp) * per), t1 = min(tiles, t0 + per);
+    int cur = -1, taken = 0, turn = 0;
     double M = 1.;
-    Residual w{P, Q, 0., gone, 0};
+    bool summed = false;   // M is the sum of W, and the warps' parts of it are in shared memory
+    Residual w{P, nullptr, 0., sh.gone, 0};
     for (int i = 0; i < L; ++i) {
-        const int par = p.parent ? __ldg(p.parent + (size_t)b * N + i) : i - 1;
-        if (par != cur) continue;
-        const int x = __ldg(p.tokens + (size_t)b * N + i);
-        const double left = w.at(x), q = Q ? (double)__ldg(w.q + x) : 1.;
-        if ((double)__ldg(p.u + (size_t)b * (N + 1) + i) * q * M < left) {
+        if (sh.par[i] != cur) continue;
+        const int x = sh.tok[i];
+        double left = fma(-w.c, sh.q[i], sh.p[i]);
+        if (!Q) left = w.is_gone(x) ? 0. : sh.p[i];
+        left = left > 0. ? left : 0.;
+        if (sh.u[i] * sh.q[i] * M < left) {
             cur = i;
-            if (tid == 0) path[taken] = i;
+            if (rank == 0 && tid == 0) path[taken] = i;
             ++taken;
             M = 1.;
-            w.p = P + (size_t)(cur + 1) * V;
-            w.q = Q && cur + 1 < N ? Q + (size_t)(cur + 1) * V : nullptr;
-            w.c = 0.;
-            w.n_gone = 0;
+            w = Residual{P + (size_t)(cur + 1) * V, nullptr, 0., sh.gone, 0};
+            summed = false;
         } else if (Q) {
             w.c += M;
-            M = segment_sums(w, V, seg);
-        } else {
+            w.q = Q + (size_t)(cur + 1) * V;
+            M = row_sum(w, p, sh, rank, t0, t1, turn);
+            summed = true;
+        } else if (left > 0.) {
             __syncthreads();
-            if (tid == 0) gone[w.n_gone] = x;
+            if (tid == 0) sh.gone[w.n_gone] = x;
             ++w.n_gone;
             M -= left;
             __syncthreads();
         }
     }
-    double total = segment_sums(w, V, seg);
+    double total = summed ? M : row_sum(w, p, sh, rank, t0, t1, turn);
     if (!(total > 0.)) {   // nothing is left (a draft that equals the target, rejected by rounding): the target itself
         w.q = nullptr;
         w.n_gone = 0;
-        total = segment_sums(w, V, seg);
+        total = row_sum(w, p, sh, rank, t0, t1, turn);
     }
-    const double want = (double)__ldg(p.u + (size_t)b * (N + 1) + N) * total;
+    // the warp whose tiles hold the border looks for it
+    const double want = sh.u[TREE_MAX] * total;
     double before = 0.;
-    for (int i = 0; i < warp; ++i) before += seg[i];
-    const int len = (V + VWARPS - 1) / VWARPS, t0 = warp * len, t1 = min(V, t0 + len);
-    // the warp whose segment holds the border scans it; the last token with any mass stands in when rounding
-    // leaves the border behind the last sum
-    for (int tb = t0; tb < t1; tb += 32) {
-        const int t = tb + lane;
-        const double v = t < t1 ? w.at(t) : 0.;
-        double s = v;
+    if (p.C > 1)
+        for (int r = 0; r < rank; ++r) before += ld_cluster(&sh.cta_sum[turn], r);
+    for (int i = 0; i < warp; ++i) before += sh.warp_sum[i];
+    const double mine = sh.warp_sum[warp];
+    if (mine > 0.) {
+        int found = V;
+        const bool border = before + mine > want;
+        for (int t = t0; t < t1 && found == V && border; t += BATCH) {
+            double part[BATCH];
+            batch_sums(w, t, t1, lane, V, p.vec, w.n_gone > 0, part);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double up = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += up;
+            for (int i = 0; i < BATCH; ++i) {
+                const double tile = warp_sum(part[i]);
+                if (found == V && tile > 0. && before + tile > want) {
+                    double at = before;
+                    for (int j = 0; j < TILE / 32 && found == V; ++j) {   // token by token, in order
+                        const int tok = (t + i) * TILE + 32 * j + lane;
+                        const double v = tok < V ? w.at(tok) : 0.;
+                        double s = v;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const double up = __shfl_up_sync(0xffffffffu, s, o);
+                            if (lane >= o) s += up;
+                        }
+                        const unsigned hit = __ballot_sync(0xffffffffu, v > 0. && at + s > want);
+                        if (hit) found = (t + i) * TILE + 32 * j + __ffs(hit) - 1;
+                        at += __shfl_sync(0xffffffffu, s, 31);
+                    }
+                }
+                before += tile;
+            }
         }
-        if (v > 0.) {
-            if (before + s > want) atomicMin(&sm_next, t);
-            atomicMax(&sm_last, t);
-        }
-        before += __shfl_sync(0xffffffffu, s, 31);
+        if (lane == 0 && found < V) atomicMin(&sh.next, found);
     }
     __syncthreads();
-    if (tid == 0) {
-        const int last = sm_last < 0 ? V - 1 : sm_last;
-        p.next[b] = min(sm_next, last);
-        p.n_accept[b] = taken;
-        for (int i = taken; i < N; ++i) path[i] = -1;
+    int next = sh.next;
+    if (p.C > 1) {
+        if (tid == 0) sh.cta_next = next;
+        cluster_sync();
+        if (rank == 0 && tid < p.C) {
+            int o;
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(o) : "r"(mapa_shared(&sh.cta_next, tid)) : "memory");
+            atomicMin(&sh.next, o);
+        }
+        cluster_sync();
+        next = sh.next;
     }
+    if (rank != 0) return;
+    if (next == V && warp == 0) {   // rounding left the border behind the last sum: the last token with any mass
+        int last = -1;
+        for (int t = (V - 1) / 32 * 32; t >= 0 && last < 0; t -= 32) {
+            const unsigned hit = __ballot_sync(0xffffffffu, t + lane < V && w.at(t + lane) > 0.);
+            if (hit) last = t + 31 - __clz(hit);
+        }
+        next = last < 0 ? V - 1 : last;
+    }
+    if (tid == 0) {
+        p.next[b] = next;
+        p.n_accept[b] = taken;
+    }
+    if (tid >= taken && tid < N) path[tid] = -1;
+}
+
+// CTAs of a row of V values: at most `most` values each, and smaller parts while the device is not full
+int row_cluster(int rows, int V, int most, int least) {
+    const int sms = device_sms() > 0 ? device_sms() : 148;
+    int C = 1;
+    while (C < CLUSTER_MAX && (V > C * most || (rows * C < sms && V > C * least))) C *= 2;
+    return C;
 }
 
 }  // namespace
@@ -204,15 +428,17 @@ focr_status focr_token_probs(const float* logits, int32_t T, int32_t V, float te
     if (!logits || !probs) return report_error(FOCR_ERR_INVALID_ARG, "NULL argument");
     if (T < 1 || T > FOCR_T_MAX) return reportf(FOCR_ERR_INVALID_ARG, "T=%d outside [1, %d]", T, FOCR_T_MAX);
     if (V < 1 || V > FOCR_V_MAX) return reportf(FOCR_ERR_INVALID_ARG, "V=%d outside [1, %d]", V, FOCR_V_MAX);
-    if (!(temperature > 0.f) || !isfinite(temperature))
-        return reportf(FOCR_ERR_INVALID_ARG, "temperature=%g must be positive", (double)temperature);
+    if (!(temperature >= 1e-6f && temperature <= 1e6f))
+        return reportf(FOCR_ERR_INVALID_ARG, "temperature=%g outside [1e-6, 1e6]", (double)temperature);
     if (misaligned(logits, 4) || misaligned(probs, 4)) return report_error(FOCR_ERR_INVALID_ARG, "misaligned logits or probs");
     const size_t bytes = 4ull * T * V;
     if (probs != logits && ranges_overlap(logits, bytes, probs, bytes))
         return report_error(FOCR_ERR_INVALID_ARG, "probs overlaps logits without being it");
-    ProbsParams p{logits, probs, V, temperature};
+    ProbsParams p{logits, probs, V, row_cluster(T, V, 4 * VT * HELD, 4 * VT), temperature, 1.f / temperature};
+    const bool vec = V % 4 == 0 && !misaligned(logits, 16) && !misaligned(probs, 16);
+    const void* fn = vec ? (const void*)token_probs_kernel<true> : (const void*)token_probs_kernel<false>;
     void* args[] = {&p};
-    return report_launch(launch_kernel((const void*)token_probs_kernel, dim3(T), dim3(VT), 0, 1, args, (cudaStream_t)stream),
+    return report_launch(launch_kernel(fn, dim3((unsigned)T * p.C), dim3(VT), 0, p.C, args, (cudaStream_t)stream),
                          "token_probs_kernel");
 }
 
@@ -229,9 +455,12 @@ focr_status focr_spec_verify(const float* target, const float* draft, int32_t V,
     const void* all[] = {target, draft, tokens, parent, n_nodes, u, n_accept, path, next_token};
     for (const void* x : all)
         if (misaligned(x, 4)) return report_error(FOCR_ERR_INVALID_ARG, "misaligned argument");
-    VerifyParams p{target, draft, u, tokens, parent, n_nodes, n_accept, path, next_token, N, V};
+    VerifyParams p{target, draft, u, tokens, parent, n_nodes, n_accept, path, next_token, N, V,
+                   row_cluster(B, V, VWARPS * TILE * BATCH, VWARPS * TILE),
+                   V % 4 == 0 && !misaligned(target, 16) && !misaligned(draft, 16)};
     void* args[] = {&p};
-    return report_launch(launch_kernel((const void*)spec_verify_kernel, dim3(B), dim3(VT), 0, 1, args, (cudaStream_t)stream),
+    return report_launch(launch_kernel((const void*)spec_verify_kernel, dim3((unsigned)B * p.C), dim3(VT), 0, p.C, args,
+                                       (cudaStream_t)stream),
                          "spec_verify_kernel");
 }
 
