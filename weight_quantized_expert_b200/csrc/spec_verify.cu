@@ -17,7 +17,7 @@
 //
 // Both are bound by memory (one row of V floats read and written; one row of p and q read per rejection), and by
 // latency for few rows.  A row belongs to a cluster of up to eight CTAs, which exchange one pair of numbers through
-// distributed shared memory; token_probs keeps its part of the row in registers, so the row is read once.  The
+// distributed shared memory; token_probs keeps its part of the row in shared memory, so the row is read once.  The
 // verification looks up p and q of all drafted tokens at once before it walks, so an accepted node costs no memory
 // latency; a rejection is one pass over the rows, spread over the cluster's warps.
 #include <math.h>
@@ -36,13 +36,16 @@ constexpr int CLUSTER_MAX = 8;
 
 // ------------------------------------------------------------------ probabilities
 
-constexpr int HELD = 8;   // groups of four values a thread keeps: 16,384 of a row per CTA
+constexpr int PT = 1024, PWARPS = PT / 32;
+
+// values of a row per CTA of its cluster
+__host__ __device__ inline int row_share(int V, int C) { return ((V + C - 1) / C + 3) & ~3; }
 
 struct ProbsParams {
     const float* logits;
     float* probs;
-    int V, C;        // C: CTAs of a row
-    float temp, inv; // inv = 1 / temp
+    int T, V, C;             // C: CTAs of a row
+    float scale, scale_lo;   // log2(e) / temperature, as a sum of two floats
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
@@ -50,107 +53,195 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-// exp((x - base) / temp): the quotient from the reciprocal and one correction (correctly rounded but for rare
-// halfway cases); -inf is held at a finite value, whose exponential is 0, so that the correction stays finite
+// exp((x - base) / temperature).  The exponent's rounding is that of the difference and of one product (the scale
+// carries two floats).  -inf is held at a finite value, whose exponential is 0, so that the sum below stays finite.
 __device__ __forceinline__ float expo(float x, float base, const ProbsParams& p) {
     const float t = max_nan(x - base, -1e30f);
-    const float q = t * p.inv;
-    return expf(fmaf(fmaf(-q, p.temp, t), p.inv, q));
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(fmaf(t, p.scale, t * p.scale_lo)));
+    return y;
 }
 
-// Group g of a thread: values 4 g' .. 4 g' + 3 (VEC: rows are 16-byte aligned) or four values VT apart.
+// Group g of a thread: values 4 g' .. 4 g' + 3 (VEC: rows are 16-byte aligned) or four values PT apart.
 template <bool VEC>
 __device__ __forceinline__ float4 get4(const float* x, int g, int tid, int n, float none) {
     if (VEC) {
-        const int i = 4 * (g * VT + tid);
+        const int i = 4 * (g * PT + tid);
         return i < n ? *reinterpret_cast<const float4*>(x + i) : make_float4(none, none, none, none);
     }
-    const int i = 4 * g * VT + tid;
-    return make_float4(i < n ? x[i] : none, i + VT < n ? x[i + VT] : none, i + 2 * VT < n ? x[i + 2 * VT] : none,
-                       i + 3 * VT < n ? x[i + 3 * VT] : none);
+    const int i = 4 * g * PT + tid;
+    return make_float4(i < n ? x[i] : none, i + PT < n ? x[i + PT] : none, i + 2 * PT < n ? x[i + 2 * PT] : none,
+                       i + 3 * PT < n ? x[i + 3 * PT] : none);
 }
 template <bool VEC>
 __device__ __forceinline__ void put4(float* y, int g, int tid, int n, float4 v) {
     if (VEC) {
-        const int i = 4 * (g * VT + tid);
+        const int i = 4 * (g * PT + tid);
         if (i < n) *reinterpret_cast<float4*>(y + i) = v;
         return;
     }
-    const int i = 4 * g * VT + tid;
+    const int i = 4 * g * PT + tid;
     if (i < n) y[i] = v.x;
-    if (i + VT < n) y[i + VT] = v.y;
-    if (i + 2 * VT < n) y[i + 2 * VT] = v.z;
-    if (i + 3 * VT < n) y[i + 3 * VT] = v.w;
+    if (i + PT < n) y[i + PT] = v.y;
+    if (i + 2 * PT < n) y[i + 2 * PT] = v.z;
+    if (i + 3 * PT < n) y[i + 3 * PT] = v.w;
 }
 __device__ __forceinline__ float max4(float m, float4 v) { return fmaxf(fmaxf(m, fmaxf(v.x, v.y)), fmaxf(v.z, v.w)); }
 
+// Starts the copy of group g into its place in shared memory (values past n become -inf).  A thread reads back only
+// what it copied itself, so waiting for its own copies is enough.
 template <bool VEC>
-__global__ void __launch_bounds__(VT, 2) token_probs_kernel(ProbsParams p) {
-    __shared__ float wm[VWARPS], cta_m;
-    __shared__ double ws[VWARPS], cta_s;
+__device__ __forceinline__ void fetch4(float4* held, const float* x, int g, int tid, int n) {
+    float4* at = held + g * PT + tid;
+    const uint32_t dst = smem_u32(at);
+    if (VEC) {
+        const int i = 4 * (g * PT + tid);
+        if (i < n)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(x + i) : "memory");
+        else
+            *at = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int i = (4 * g + j) * PT + tid;
+        if (i < n)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * j), "l"(x + i) : "memory");
+        else
+            reinterpret_cast<float*>(at)[j] = -INFINITY;
+    }
+}
+
+struct Part {   // maximum of some logits and the sum of their exponentials relative to it
+    float m;
+    double s;
+};
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }   // masked logits alone sum to 0
+// Joins the parts of `width` neighbouring lanes, in every one of them.
+__device__ __forceinline__ Part join_lanes(Part a, int width, const ProbsParams& p) {
+    float M = a.m;
+    for (int o = width / 2; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    double s = a.s * (double)expo(base_of(a.m), base_of(M), p);
+    for (int o = width / 2; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return {M, s};
+}
+
+// A cluster takes rows in turn: a row's part goes from shared memory to registers, the next row's copies start, and are
+// in flight while this row is worked on, its sums come together and its probabilities are written.
+// KEPT: groups of four values a thread keeps; the rest of a long row is read again.
+template <bool VEC, int KEPT>
+__global__ void __launch_bounds__(PT) token_probs_kernel(const __grid_constant__ ProbsParams p) {
+    extern __shared__ __align__(16) float4 held[];   // [KEPT][PT]
+    __shared__ float wm[PWARPS];
+    __shared__ double ws[PWARPS], parts[2][2 * CLUSTER_MAX];   // parts: every CTA's maximum and sum of a row
+    __shared__ uint64_t bar[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = p.C > 1 ? (int)cluster_rank() : 0;
-    const size_t row = blockIdx.x / p.C;
-    const int share = ((p.V + p.C - 1) / p.C + 3) & ~3, first = min(p.V, rank * share), n = min(share, p.V - first);
-    const float* x = p.logits + row * p.V + first;
-    float* y = p.probs + row * p.V + first;
-    const int groups = (n + 4 * VT - 1) / (4 * VT);
+    const int rank = p.C > 1 ? (int)cluster_rank() : 0, rows = gridDim.x / p.C;
+    const int share = row_share(p.V, p.C), first = min(p.V, rank * share), n = min(share, p.V - first);
+    const int groups = (n + 4 * PT - 1) / (4 * PT);
+    int row = blockIdx.x / p.C, turn = 0, phase = 0;
     pdl_wait();
-    // the part's maximum; the first HELD groups stay in registers
-    float4 v[HELD];
+    auto fetch = [&](int r) {
 #pragma unroll
-    for (int g = 0; g < HELD; ++g) v[g] = get4<VEC>(x, g, tid, n, -INFINITY);
-    float m = -INFINITY;
-#pragma unroll
-    for (int g = 0; g < HELD; ++g) m = max4(m, v[g]);
-    for (int g = HELD; g < groups; ++g) m = max4(m, get4<VEC>(x, g, tid, n, -INFINITY));
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) wm[warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < VWARPS; ++w) m = fmaxf(m, wm[w]);
-    const float base = m == -INFINITY ? 0.f : m;   // a part of masked logits alone sums to 0
-    // exponentials relative to it, and their sum (fp32 in a thread's group of four, fp64 beyond)
-    double s = 0.;
-#pragma unroll
-    for (int g = 0; g < HELD; ++g) {
-        v[g] = make_float4(expo(v[g].x, base, p), expo(v[g].y, base, p), expo(v[g].z, base, p), expo(v[g].w, base, p));
-        s += (double)((v[g].x + v[g].y) + (v[g].z + v[g].w));
-    }
-    for (int g = HELD; g < groups; ++g) {
-        const float4 t = get4<VEC>(x, g, tid, n, -INFINITY);
-        s += (double)((expo(t.x, base, p) + expo(t.y, base, p)) + (expo(t.z, base, p) + expo(t.w, base, p)));
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) ws[warp] = s;
-    __syncthreads();
-    s = 0.;
-#pragma unroll
-    for (int w = 0; w < VWARPS; ++w) s += ws[w];
-    float M = m;
+        for (int g = 0; g < KEPT; ++g) fetch4<VEC>(held, p.logits + (size_t)r * p.V + first, g, tid, n);
+    };
+    fetch(row);
     if (p.C > 1) {
-        if (tid == 0) cta_m = m, cta_s = s;
-        cluster_sync();
-        for (int r = 0; r < p.C; ++r) M = fmaxf(M, ld_cluster(&cta_m, r));
-        double total = 0.;
-        for (int r = 0; r < p.C; ++r) {
-            const float mr = ld_cluster(&cta_m, r);
-            total += ld_cluster(&cta_s, r) * (double)expo(mr == -INFINITY ? 0.f : mr, M, p);
+        if (tid == 0) {
+            mbar_init(&bar[0], 1);
+            mbar_init(&bar[1], 1);
+            fence_barrier_init();
         }
-        s = total;
-        cluster_arrive();   // waited for before the CTA ends
+        cluster_sync();
     }
-    // a row of -inf alone has no distribution
-    const float f = M == -INFINITY ? __int_as_float(0x7fc00000) : (float)((double)expo(base, M, p) / s);
+    for (; row < p.T; row += rows, phase ^= turn, turn ^= 1) {
+        const float* x = p.logits + (size_t)row * p.V + first;
+        float* y = p.probs + (size_t)row * p.V + first;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        float4 v[KEPT];
 #pragma unroll
-    for (int g = 0; g < HELD; ++g) put4<VEC>(y, g, tid, n, make_float4(v[g].x * f, v[g].y * f, v[g].z * f, v[g].w * f));
-    for (int g = HELD; g < groups; ++g) {
-        const float4 t = get4<VEC>(x, g, tid, n, -INFINITY);
-        put4<VEC>(y, g, tid, n, make_float4(expo(t.x, base, p) * f, expo(t.y, base, p) * f, expo(t.z, base, p) * f, expo(t.w, base, p) * f));
+        for (int g = 0; g < KEPT; ++g) v[g] = held[g * PT + tid];   // what this thread copied itself
+        if (row + rows < p.T) fetch(row + rows);
+        // relative to the warp's maximum: sums within the warp need no factors
+        Part a{-INFINITY, 0.};
+#pragma unroll
+        for (int g = 0; g < KEPT; ++g) a.m = max4(a.m, v[g]);
+        for (int g = KEPT; g < groups; ++g) a.m = max4(a.m, get4<VEC>(x, g, tid, n, -INFINITY));
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) a.m = fmaxf(a.m, __shfl_xor_sync(0xffffffffu, a.m, o));
+        const float base = base_of(a.m);
+#pragma unroll
+        for (int g = 0; g < KEPT; ++g) {
+            v[g] = make_float4(expo(v[g].x, base, p), expo(v[g].y, base, p), expo(v[g].z, base, p), expo(v[g].w, base, p));
+            a.s += (double)((v[g].x + v[g].y) + (v[g].z + v[g].w));
+        }
+        for (int g = KEPT; g < groups; ++g) {
+            const float4 t = get4<VEC>(x, g, tid, n, -INFINITY);
+            a.s += (double)((expo(t.x, base, p) + expo(t.y, base, p)) + (expo(t.z, base, p) + expo(t.w, base, p)));
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+        // Warps, then CTAs.  The first warp stores the CTA's pair into every CTA of the cluster, completing on their
+        // barriers: unlike a cluster barrier this does not wait for the stores of the row before.  A CTA sends a row's
+        // pair after it has all pairs of the row before, so two places are enough.
+        if (lane == 0) wm[warp] = a.m, ws[warp] = a.s;
+        __syncthreads();
+        if (warp == 0) {
+            a = join_lanes({wm[lane & (PWARPS - 1)], ws[lane & (PWARPS - 1)]}, PWARPS, p);
+            if (p.C == 1) {   // st.async belongs to clusters
+                if (lane == 0) parts[turn][0] = (double)a.m, parts[turn][1] = a.s;
+            } else {
+                if (lane == 0) mbar_arrive_expect_tx(&bar[turn], 16 * p.C);
+                if (lane < p.C) {
+                    const uint32_t at = mapa_shared(&parts[turn][2 * rank], lane), on = mapa_shared(&bar[turn], lane);
+                    st_async_f64(at, (double)a.m, on);
+                    st_async_f64(at + 8, a.s, on);
+                }
+            }
+        }
+        bool arrived = true;
+        if (p.C == 1)
+            __syncthreads();
+        else
+            arrived = mbar_wait_bounded(&bar[turn], phase, 2000000000ull);
+        const int from = 2 * (lane & (p.C - 1));
+        a = join_lanes({(float)parts[turn][from], parts[turn][from + 1]}, p.C, p);
+        // a row of -inf alone has no distribution (and a wait that ran out gives no numbers)
+        const float f = a.m == -INFINITY || !arrived ? __int_as_float(0x7fc00000) : expo(base, a.m, p) / (float)a.s;
+#pragma unroll
+        for (int g = 0; g < KEPT; ++g) put4<VEC>(y, g, tid, n, make_float4(v[g].x * f, v[g].y * f, v[g].z * f, v[g].w * f));
+        for (int g = KEPT; g < groups; ++g) {
+            const float4 t = get4<VEC>(x, g, tid, n, -INFINITY);
+            put4<VEC>(y, g, tid, n, make_float4(expo(t.x, base, p) * f, expo(t.y, base, p) * f, expo(t.z, base, p) * f, expo(t.w, base, p) * f));
+        }
     }
-    if (p.C > 1) cluster_wait();
+}
+
+template <bool VEC, int KEPT>
+cudaError_t launch_probs(ProbsParams& p, cudaStream_t st) {
+    const void* fn = (const void*)token_probs_kernel<VEC, KEPT>;
+    const size_t smem = (size_t)KEPT * PT * 16;
+    const cudaError_t e = once_per_device(fn, [&] {
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    });
+    if (e != cudaSuccess) return e;
+    // as many clusters as stay resident: they take rows in turn
+    int rows = p.T;
+    if (p.T * p.C > 128) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)p.C);
+        cfg.blockDim = dim3(PT);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)p.C, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int most = 0;
+        if (cudaOccupancyMaxActiveClusters(&most, fn, &cfg) == cudaSuccess && most > 0 && rows > most) rows = most;
+    }
+    void* args[] = {&p};
+    return launch_kernel(fn, dim3((unsigned)(rows * p.C)), dim3(PT), smem, p.C, args, st);
 }
 
 // ------------------------------------------------------------------ verification
@@ -267,7 +358,7 @@ __device__ double row_sum(const Residual& w, const VerifyParams& p, VerifyShared
     return total;
 }
 
-__global__ void __launch_bounds__(VT, 1) spec_verify_kernel(VerifyParams p) {
+__global__ void __launch_bounds__(VT, 2) spec_verify_kernel(VerifyParams p) {
     __shared__ VerifyShared sh;
     const int rank = p.C > 1 ? (int)cluster_rank() : 0, b = blockIdx.x / p.C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, N = p.N, V = p.V;
@@ -434,12 +525,18 @@ focr_status focr_token_probs(const float* logits, int32_t T, int32_t V, float te
     const size_t bytes = 4ull * T * V;
     if (probs != logits && ranges_overlap(logits, bytes, probs, bytes))
         return report_error(FOCR_ERR_INVALID_ARG, "probs overlaps logits without being it");
-    ProbsParams p{logits, probs, V, row_cluster(T, V, 4 * VT * HELD, 4 * VT), temperature, 1.f / temperature};
+    ProbsParams p;
+    p.logits = logits, p.probs = probs, p.T = T, p.V = V;
+    p.C = row_cluster(T, V, 4 * PT * 8, 4 * PT);
+    const double scale = 1.4426950408889634 / (double)temperature;
+    p.scale = (float)scale, p.scale_lo = (float)(scale - (double)p.scale);
     const bool vec = V % 4 == 0 && !misaligned(logits, 16) && !misaligned(probs, 16);
-    const void* fn = vec ? (const void*)token_probs_kernel<true> : (const void*)token_probs_kernel<false>;
-    void* args[] = {&p};
-    return report_launch(launch_kernel(fn, dim3((unsigned)T * p.C), dim3(VT), 0, p.C, args, (cudaStream_t)stream),
-                         "token_probs_kernel");
+    const int groups = (row_share(V, p.C) + 4 * PT - 1) / (4 * PT);
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = groups <= 1   ? (vec ? launch_probs<true, 1>(p, st) : launch_probs<false, 1>(p, st))
+                          : groups <= 4 ? (vec ? launch_probs<true, 4>(p, st) : launch_probs<false, 4>(p, st))
+                                        : (vec ? launch_probs<true, 8>(p, st) : launch_probs<false, 8>(p, st));
+    return report_launch(e, "token_probs_kernel");
 }
 
 focr_status focr_spec_verify(const float* target, const float* draft, int32_t V, const int32_t* tokens,
