@@ -18,8 +18,7 @@ namespace focr {
 namespace {
 
 constexpr int RD = FOCR_RSWA_DIM;
-constexpr int RT = 256;            // threads: eight warps, one row each at a time
-constexpr int RWARPS = RT / 32;
+constexpr int RWARPS = 16;         // most warps of a block
 
 struct RopeParams {
     const float *q, *k;
@@ -32,56 +31,89 @@ struct RopeParams {
     double rev[RD / 2];   // revolutions per position of each pair: theta^(-2i / rot) / (2 pi)
 };
 
-__global__ void __launch_bounds__(RT) qk_rope_kernel(const __grid_constant__ RopeParams p) {
-    __shared__ float2 cs[RD / 2];
-    __shared__ __align__(16) float row[RWARPS][RD];
-    const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int half = p.rot / 2;
-    const bool inter = p.flags & FOCR_ROPE_INTERLEAVED, norm = p.flags & FOCR_QK_NORM;
+// A block has one token; half a warp has a row (two rows a warp share its instructions), loaded before the angles are
+// formed.  Lane l of a half has dims 4 l .. 4 l + 3 and 64 + 4 l .. 64 + 4 l + 3.
+// HOW: 0 pairs (2i, 2i + 1); 1 pairs (i, i + 64): both in a lane.  2 pairs (i, i + rot / 2), rot < 128, through shared
+// memory.
+template <int HOW, bool NORM>
+__global__ void __launch_bounds__(32 * RWARPS, 3) qk_rope_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ __align__(16) float2 cs[RD / 2];
+    __shared__ __align__(16) float row[HOW == 2 ? 2 * RWARPS : 1][RD];
+    const int t = blockIdx.x, l = threadIdx.x & 15, h0 = threadIdx.x >> 4, step = blockDim.x >> 4;
+    const int half = p.rot / 2, heads = p.hq + p.hk;
+    const float* q = p.q + (size_t)t * p.ldq + 4 * l;
+    const float* k = p.k + (size_t)t * p.ldk + 4 * l;
     pdl_wait();
-    if (threadIdx.x < half) {
+    auto load = [&](int h, float4& a, float4& b) {
+        const float4* src = reinterpret_cast<const float4*>(h < p.hq ? q + h * RD : k + (h - p.hq) * RD);
+        a = src[0], b = src[16];
+    };
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (h0 < heads) load(h0, a, b);
+    float4 g0, g1;
+    auto weights = [&](int h) {
+        const float4* g = reinterpret_cast<const float4*>(h < p.hq ? p.gamma_q : p.gamma_k);
+        g0 = g ? __ldg(g + l) : make_float4(1.f, 1.f, 1.f, 1.f);
+        g1 = g ? __ldg(g + l + 16) : make_float4(1.f, 1.f, 1.f, 1.f);
+    };
+    if (NORM) weights(h0);
+    if (threadIdx.x < RD / 2) {   // behind the last pair: no turn
         const double r = (double)__ldg(p.pos + t) * p.rev[threadIdx.x];
         float s, c;
         sincospif(2.f * (float)(r - rint(r)), &s, &c);
         cs[threadIdx.x] = make_float2(c, s);
     }
     __syncthreads();
-    for (int h = warp; h < p.hq + p.hk; h += RWARPS) {
-        const bool isq = h < p.hq;
-        const int hh = isq ? h : h - p.hq;
-        const float* src = (isq ? p.q + (size_t)t * p.ldq : p.k + (size_t)t * p.ldk) + (size_t)hh * RD;
-        float* dst = (isq ? p.q_out + (size_t)t * p.ldqo : p.k_out + (size_t)t * p.ldko) + (size_t)hh * RD;
-        float4 v = reinterpret_cast<const float4*>(src)[lane];
-        if (norm) {
-            float ss = v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float inv = 1.f / sqrtf(ss * (1.f / RD) + p.eps);
-            const float* gamma = isq ? p.gamma_q : p.gamma_k;
-            float4 g = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (gamma) g = __ldg(reinterpret_cast<const float4*>(gamma) + lane);
-            v = make_float4(v.x * inv * g.x, v.y * inv * g.y, v.z * inv * g.z, v.w * inv * g.w);
+    // cosines and sines of the lane's pairs
+    float4 t0, t1;
+    if (HOW == 0) t0 = *reinterpret_cast<const float4*>(&cs[2 * l]), t1 = *reinterpret_cast<const float4*>(&cs[32 + 2 * l]);
+    if (HOW == 1) t0 = *reinterpret_cast<const float4*>(&cs[4 * l]), t1 = *reinterpret_cast<const float4*>(&cs[4 * l + 2]);
+    for (int h = h0; h - (h0 & 1) < heads; h += step) {   // both halves of a warp stay together
+        const bool live = h < heads, isq = h < p.hq;
+        if (h != h0 && live) {
+            load(h, a, b);
+            if (NORM) weights(h);
         }
-        __syncwarp();
-        reinterpret_cast<float4*>(row[warp])[lane] = v;
-        __syncwarp();
-        float o[4];
+        if (NORM) {
+            float ss = (a.x * a.x + a.y * a.y) + (a.z * a.z + a.w * a.w) + ((b.x * b.x + b.y * b.y) + (b.z * b.z + b.w * b.w));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int d = 4 * lane + j;
-            const float x = row[warp][d];
-            if (d >= p.rot) {
-                o[j] = x;
-            } else if (inter) {
-                const float2 a = cs[d >> 1];
-                o[j] = d & 1 ? x * a.x + row[warp][d - 1] * a.y : x * a.x - row[warp][d + 1] * a.y;
-            } else {
-                const float2 a = cs[d < half ? d : d - half];
-                o[j] = d < half ? x * a.x - row[warp][d + half] * a.y : x * a.x + row[warp][d - half] * a.y;
-            }
+            for (int o = 8; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float inv = rsqrtf(ss * (1.f / RD) + p.eps);
+            a = make_float4(a.x * inv * g0.x, a.y * inv * g0.y, a.z * inv * g0.z, a.w * inv * g0.w);
+            b = make_float4(b.x * inv * g1.x, b.y * inv * g1.y, b.z * inv * g1.z, b.w * inv * g1.w);
         }
-        reinterpret_cast<float4*>(dst)[lane] = make_float4(o[0], o[1], o[2], o[3]);
+        float4 x = a, y = b;
+        if (HOW == 0) {
+            x = make_float4(a.x * t0.x - a.y * t0.y, a.y * t0.x + a.x * t0.y, a.z * t0.z - a.w * t0.w, a.w * t0.z + a.z * t0.w);
+            y = make_float4(b.x * t1.x - b.y * t1.y, b.y * t1.x + b.x * t1.y, b.z * t1.z - b.w * t1.w, b.w * t1.z + b.z * t1.w);
+        } else if (HOW == 1) {
+            x = make_float4(a.x * t0.x - b.x * t0.y, a.y * t0.z - b.y * t0.w, a.z * t1.x - b.z * t1.y, a.w * t1.z - b.w * t1.w);
+            y = make_float4(b.x * t0.x + a.x * t0.y, b.y * t0.z + a.y * t0.w, b.z * t1.x + a.z * t1.y, b.w * t1.z + a.w * t1.w);
+        } else {
+            float* r = row[threadIdx.x >> 4];
+            __syncwarp();
+            reinterpret_cast<float4*>(r)[l] = a, reinterpret_cast<float4*>(r)[l + 16] = b;
+            __syncwarp();
+            auto turned = [&](int d) {
+                if (d >= p.rot) return r[d];
+                const float2 c = cs[d < half ? d : d - half];
+                return d < half ? r[d] * c.x - r[d + half] * c.y : r[d] * c.x + r[d - half] * c.y;
+            };
+            x = make_float4(turned(4 * l), turned(4 * l + 1), turned(4 * l + 2), turned(4 * l + 3));
+            y = make_float4(turned(64 + 4 * l), turned(65 + 4 * l), turned(66 + 4 * l), turned(67 + 4 * l));
+        }
+        if (live) {
+            float4* dst = reinterpret_cast<float4*>((isq ? p.q_out + (size_t)t * p.ldqo + h * RD
+                                                         : p.k_out + (size_t)t * p.ldko + (h - p.hq) * RD) + 4 * l);
+            dst[0] = x, dst[16] = y;
+        }
     }
+}
+
+template <bool NORM>
+const void* rope_kernel(const RopeParams& p) {
+    if (p.flags & FOCR_ROPE_INTERLEAVED) return (const void*)qk_rope_kernel<0, NORM>;
+    return p.rot == RD ? (const void*)qk_rope_kernel<1, NORM> : (const void*)qk_rope_kernel<2, NORM>;
 }
 
 // Whether rows of `wa` floats at `a` (stride lda) and of `wb` floats at `b` (stride ldb) share an element.
@@ -141,7 +173,10 @@ extern "C" focr_status focr_qk_norm_rope(const float* q, int64_t ldq, int32_t he
     const double ratio = pow(theta, -2. / rot_dim);
     double rev = 0.15915494309189535;   // 1 / (2 pi)
     for (int i = 0; i < RD / 2; ++i, rev *= ratio) p.rev[i] = i < rot_dim / 2 ? rev : 0.;
+    const int warps = (heads_q + heads_k + 1) / 2;   // two rows each; at least the 64 threads that form the angles
+    const int threads = 32 * (warps < 2 ? 2 : warps < RWARPS ? warps : RWARPS);
     void* args[] = {&p};
-    return report_launch(launch_kernel((const void*)qk_rope_kernel, dim3(T), dim3(RT), 0, 1, args, (cudaStream_t)stream),
+    return report_launch(launch_kernel(flags & FOCR_QK_NORM ? rope_kernel<true>(p) : rope_kernel<false>(p), dim3(T), dim3(threads), 0,
+                                       1, args, (cudaStream_t)stream),
                          "qk_rope_kernel");
 }
