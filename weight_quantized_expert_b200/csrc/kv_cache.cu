@@ -14,7 +14,7 @@ namespace focr {
 namespace {
 
 constexpr int RD = FOCR_RSWA_DIM;
-constexpr int CT = 256, CWARPS = CT / 32;
+constexpr int CT = 256, CROWS = CT / 16;   // half a warp has a token of a head: its K row and its V row
 
 struct WriteParams {
     KvView c;
@@ -24,47 +24,70 @@ struct WriteParams {
     int n_max, wrap;
 };
 
-// One row of 128 by a warp (four values a lane).
-__device__ __forceinline__ void quantise_row(float4 x, int type, void* codes, float* scale, int lane) {
-    float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+// The code of one value: round-half-even(fp32(x / s)).  The product with the reciprocal is within 127 x 2^-21 of the
+// quotient; only where it lies nearer than that to a border of the rounding (or is not a number) is the division done.
+__device__ __forceinline__ int code_of(float x, float s, float inv) {
+    const float t = x * inv, r = rintf(t);
+    if (!(fabsf(t - r) < 0.4999f)) return __float2int_rn(x / s);
+    return (int)r;
+}
+// A row of 128 by half a warp: lane l has values 4 l .. 4 l + 3 (a) and 64 + 4 l .. 64 + 4 l + 3 (b).
+template <bool INT4>
+__device__ __forceinline__ void quantise_row(float4 a, float4 b, bool live, uint8_t* codes, float* scale, int l) {
+    float m = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
+                    fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    const float s = a / (type == FOCR_W_INT8 ? 127.f : 7.f);
-    const float in[4] = {x.x, x.y, x.z, x.w};
-    int q[4];
+    for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float s = m / (INT4 ? 7.f : 127.f), inv = 1.f / s;
+    const float in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t w[2] = {0u, 0u};
+    if (s > 0.f) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int r = s > 0.f ? __float2int_rn(in[j] / s) : 0;
-        q[j] = type == FOCR_W_INT8 ? max(-127, min(127, r)) : max(-8, min(7, r));
+        for (int j = 0; j < 8; ++j) {
+            const int q = code_of(in[j], s, inv);
+            if (INT4)
+                w[j / 4] |= (uint32_t)(max(-8, min(7, q)) & 15) << 4 * (j % 4);
+            else
+                w[j / 4] |= (uint32_t)(max(-127, min(127, q)) & 255) << 8 * (j % 4);
+        }
     }
-    if (type == FOCR_W_INT8)
-        reinterpret_cast<uint32_t*>(codes)[lane] =
-            (q[0] & 255) | (q[1] & 255) << 8 | (q[2] & 255) << 16 | (uint32_t)(q[3] & 255) << 24;
-    else
-        reinterpret_cast<uint16_t*>(codes)[lane] =
-            (uint16_t)((q[0] & 15) | (q[1] & 15) << 4 | (q[2] & 15) << 8 | (q[3] & 15) << 12);
-    if (lane == 0) *scale = s;
+    if (!live) return;
+    if (INT4) {
+        reinterpret_cast<uint16_t*>(codes)[l] = (uint16_t)w[0];
+        reinterpret_cast<uint16_t*>(codes)[l + 16] = (uint16_t)w[1];
+    } else {
+        reinterpret_cast<uint32_t*>(codes)[l] = w[0];
+        reinterpret_cast<uint32_t*>(codes)[l + 16] = w[1];
+    }
+    if (l == 0) *scale = s;
 }
 
-// A warp writes one token of one head: its K row and its V row.
+template <bool INT4>
 __global__ void __launch_bounds__(CT) kv_write_kernel(const __grid_constant__ WriteParams p) {
-    const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31;
-    const int i = blockIdx.x * CWARPS + (threadIdx.x >> 5);
+    const int b = blockIdx.z, h = blockIdx.y, l = threadIdx.x & 15;
+    const int i = blockIdx.x * CROWS + (threadIdx.x >> 4);
     pdl_wait();
     const int n = __ldg(p.count + b), s0 = __ldg(p.start + b);
-    if (n < 0 || n > p.n_max || i >= n || s0 < 0) return;
-    if (!p.wrap && (int64_t)s0 + n > p.c.cap) return;
-    if (p.wrap && i < n - p.c.cap) return;   // a later token of the call takes its slot
-    const int64_t src = (p.row0 ? (int64_t)__ldg(p.row0 + b) : (int64_t)b * p.n_max) +
-                        (p.index ? __ldg(p.index + (size_t)b * p.n_max + i) : i);
-    if (src < 0 || src >= p.n_rows) return;
-    const int slot = (int)(((int64_t)s0 + i) % p.c.cap);
-    const float4 xk = __ldg(reinterpret_cast<const float4*>(p.k + src * p.ldk + (size_t)h * RD) + lane);
-    const float4 xv = __ldg(reinterpret_cast<const float4*>(p.v + src * p.ldv + (size_t)h * RD) + lane);
+    bool live = n >= 0 && n <= p.n_max && i < n && s0 >= 0;
+    if (p.wrap)
+        live = live && i >= n - p.c.cap;   // a later token of the call takes the slot of an earlier one
+    else
+        live = live && s0 <= p.c.cap - n;
+    int64_t src = 0;
+    if (live) {
+        src = (p.row0 ? (int64_t)__ldg(p.row0 + b) : (int64_t)b * p.n_max) + (p.index ? __ldg(p.index + (size_t)b * p.n_max + i) : i);
+        live = src >= 0 && src < p.n_rows;
+    }
+    if (!__any_sync(0xffffffffu, live)) return;   // both halves stay for the shuffles
+    if (!live) src = 0;
+    const float4* k = reinterpret_cast<const float4*>(p.k + src * p.ldk + (size_t)h * RD) + l;
+    const float4* v = reinterpret_cast<const float4*>(p.v + src * p.ldv + (size_t)h * RD) + l;
+    float4 ka = __ldg(k), kb = __ldg(k + 16), va = __ldg(v), vb = __ldg(v + 16);
+    const int slot = p.wrap ? (int)(((uint32_t)s0 + (uint32_t)i) % (uint32_t)p.c.cap) : s0 + i;
     const size_t r = ((size_t)b * p.c.heads + h) * p.c.cap + slot;
-    const size_t rb = p.c.type == FOCR_W_INT8 ? RD : RD / 2;
-    quantise_row(xk, p.c.type, p.c.k + r * rb, p.c.ks + r, lane);
-    quantise_row(xv, p.c.type, p.c.v + r * rb, p.c.vs + r, lane);
+    constexpr size_t RB = INT4 ? RD / 2 : RD;
+    quantise_row<INT4>(ka, kb, live, p.c.k + r * RB, p.c.ks + r, l);
+    quantise_row<INT4>(va, vb, live, p.c.v + r * RB, p.c.vs + r, l);
 }
 
 struct ReadParams {
@@ -73,29 +96,38 @@ struct ReadParams {
     float *k_out, *v_out;
 };
 
+// four codes as values
+template <bool INT4>
+__device__ __forceinline__ float4 values4(uint32_t w, float s) {
+    if (INT4)
+        return make_float4((float)((int)(w << 28) >> 28) * s, (float)((int)(w << 24) >> 28) * s, (float)((int)(w << 20) >> 28) * s,
+                           (float)((int)(w << 16) >> 28) * s);
+    return make_float4((float)(int8_t)w * s, (float)(int8_t)(w >> 8) * s, (float)(int8_t)(w >> 16) * s, (float)(int8_t)(w >> 24) * s);
+}
+
+template <bool INT4>
 __global__ void __launch_bounds__(CT) kv_read_kernel(const __grid_constant__ ReadParams p) {
-    const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31;
-    const int i = blockIdx.x * CWARPS + (threadIdx.x >> 5);
+    const int b = blockIdx.z, h = blockIdx.y, l = threadIdx.x & 15;
+    const int i = blockIdx.x * CROWS + (threadIdx.x >> 4);
     pdl_wait();
     const int n = __ldg(p.len + b);
     if (n < 0 || n > p.c.cap || i >= n) return;
     const size_t r = ((size_t)b * p.c.heads + h) * p.c.cap + i;
+    uint32_t w[2][2];
+    float s[2];
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-        const uint8_t* codes = kv ? p.c.v : p.c.k;
-        const float s = (kv ? p.c.vs : p.c.ks)[r];
-        float o[4];
-        if (p.c.type == FOCR_W_INT8) {
-            const uint32_t w = reinterpret_cast<const uint32_t*>(codes + r * RD)[lane];
+        const uint8_t* codes = (kv ? p.c.v : p.c.k) + r * (INT4 ? RD / 2 : RD);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = (float)(int8_t)(w >> 8 * j) * s;
-        } else {
-            const uint32_t w = reinterpret_cast<const uint16_t*>(codes + r * (RD / 2))[lane];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = (float)((int)(w << (28 - 4 * j)) >> 28) * s;
-        }
-        reinterpret_cast<float4*>((kv ? p.v_out : p.k_out) + r * RD)[lane] = make_float4(o[0], o[1], o[2], o[3]);
+        for (int j = 0; j < 2; ++j)
+            w[kv][j] = INT4 ? reinterpret_cast<const uint16_t*>(codes)[l + 16 * j] : reinterpret_cast<const uint32_t*>(codes)[l + 16 * j];
+        s[kv] = (kv ? p.c.vs : p.c.ks)[r];
     }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            reinterpret_cast<float4*>((kv ? p.v_out : p.k_out) + r * RD)[l + 16 * j] = values4<INT4>(w[kv][j], s[kv]);
 }
 
 }  // namespace
@@ -144,8 +176,9 @@ focr_status focr_kv_write(const focr_kv_cache* c, const float* k, int64_t ldk, c
     p.k = k, p.v = v, p.row0 = row0, p.count = count, p.index = index, p.start = start;
     p.ldk = ldk, p.ldv = ldv, p.n_rows = n_rows, p.n_max = n_max, p.wrap = flags & FOCR_KV_WRAP;
     void* args[] = {&p};
-    const dim3 grid((n_max + CWARPS - 1) / CWARPS, c->heads, c->B);
-    return report_launch(launch_kernel((const void*)kv_write_kernel, grid, dim3(CT), 0, 1, args, (cudaStream_t)stream),
+    const dim3 grid((n_max + CROWS - 1) / CROWS, c->heads, c->B);
+    const void* fn = c->type == FOCR_W_INT4 ? (const void*)kv_write_kernel<true> : (const void*)kv_write_kernel<false>;
+    return report_launch(launch_kernel(fn, grid, dim3(CT), 0, 1, args, (cudaStream_t)stream),
                          "kv_write_kernel");
 }
 
@@ -162,8 +195,9 @@ focr_status focr_kv_read(const focr_kv_cache* c, const int32_t* len, float* k_ou
     if (ranges_overlap(k_out, bytes, v_out, bytes)) return report_error(FOCR_ERR_INVALID_ARG, "k_out and v_out overlap");
     p.len = len, p.k_out = k_out, p.v_out = v_out;
     void* args[] = {&p};
-    const dim3 grid((c->cap + CWARPS - 1) / CWARPS, c->heads, c->B);
-    return report_launch(launch_kernel((const void*)kv_read_kernel, grid, dim3(CT), 0, 1, args, (cudaStream_t)stream),
+    const dim3 grid((c->cap + CROWS - 1) / CROWS, c->heads, c->B);
+    const void* fn = c->type == FOCR_W_INT4 ? (const void*)kv_read_kernel<true> : (const void*)kv_read_kernel<false>;
+    return report_launch(launch_kernel(fn, grid, dim3(CT), 0, 1, args, (cudaStream_t)stream),
                          "kv_read_kernel");
 }
 
