@@ -97,23 +97,32 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 __device__ __forceinline__ void cp_wait1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 __device__ __forceinline__ void cp_wait0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-// d += a (16 x 32) * b (32 x 8); A_S8: a is signed and b too (query top digit x codes); else a is unsigned digits
+// d = a (16 x 32) * b (32 x 8) + c.  A_S8: a is signed like b (the query's top digit); else a holds unsigned digits.
 template <bool A_S8>
-__device__ __forceinline__ void mma(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, int c0, int c1, int c2, int c3) {
     if (A_S8)
-        asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
     else
-        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
 }
-// 65536 d2 + 256 d1 + d0 of three accumulators that started at MAGIC_BITS
-__device__ __forceinline__ float join(int d2, int d1, int d0) {
-    const float f2 = __int_as_float(d2) - MAGIC, f1 = __int_as_float(d1) - MAGIC, f0 = __int_as_float(d0) - MAGIC;
-    return fmaf(f2, 65536.f, fmaf(f1, 256.f, f0));
+// the same, with the accumulator started (FIRST) at the pattern that reads as MAGIC + sum
+template <bool A_S8, bool FIRST>
+__device__ __forceinline__ void mma(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (FIRST)
+        mma<A_S8>(d, a, b0, b1, MAGIC_BITS, MAGIC_BITS, MAGIC_BITS, MAGIC_BITS);
+    else
+        mma<A_S8>(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
+// 65536 d2 + 256 d1 + d0 of three accumulators that started at MAGIC_BITS, as two parts: lower() + upper().  The
+// products with the constants are exact (multiples of 256 and 65536 below 2^24 of them), the sums round once each.
+__device__ __forceinline__ float lower(int d1, int d0) {
+    return fmaf(__int_as_float(d1), 256.f, -257.f * MAGIC) + __int_as_float(d0);
+}
+__device__ __forceinline__ float upper(int d2) { return fmaf(__int_as_float(d2), 65536.f, -65536.f * MAGIC); }
 // bytes of four words, transposed: o[i] = byte i of a, b, c, d
 __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&o)[4]) {
     const uint32_t t0 = __byte_perm(a, b, 0x5140), t1 = __byte_perm(c, d, 0x5140);
@@ -141,14 +150,24 @@ struct Block {   // where a block's rows are
     int ring_slot;   // first ring slot, or -1 for reference rows
 };
 
+// Starts the copies of a block's codes; a whole block's addresses are one base and constants.
 template <bool INT4>
 __device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* src, int rows, bool is_v, int lane) {
-    constexpr int CH = INT4 ? 4 : 8, STEP = 32 / CH;
-    const int j = lane % CH;
+    constexpr int CH = INT4 ? 4 : 8, STEP = 32 / CH;   // STEP rows a round: a multiple of 4, so the swizzle repeats
+    const int j = lane % CH, r0 = lane / CH;
+    if (rows == BLK) {
+        const uint8_t* from = src + lane * 16;
 #pragma unroll
-    for (int i = 0; i < BLK / STEP; ++i) {
-        const int r = lane / CH + STEP * i;
-        cp16(dst + (is_v ? v_off<INT4>(r, j) : k_off<INT4>(r, j)), src + (size_t)min(r, rows - 1) * (CH * 16) + j * 16);
+        for (int i = 0; i < BLK / STEP; ++i) {
+            const int r = r0 + STEP * i;
+            cp16(dst + (is_v ? v_off<INT4>(r, j) : k_off<INT4>(r, j)), from + STEP * i * (CH * 16));
+        }
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < BLK / STEP; ++i) {
+            const int r = r0 + STEP * i;
+            cp16(dst + (is_v ? v_off<INT4>(r, j) : k_off<INT4>(r, j)), src + (size_t)min(r, rows - 1) * (CH * 16) + j * 16);
+        }
     }
 }
 __device__ __forceinline__ void load_scales(uint32_t dst, const float* src, int rows, int lane) {
@@ -300,12 +319,6 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             int acc[4][3][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int d = 0; d < 3; ++d)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j][d][i] = MAGIC_BITS;
             uint32_t kb[4][8];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -329,10 +342,17 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
                     const uint32_t a[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        if (d == 2)
-                            mma<true>(acc[j][d], a, kb[j][2 * s], kb[j][2 * s + 1]);
-                        else
-                            mma<false>(acc[j][d], a, kb[j][2 * s], kb[j][2 * s + 1]);
+                        if (s == 0) {
+                            if (d == 2)
+                                mma<true, true>(acc[j][d], a, kb[j][2 * s], kb[j][2 * s + 1]);
+                            else
+                                mma<false, true>(acc[j][d], a, kb[j][2 * s], kb[j][2 * s + 1]);
+                        } else {
+                            if (d == 2)
+                                mma<true, false>(acc[j][d], a, kb[j][2 * s], kb[j][2 * s + 1]);
+                            else
+                                mma<false, false>(acc[j][d], a, kb[j][2 * s], kb[j][2 * s + 1]);
+                        }
                     }
                 }
 #pragma unroll
@@ -343,7 +363,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
                 vs[jj][0] = v2.x, vs[jj][1] = v2.y;
 #pragma unroll
                 for (int i = 0; i < (W16 ? 4 : 2); ++i)
-                    T[jj][i] = join(acc[j][2][i], acc[j][1][i], acc[j][0][i]) * (i & 1 ? ks.y : ks.x);
+                    T[jj][i] = (upper(acc[j][2][i]) + lower(acc[j][1][i], acc[j][0][i])) * (i & 1 ? ks.y : ks.x);
                 if (!whole) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -471,20 +491,25 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         __syncwarp();
         if (next < nblk) load_codes<INT4>(st + St::V, nxt.v, nxt.rows, true, lane);
         cp_commit();
+        bool moved = false;   // a new maximum rescales what there is; mostly there is none
+#pragma unroll
+        for (int e = 0; e < HALVES; ++e) moved |= alpha[e] != 1.f;
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int t = 0; t < 16; ++t)
+#pragma unroll
+                for (int i = 0; i < (W16 ? 4 : 2); ++i) O[t][i] *= alpha[i >> 1];
+        }
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
             int acc[3][4];
 #pragma unroll
-            for (int d = 0; d < 3; ++d)
+            for (int d = 0; d < 3; ++d) mma<false, true>(acc[d], pd[0][d], vb[0][t][0], vb[0][t][1]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[d][i] = MAGIC_BITS;
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int d = 0; d < 3; ++d) mma<false>(acc[d], pd[kk][d], vb[kk][t][0], vb[kk][t][1]);
+            for (int d = 0; d < 3; ++d) mma<false, false>(acc[d], pd[1][d], vb[1][t][0], vb[1][t][1]);
 #pragma unroll
             for (int i = 0; i < (W16 ? 4 : 2); ++i)
-                O[t][i] = fmaf(O[t][i], alpha[i >> 1], gain[i >> 1] * join(acc[2][i], acc[1][i], acc[0][i]));
+                O[t][i] = fmaf(upper(acc[2][i]), gain[i >> 1], fmaf(lower(acc[1][i], acc[0][i]), gain[i >> 1], O[t][i]));
         }
         cur = nxt;
     }
