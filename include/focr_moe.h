@@ -435,8 +435,8 @@ focr_status focr_rswa_decode(const float* q, const float* k_new, const float* v_
  * probabilities, verify the drafts, commit the accepted ones to the ring.  Source of the geometry: franken_ocr README,
  * "Design Philosophy" and "Architecture" (R-SWA), frankenocr.pages.dev, "One forward pass", steps 6 and 7, and
  * "Four bits, one shared scale" (the codes).  The pages fix none of these formulas; each call states its own.
- * Every call is asynchronous on `stream`, needs no workspace, holds no state between calls and gives the same bits
- * for the same inputs.  Calls may overlap as long as no buffer that one of them writes is used by another.
+ * Every call is asynchronous on `stream`, holds no state between calls and gives the same bits for the same inputs.
+ * Calls may overlap as long as no buffer that one of them writes (a workspace is one) is used by another.
  */
 #define FOCR_HEADS_MAX 128          /* most heads (query or kv) of these calls */
 #define FOCR_TREE_NODES_MAX 64      /* most drafted nodes x query heads per kv head */
@@ -521,12 +521,16 @@ focr_status focr_kv_read(const focr_kv_cache* c, const int32_t* len, float* k_ou
  *   1 <= N, N * heads_q / heads <= FOCR_TREE_NODES_MAX.
  *   Rows of nodes >= n_nodes[b] are left as they were.  A sequence with ref_len outside [0, ref->cap], n_gen < 0,
  *   n_nodes outside [0, N] or a bad parent of a live node gets NaN (in all N rows if n_nodes is the bad value).
+ *   workspace: DEVICE, 256-byte aligned, >= focr_rswa_tree_workspace_bytes(B, N, heads_q, heads, ref->cap) bytes (0 for
+ *   small calls: may then be NULL).  It needs no zero fill and holds nothing between calls; calls that share one must
+ *   not overlap.
  * Errors: FOCR_ERR_INVALID_ARG, FOCR_ERR_UNSUPPORTED (types, ring size, heads), FOCR_ERR_CUDA.
  */
+size_t focr_rswa_tree_workspace_bytes(int32_t B, int32_t N, int32_t heads_q, int32_t heads, int32_t ref_cap);
 focr_status focr_rswa_tree(const float* q, const float* k_new, const float* v_new, int32_t B, int32_t N,
                            int32_t heads_q, const focr_kv_cache* ref, const int32_t* ref_len,
                            const focr_kv_cache* ring, const int32_t* n_gen, const int32_t* parent,
-                           const int32_t* n_nodes, float* out, void* stream);
+                           const int32_t* n_nodes, float* out, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * focr_token_probs -- probs[t] = softmax(logits[t] / temperature), DEVICE fp32 [T][V], fp32 arithmetic.  probs may be

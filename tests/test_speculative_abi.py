@@ -82,7 +82,8 @@ def test_read_refusals():
 
 def tree(ref=None, ring=None, **kw):
     a = dict(dict(q=at(8), k=at(10), v=at(12), B=1, N=1, hq=10), **{k: kw.pop(k) for k in ("q", "k", "v", "B", "N", "hq") if k in kw})
-    b = dict(dict(n_gen=at(5), parent=None, n_nodes=None, out=at(14)), **{k: kw.pop(k) for k in ("n_gen", "parent", "n_nodes", "out") if k in kw})
+    b = dict(dict(n_gen=at(5), parent=None, n_nodes=None, out=at(14), ws=None, ws_bytes=0),
+             **{k: kw.pop(k) for k in ("n_gen", "parent", "n_nodes", "out", "ws", "ws_bytes") if k in kw})
     ref, ring = cache(**(ref or dict(cap=289))), cache(**(ring or {}))
     return api.lib().focr_rswa_tree(*a.values(), ctypes.byref(ref), kw.get("ref_len", at(4)), ctypes.byref(ring), *b.values(), None)
 
@@ -94,10 +95,18 @@ def tree(ref=None, ring=None, **kw):
     (dict(hq=15), UNSUPPORTED, "query heads"), (dict(hq=5), UNSUPPORTED, "query heads"), (dict(hq=130), UNSUPPORTED, "query heads"),
     (dict(N=0), INVALID, "nodes"), (dict(N=65), INVALID, "nodes"), (dict(N=33, hq=20), INVALID, "nodes"),
     (dict(N=1 << 30, hq=40), INVALID, "nodes"), (dict(q=at(8) + 4), INVALID, "aligned"), (dict(parent=at(6) + 2), INVALID, "misaligned"),
+    (dict(ref=dict(cap=32768)), INVALID, "workspace"), (dict(ref=dict(cap=32768), ws=at(15), ws_bytes=256), INVALID, "workspace"),
+    (dict(ref=dict(cap=32768), ws=at(15) + 64, ws_bytes=1 << 30), INVALID, "workspace"),
     (dict(out=at(8)), INVALID, "overlap"), (dict(out=at(10)), INVALID, "overlap"), (dict(out=at(12) + 16), INVALID, "overlap"),
 ])
 def test_tree_refusals(bad, status, word):
     assert tree(**bad) == status and word in api.focr_last_error()
+
+
+def test_tree_workspace_sizes():
+    size = api.focr_rswa_tree_workspace_bytes
+    assert size(1, 1, 10, 10, 289) == 0 and size(8, 32, 10, 10, 32768) % 256 == 0 < size(8, 32, 10, 10, 32768)
+    assert all(size(*a) == 0 for a in ((0, 1, 1, 1, 64), (1, 0, 1, 1, 64), (1, 1, 1, 0, 64), (1, 1, 1, 2, 64), (1, 1, 1, 1, 1 << 20)))
 
 
 @pytest.mark.parametrize("args,word", [

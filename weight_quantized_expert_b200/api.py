@@ -37,7 +37,7 @@ EXPORTED = (
     "focr_decode_step_workspace_bytes", "focr_decode_step", "focr_w8a8_pack", "focr_w8a8_free",
     "focr_w8a8_export", "focr_w8a8_quantize_x", "focr_w8a8_workspace_bytes", "focr_w8a8_gemv", "focr_w8a8_check",
     "focr_lm_head_check", "focr_rswa_workspace_bytes", "focr_rswa_decode", "focr_qk_norm_rope", "focr_kv_write",
-    "focr_kv_read", "focr_rswa_tree", "focr_token_probs", "focr_spec_verify",
+    "focr_kv_read", "focr_rswa_tree_workspace_bytes", "focr_rswa_tree", "focr_token_probs", "focr_spec_verify",
 )
 FWD_RESIDUAL = 1
 FWD_DETERMINISTIC = 2
@@ -128,7 +128,8 @@ def lib():
                 "focr_kv_write": (i32, [ctypes.POINTER(KVCacheDesc), P, i64, P, i64, i64, P, P, P, i32, P, i32, P]),
                 "focr_kv_read": (i32, [ctypes.POINTER(KVCacheDesc), P, P, P, P]),
                 "focr_rswa_tree": (i32, [P, P, P, i32, i32, i32, ctypes.POINTER(KVCacheDesc), P,
-                                         ctypes.POINTER(KVCacheDesc), P, P, P, P, P]),
+                                         ctypes.POINTER(KVCacheDesc), P, P, P, P, P, sz, P]),
+                "focr_rswa_tree_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
                 "focr_token_probs": (i32, [P, i32, i32, ctypes.c_float, P, P]),
                 "focr_spec_verify": (i32, [P, P, i32, P, P, P, P, i32, i32, P, P, P, P]),
                 "focr_last_error": (ctypes.c_char_p, []),
@@ -591,10 +592,15 @@ def focr_kv_read(cache, length, k_out=None, v_out=None, stream=None):
     return k_out, v_out
 
 
-def focr_rswa_tree(q, k_new, v_new, ref, ref_len, ring, n_gen, parent=None, n_nodes=None, out=None, stream=None):
+def focr_rswa_tree_workspace_bytes(B: int, N: int, heads_q: int, heads: int, ref_cap: int) -> int:
+    return int(lib().focr_rswa_tree_workspace_bytes(B, N, heads_q, heads, ref_cap))
+
+
+def focr_rswa_tree(q, k_new, v_new, ref, ref_len, ring, n_gen, parent=None, n_nodes=None, out=None, workspace=None,
+                   stream=None):
     """out [B, N, heads_q, 128]: R-SWA attention of N drafted nodes per sequence (N = 1: one token) over the quantised
     caches `ref` and `ring`; parent [B, N] (None: a chain), n_nodes [B] (None: N each).  Rows of nodes >= n_nodes keep
-    what `out` held (zero where it is made here)."""
+    what `out` held (zero where it is made here).  workspace: uint8, focr_rswa_tree_workspace_bytes (made here if None)."""
     torch, L = _tensor_lib()
     dev = _device_of(q, "q")
     shape, f32, i32 = q.shape, torch.float32, torch.int32
@@ -603,13 +609,18 @@ def focr_rswa_tree(q, k_new, v_new, ref, ref_len, ring, n_gen, parent=None, n_no
     dref, dring = _kv_desc(ref, dev, "ref"), _kv_desc(ring, dev, "ring")
     if out is None:
         out = _new(dev, stream, shape, zero=True)
+    if workspace is None:
+        need = L.focr_rswa_tree_workspace_bytes(B, N, hq, dref.heads, dref.cap)
+        workspace = _new(dev, stream, (need,), torch.uint8) if need else None
+    ws_bytes = 0 if workspace is None else workspace.numel()
     new = (B, N, dref.heads, RSWA_DIM)
     _call(L.focr_rswa_tree, dev, stream, _need_tensor("q", q, dev, f32, shape), _need_tensor("k_new", k_new, dev, f32, new),
           _need_tensor("v_new", v_new, dev, f32, new), B, N, hq, ctypes.byref(dref),
           _need_tensor("ref_len", ref_len, dev, i32, (B,)), ctypes.byref(dring), _need_tensor("n_gen", n_gen, dev, i32, (B,)),
           None if parent is None else _need_tensor("parent", parent, dev, i32, (B, N)),
           None if n_nodes is None else _need_tensor("n_nodes", n_nodes, dev, i32, (B,)),
-          _need_tensor("out", out, dev, f32, shape))
+          _need_tensor("out", out, dev, f32, shape),
+          None if workspace is None else _need_tensor("workspace", workspace, dev, torch.uint8, (ws_bytes,)), ws_bytes)
     return out
 
 

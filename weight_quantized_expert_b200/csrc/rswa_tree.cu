@@ -25,10 +25,14 @@
 //   bit pattern of 1.5 * 2^23 and are read back as floats by one subtraction.
 // Drafted keys and values stay fp32 and are few: a warp takes a column and walks its line on the CUDA cores.
 //
-// Work split: a cluster of S CTAs (four warps each) has one kv head of one sequence and up to 16 columns; its warps
-// take the 64-key blocks in turn (reference rows, then the ring), each with its own copies in flight (cp.async into
-// its part of shared memory: the next block's K loads while P V runs, its V while Q K runs).  Warps join in shared
-// memory, CTAs through distributed shared memory.  Bound by memory: 264 B (int8) or 136 B (int4) a key and head.
+// Work split: a unit is one kv head of one sequence with up to 16 columns; its keys are blocks of 64 (reference rows,
+// then the ring), which the four warps of a CTA take in turn, each with its own copies in flight (cp.async into its part
+// of shared memory: the next block's K loads while P V runs, its V while Q K runs).  Warps join in shared memory.
+//   few units   a cluster of S CTAs has a unit and joins through distributed shared memory: one launch.
+//   many units  all blocks of all units in one row, cut into equal ranges, one per resident CTA (the lengths are read
+//               on the device, so ragged batches stay balanced); units that a cut divides leave partial results in
+//               the workspace, and a second kernel joins them.
+// Bound by memory: 264 B (int8) or 136 B (int4) a key and head.
 #include <math.h>
 
 #include "abi_util.h"
@@ -60,8 +64,11 @@ struct TreeParams {
     KvView ref, ring;
     const int32_t *ref_len, *n_gen, *parent, *n_nodes;
     float* out;
-    int N, hq, hk, G, S, groups;   // S: CTAs of a cluster; groups: column groups of 16 per kv head
+    int B, N, hq, hk, G, S, groups;   // S: CTAs of a cluster; groups: column groups of 16 per kv head
+    float* part;                      // ranges: two partial results per CTA, or nullptr (clusters)
 };
+// A partial result: 16 columns' maxima, sums and unnormalised outputs.
+constexpr int PART_L = COLS, PART_O = 2 * COLS, PART_FLOATS = 2 * COLS + COLS * RD;
 
 template <bool INT4>
 struct Stage {   // a warp's part of shared memory: one block of keys; later its partial output
@@ -79,8 +86,63 @@ struct Shared {
     int ages[COLS];                    // ring slots younger than this are seen (0 for a column without a node)
     unsigned long long line[TREE_MAX];
     int par[TREE_MAX];
-    int bad;
+    int scan[WARPS + 4];
 };
+
+// Blocks of a sequence (one at least: the drafted keys need a CTA too).
+__device__ __forceinline__ int sequence_blocks(const TreeParams& p, int b) {
+    const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b);
+    if (R < 0 || R > p.ref.cap || n < 0) return 1;
+    return max(1, (R + BLK - 1) / BLK + (min(n, RW) + BLK - 1) / BLK);
+}
+struct Place {   // a block in the row of all units' blocks
+    int b, unit, block;   // sequence, unit of the sequence, block of the unit
+};
+// Sums over all threads of the CTA; the threads' inclusive prefix in `mine`.
+__device__ __forceinline__ int cta_scan(int& mine, int* scan) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, mine, o);
+        if (lane >= o) mine += up;
+    }
+    __syncthreads();
+    if (lane == 31) scan[warp] = mine;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) mine += scan[w];
+        total += scan[w];
+    }
+    return total;
+}
+// All blocks of the call.
+__device__ int all_blocks(const TreeParams& p, int* scan) {
+    int mine = 0;
+    for (int b = threadIdx.x; b < p.B; b += PT) mine += sequence_blocks(p, b);
+    return cta_scan(mine, scan) * p.hk * p.groups;
+}
+// Where block `at` of the row is.
+__device__ Place find_block(const TreeParams& p, int at, int* scan) {
+    const int per = p.hk * p.groups;
+    int before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += PT) {
+        const int b = b0 + threadIdx.x, own = b < p.B ? sequence_blocks(p, b) : 0;
+        int sum = own;
+        const int total = cta_scan(sum, scan);
+        if ((int64_t)(before + total) * per > at) {
+            const int64_t first = (int64_t)(before + sum - own) * per;
+            if (at >= first && at < first + (int64_t)own * per) scan[WARPS] = b, scan[WARPS + 1] = (int)(at - first), scan[WARPS + 2] = own;
+            __syncthreads();
+            const Place x{scan[WARPS], scan[WARPS + 1] / scan[WARPS + 2], scan[WARPS + 1] % scan[WARPS + 2]};
+            __syncthreads();
+            return x;
+        }
+        before += total;
+    }
+    return Place{p.B, 0, 0};
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -183,56 +245,70 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
     Shared& sh = *reinterpret_cast<Shared*>(smem + WARPS * St::BYTES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, c = lane & 3;
     const int rank = p.S > 1 ? (int)cluster_rank() : 0;
-    const int unit = blockIdx.x / p.S, group = unit % p.groups, pair = unit / p.groups, b = pair / p.hk, h = pair % p.hk;
-    const int col0 = group * COLS, cols = min(COLS, p.N * p.G - col0);
     uint8_t* stage = smem + warp * St::BYTES;
     const uint32_t st = smem_u32(stage);
-
     pdl_wait();
-    const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b), L = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
-    if (tid == 0) sh.bad = R < 0 || R > p.ref.cap || n < 0 || L < 0 || L > p.N;
-    __syncthreads();
-    if (tid < min(L, p.N)) {
-        const int par = p.parent ? __ldg(p.parent + (size_t)b * p.N + tid) : tid - 1;
-        sh.par[tid] = par;
-        if (par < -1 || par >= tid) sh.bad = 1;
+    Place at{(int)(blockIdx.x / p.S) / (p.hk * p.groups), (int)(blockIdx.x / p.S) % (p.hk * p.groups), 0};
+    int left = 1 << 30;   // blocks of this CTA's range
+    if (p.part) {
+        const int all = all_blocks(p, sh.scan), per = (all + gridDim.x - 1) / gridDim.x;
+        left = min(per, all - (int)min((int64_t)blockIdx.x * per, (int64_t)all));
+        if (left == 0) return;
+        at = find_block(p, blockIdx.x * per, sh.scan);
     }
-    __syncthreads();
-    if (sh.bad) {   // the whole cluster sees the same: nobody waits for it
+  for (bool again = true; again;) {
+    const int b = at.b, h = at.unit / p.groups, col0 = at.unit % p.groups * COLS, cols = min(COLS, p.N * p.G - col0);
+    // ---- everything that depends on nothing, at once: lengths, parents, queries
+    const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b), L = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
+    const int par = tid < p.N && p.parent ? __ldg(p.parent + (size_t)b * p.N + tid) : tid - 1;
+    float4 q[COLS / WARPS];
+#pragma unroll
+    for (int i = 0; i < COLS / WARPS; ++i) {
+        const int col = warp + i * WARPS, node = (col0 + col) / p.G, x = h * p.G + (col0 + col) % p.G;
+        q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (col < cols) q[i] = __ldg(reinterpret_cast<const float4*>(p.q + (((size_t)b * p.N + node) * p.hq + x) * RD) + lane);
+    }
+    const bool lengths = R >= 0 && R <= p.ref.cap && n >= 0 && L >= 0 && L <= p.N;
+    if (tid < p.N) sh.par[tid] = par;
+    const bool bad = __syncthreads_or(!lengths || (tid < L && (par < -1 || par >= tid)));
+    // ---- this CTA's blocks of the unit; its first ones are on their way while the query is prepared
+    const int nref = bad ? 0 : (R + BLK - 1) / BLK, nring = bad ? 0 : (min(n, RW) + BLK - 1) / BLK, nblk = nref + nring;
+    const int whole = p.part ? sequence_blocks(p, b) : nblk;   // of the unit, as the ranges count it
+    const int first = at.block, last = min(whole, first + min(left, whole)), stride = p.S * WARPS;
+    const bool head = first == 0, complete = head && last == whole;
+    const bool dead = bad || col0 / p.G >= L;   // nothing to compute, for the whole cluster
+    if (bad && head) {
         const int live = L < 0 || L > p.N ? p.N : L;
         for (int col = rank; col < cols; col += p.S) {
             const int node = (col0 + col) / p.G;
             if (node < live)
                 p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = __int_as_float(0x7fc00000);
         }
-        return;
     }
-    if (col0 / p.G >= L) return;   // no live node in this group, in any CTA of the cluster
-
-    // the warp's blocks: rank * WARPS + warp, then every S * WARPS-th
-    const int nref = (R + BLK - 1) / BLK, nring = (min(n, RW) + BLK - 1) / BLK, nblk = nref + nring;
+    if (!dead) {
+    const int end = min(last, nblk);
     const size_t ref0 = ((size_t)b * p.hk + h) * p.ref.cap, ring0 = ((size_t)b * p.hk + h) * RW;
     auto block_at = [&](int i) {
         Block x;
         const bool ring = i >= nref;
         const KvView& v = ring ? p.ring : p.ref;
-        const int first = (ring ? i - nref : i) * BLK;
-        const size_t row = (ring ? ring0 : ref0) + first;
+        const int from = (ring ? i - nref : i) * BLK;
+        const size_t row = (ring ? ring0 : ref0) + from;
         x.k = v.k + row * St::ROW, x.v = v.v + row * St::ROW, x.ks = v.ks + row, x.vs = v.vs + row;
-        x.rows = min(BLK, (ring ? min(n, RW) : R) - first);
-        x.ring_slot = ring ? first : -1;
+        x.rows = min(BLK, (ring ? min(n, RW) : R) - from);
+        x.ring_slot = ring ? from : -1;
         return x;
     };
-    int blk = rank * WARPS + warp;
+    int blk = first + rank * WARPS + warp;
     Block cur{};
-    if (blk < nblk) {
+    if (blk < end) {
         cur = block_at(blk);
         load_codes<INT4>(st, cur.k, cur.rows, false, lane);
         load_scales(st + St::KS, cur.ks, cur.rows, lane);
         load_scales(st + St::VS, cur.vs, cur.rows, lane);
     }
     cp_commit();
-    if (blk < nblk) load_codes<INT4>(st + St::V, cur.v, cur.rows, true, lane);
+    if (blk < end) load_codes<INT4>(st + St::V, cur.v, cur.rows, true, lane);
     cp_commit();
 
     // ---- lines of the tree
@@ -243,17 +319,18 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
     }
     __syncthreads();
     // ---- query digits and per-column constants; the drafted keys' part
-    for (int col = warp; col < COLS; col += WARPS) {
-        const int node = (col0 + col) / p.G, x = h * p.G + (col0 + col) % p.G;
+#pragma unroll 1
+    for (int i = 0; i < COLS / WARPS; ++i) {
+        const int col = warp + i * WARPS, node = (col0 + col) / p.G;
         const bool live = col < cols && node < L;
-        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live) q = __ldg(reinterpret_cast<const float4*>(p.q + (((size_t)b * p.N + node) * p.hq + x) * RD) + lane);
-        float a = fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w)));
+        float4 x = i == 0 ? q[0] : i == 1 ? q[1] : i == 2 ? q[2] : q[3];
+        if (!live) x = make_float4(0.f, 0.f, 0.f, 0.f);
+        float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
         a = fmaxf(a, TINY);
         const float inv = Q_TOP / a;
-        const int f[4] = {__float2int_rn(q.x * inv), __float2int_rn(q.y * inv), __float2int_rn(q.z * inv), __float2int_rn(q.w * inv)};
+        const int f[4] = {__float2int_rn(x.x * inv), __float2int_rn(x.y * inv), __float2int_rn(x.z * inv), __float2int_rn(x.w * inv)};
         const int tl = (col & 7) * 4, hi = col >> 3;
 #pragma unroll
         for (int d = 0; d < 3; ++d) {
@@ -272,22 +349,49 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
             sh.step[col] = a / Q_TOP * (SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
             sh.ages[col] = live ? min(n, RW - __popcll(sh.line[node])) : 0;
         }
-        // a CTA of the cluster takes every S-th column's line
+        // The CTA that has the unit's first block has the drafted keys; a CTA of a cluster takes every S-th column's
+        // line.  Four keys at a time.
         float m = NONE, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live && col % p.S == rank) {
+        if (live && head && col % p.S == rank) {
             const float k2 = SCALE * LOG2E;
-            const float4 qs = make_float4(q.x * k2, q.y * k2, q.z * k2, q.w * k2);
-            for (unsigned long long line = sh.line[node]; line; line &= line - 1) {
-                const size_t r = (((size_t)b * p.N + __ffsll(line) - 1) * p.hk + h) * (RD / 4) + lane;
-                const float4 kk = __ldg(reinterpret_cast<const float4*>(p.k_new) + r);
-                const float4 vv = __ldg(reinterpret_cast<const float4*>(p.v_new) + r);
-                float s = qs.x * kk.x + qs.y * kk.y + qs.z * kk.z + qs.w * kk.w;
+            const float4 qs = make_float4(x.x * k2, x.y * k2, x.z * k2, x.w * k2);
+            for (unsigned long long line = sh.line[node]; line;) {
+                float4 kk[4], vv[4];
+                float sc[4];
 #pragma unroll
-                for (int i = 16; i >= 1; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-                const float mn = fmaxf(m, s), al = ex2(m - mn), w = ex2(s - mn);
-                l = l * al + w;
-                o.x = o.x * al + w * vv.x, o.y = o.y * al + w * vv.y, o.z = o.z * al + w * vv.z, o.w = o.w * al + w * vv.w;
+                for (int j = 0; j < 4; ++j) {
+                    sc[j] = line ? 0.f : -INFINITY;
+                    if (line) {
+                        const size_t r = (((size_t)b * p.N + __ffsll(line) - 1) * p.hk + h) * (RD / 4) + lane;
+                        kk[j] = __ldg(reinterpret_cast<const float4*>(p.k_new) + r);
+                        vv[j] = __ldg(reinterpret_cast<const float4*>(p.v_new) + r);
+                    } else {
+                        kk[j] = vv[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                    line &= line - 1;
+                }
+                float dot[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dot[j] = qs.x * kk[j].x + qs.y * kk[j].y + qs.z * kk[j].z + qs.w * kk[j].w;
+#pragma unroll
+                for (int e = 16; e >= 1; e >>= 1)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], e);
+                float mn = m;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sc[j] += dot[j];
+                    mn = fmaxf(mn, sc[j]);
+                }
+                const float al = ex2(m - mn);
+                l *= al, o.x *= al, o.y *= al, o.z *= al, o.w *= al;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float w = ex2(sc[j] - mn);
+                    l += w;
+                    o.x = fmaf(w, vv[j].x, o.x), o.y = fmaf(w, vv[j].y, o.y), o.z = fmaf(w, vv[j].z, o.z), o.w = fmaf(w, vv[j].w, o.w);
+                }
                 m = mn;
             }
         }
@@ -310,14 +414,15 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         run_m[e] = NONE, run_l[e] = 0.f;
         step[e] = sh.step[gr + 8 * e], ages[e] = sh.ages[gr + 8 * e];
     }
-    for (; blk < nblk; blk += p.S * WARPS) {
+    for (; blk < end; blk += stride) {
         cp_wait1();
         __syncwarp();
         // scores, without the column's step: T[j][..] for keys 8 j + 2 c, + 1
         float T[8][W16 ? 4 : 2], vs[8][2];
-        const bool whole = cur.rows == BLK && cur.ring_slot < 0;
+        const bool unmasked = cur.rows == BLK && cur.ring_slot < 0;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+            __syncwarp();   // keeps the second half's loads from being drawn ahead of the first half's use of registers
             int acc[4][3][4];
             uint32_t kb[4][8];
 #pragma unroll
@@ -364,7 +469,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
 #pragma unroll
                 for (int i = 0; i < (W16 ? 4 : 2); ++i)
                     T[jj][i] = (upper(acc[j][2][i]) + lower(acc[j][1][i], acc[j][0][i])) * (i & 1 ? ks.y : ks.x);
-                if (!whole) {
+                if (!unmasked) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const bool in = key + i < cur.rows;
@@ -380,9 +485,9 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         }
         __syncwarp();
         // the next block's K and scales take this block's place
-        const int next = blk + p.S * WARPS;
+        const int next = blk + stride;
         Block nxt{};
-        if (next < nblk) {
+        if (next < end) {
             nxt = block_at(next);
             load_codes<INT4>(st, nxt.k, nxt.rows, false, lane);
             load_scales(st + St::KS, nxt.ks, nxt.rows, lane);
@@ -489,7 +594,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
                 }
             }
         __syncwarp();
-        if (next < nblk) load_codes<INT4>(st + St::V, nxt.v, nxt.rows, true, lane);
+        if (next < end) load_codes<INT4>(st + St::V, nxt.v, nxt.rows, true, lane);
         cp_commit();
         bool moved = false;   // a new maximum rescales what there is; mostly there is none
 #pragma unroll
@@ -541,58 +646,138 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
             l = fmaf(g, sh.warp_l[w][col], l);
             o = fmaf(g, reinterpret_cast<const float*>(smem + w * St::BYTES)[col * PAD + (tid & 15) * 8 + (tid >> 4)], o);
         }
-        if (p.S == 1) {
+        if (p.S == 1 && complete) {
             const int node = (col0 + col) / p.G;
             if (node < L) p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = o / l;
+        } else if (p.S == 1) {
+            float* mine = p.part + ((size_t)blockIdx.x * 2 + head) * PART_FLOATS;
+            mine[PART_O + col * RD + tid] = o;
+            if (tid == 0) mine[col] = M, mine[PART_L + col] = l;
         } else {
             sh.part[col][tid] = o;
             __syncthreads();   // everybody has read the column's old maximum and sum
             if (tid == 0) sh.part_m[col] = M, sh.part_l[col] = l;
         }
     }
-    if (p.S == 1) return;
-    // ---- join the CTAs of the cluster: each takes every S-th column
-    cluster_sync();
-    for (int col = rank; col < cols; col += p.S) {
+    if (p.S > 1) {
+        // ---- join the CTAs of the cluster: each takes every S-th column
+        cluster_sync();
+        for (int col = rank; col < cols; col += p.S) {
+            const int node = (col0 + col) / p.G;
+            if (node >= L) continue;
+            float M = NONE, l = 0.f, o = 0.f;
+            for (int r = 0; r < p.S; ++r) M = fmaxf(M, ld_cluster(&sh.part_m[col], r));
+            for (int r = 0; r < p.S; ++r) {
+                const float f = ex2(ld_cluster(&sh.part_m[col], r) - M);
+                l = fmaf(f, ld_cluster(&sh.part_l[col], r), l);
+                o = fmaf(f, ld_cluster(&sh.part[col][tid], r), o);
+            }
+            p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = o / l;
+        }
+        cluster_sync();   // no CTA leaves while another reads its shared memory
+    }
+    }
+    // ---- the range's next unit
+    left -= last - first;
+    again = p.part && left > 0;
+    at.block = 0;
+    if (++at.unit == p.hk * p.groups) at.unit = 0, ++at.b;
+    __syncthreads();
+  }
+}
+
+// Joins the partial results of the units that the ranges' cuts divide.
+__global__ void __launch_bounds__(PT) rswa_tree_join_kernel(const __grid_constant__ TreeParams p, int ctas) {
+    __shared__ int scan[WARPS + 4];
+    const int tid = threadIdx.x, per_b = p.hk * p.groups, b = blockIdx.x / per_b, unit = blockIdx.x % per_b;
+    pdl_wait();
+    // the unit's blocks in the row of all blocks, and the CTAs that had them
+    int all = 0, before = 0;
+    for (int i = tid; i < p.B; i += PT) {
+        const int own = sequence_blocks(p, i);
+        all += own;
+        if (i < b) before += own;
+    }
+    all = cta_scan(all, scan) * per_b;
+    before = cta_scan(before, scan);
+    const int own = sequence_blocks(p, b), per = (all + ctas - 1) / ctas;
+    const int64_t from = (int64_t)before * per_b + (int64_t)unit * own;
+    const int c0 = (int)(from / per), c1 = (int)((from + own - 1) / per);
+    const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b), L = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
+    const int par = tid < p.N && p.parent ? __ldg(p.parent + (size_t)b * p.N + tid) : tid - 1;
+    const bool bad = __syncthreads_or(R < 0 || R > p.ref.cap || n < 0 || L < 0 || L > p.N || (tid < L && (par < -1 || par >= tid)));
+    if (bad || c0 == c1) return;
+    const int h = unit / p.groups, col0 = unit % p.groups * COLS, cols = min(COLS, p.N * p.G - col0);
+    for (int col = blockIdx.y; col < cols; col += gridDim.y) {
         const int node = (col0 + col) / p.G;
-        if (node >= L) continue;
+        if (node >= L) return;
         float M = NONE, l = 0.f, o = 0.f;
-        for (int r = 0; r < p.S; ++r) M = fmaxf(M, ld_cluster(&sh.part_m[col], r));
-        for (int r = 0; r < p.S; ++r) {
-            const float f = ex2(ld_cluster(&sh.part_m[col], r) - M);
-            l = fmaf(f, ld_cluster(&sh.part_l[col], r), l);
-            o = fmaf(f, ld_cluster(&sh.part[col][tid], r), o);
+        for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part + ((size_t)c * 2 + (c == c0)) * PART_FLOATS + col));
+        for (int c = c0; c <= c1; ++c) {
+            const float* part = p.part + ((size_t)c * 2 + (c == c0)) * PART_FLOATS;
+            const float f = ex2(__ldcg(part + col) - M);
+            l = fmaf(f, __ldcg(part + PART_L + col), l);
+            o = fmaf(f, __ldcg(part + PART_O + col * RD + tid), o);
         }
         p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = o / l;
     }
-    cluster_sync();   // no CTA leaves while another reads its shared memory
+}
+
+// How a call is split, from its sizes alone: ranges once a cluster for each unit would not fit the device at once.
+struct TreePlan {
+    int groups, S, ctas;   // ctas: of the ranges, or 0 for clusters
+};
+TreePlan tree_plan(int B, int N, int heads_q, int heads, int cap) {
+    const int sms = device_sms() > 0 ? device_sms() : 148, resident = 2 * sms;
+    TreePlan pl;
+    pl.groups = (N * (heads_q / heads) + COLS - 1) / COLS;
+    const int64_t units = (int64_t)B * heads * pl.groups;
+    const int blocks = (cap + BLK - 1) / BLK + RW / BLK;
+    pl.S = 1;
+    while (pl.S < 8 && pl.S * WARPS < blocks) pl.S *= 2;
+    pl.ctas = 0;
+    while (pl.S > 1 && units * pl.S > resident) pl.S /= 2;
+    // two blocks a warp and more: cut all of it evenly instead
+    if (blocks > 2 * pl.S * WARPS) pl.S = 1, pl.ctas = resident;
+    return pl;
 }
 
 template <bool INT4, bool W16>
-cudaError_t launch_tree(TreeParams& p, int B, cudaStream_t st) {
+cudaError_t launch_tree(TreeParams& p, const TreePlan& pl, cudaStream_t st) {
     const void* fn = (const void*)rswa_tree_kernel<INT4, W16>;
     const size_t smem = WARPS * Stage<INT4>::BYTES + sizeof(Shared);
     cudaError_t e = once_per_device(fn, [&] {
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess) return e;
-    p.groups = (p.N * p.G + COLS - 1) / COLS;
-    // enough CTAs for two per SM several times over, at least one block a warp
-    const int sms = device_sms() > 0 ? device_sms() : 148, units = B * p.hk * p.groups;
-    const int blocks = (p.ref.cap + BLK - 1) / BLK + RW / BLK;
-    p.S = 1;
-    while (p.S < 8 && units * p.S < 8 * sms && p.S * WARPS < blocks) p.S *= 2;
+    p.groups = pl.groups, p.S = pl.S;
+    const unsigned units = (unsigned)p.B * p.hk * p.groups;
     void* args[] = {&p};
-    return launch_kernel(fn, dim3((unsigned)(units * p.S)), dim3(PT), smem, p.S, args, st);
+    if (!pl.ctas) return launch_kernel(fn, dim3(units * p.S), dim3(PT), smem, p.S, args, st);
+    e = launch_kernel(fn, dim3((unsigned)pl.ctas), dim3(PT), smem, 1, args, st);
+    if (e != cudaSuccess) return e;
+    int ctas = pl.ctas;
+    void* more[] = {&p, &ctas};
+    const int cols = p.N * p.G < COLS ? p.N * p.G : COLS;
+    return launch_kernel((const void*)rswa_tree_join_kernel, dim3(units, cols < 4 ? cols : 4), dim3(PT), 0, 1, more, st);
 }
 
 }  // namespace
 }  // namespace focr
 
+extern "C" size_t focr_rswa_tree_workspace_bytes(int32_t B, int32_t N, int32_t heads_q, int32_t heads, int32_t ref_cap) {
+    using namespace focr;
+    if (B < 1 || N < 1 || heads < 1 || heads_q < heads || heads_q > FOCR_HEADS_MAX || B > FOCR_RSWA_B_MAX ||
+        ref_cap > FOCR_RSWA_RCAP_MAX || N > TREE_MAX)
+        return 0;
+    const TreePlan pl = tree_plan(B, N, heads_q, heads, ref_cap);
+    return ((size_t)pl.ctas * 2 * PART_FLOATS * sizeof(float) + 255) & ~(size_t)255;
+}
+
 extern "C" focr_status focr_rswa_tree(const float* q, const float* k_new, const float* v_new, int32_t B, int32_t N,
                                       int32_t heads_q, const focr_kv_cache* ref, const int32_t* ref_len,
                                       const focr_kv_cache* ring, const int32_t* n_gen, const int32_t* parent,
-                                      const int32_t* n_nodes, float* out, void* stream) {
+                                      const int32_t* n_nodes, float* out, void* workspace, size_t ws_bytes, void* stream) {
     using namespace focr;
     report_error(FOCR_OK, "");
     TreeParams p;
@@ -619,10 +804,15 @@ extern "C" focr_status focr_rswa_tree(const float* q, const float* k_new, const 
     if (ranges_overlap(out, qb, q, qb) || ranges_overlap(out, qb, k_new, kb) || ranges_overlap(out, qb, v_new, kb))
         return report_error(FOCR_ERR_INVALID_ARG, "out overlaps an input");
     p.q = q, p.k_new = k_new, p.v_new = v_new, p.ref_len = ref_len, p.n_gen = n_gen, p.parent = parent, p.n_nodes = n_nodes;
-    p.out = out, p.N = N, p.hq = heads_q, p.hk = ref->heads, p.G = G;
+    const TreePlan pl = tree_plan(B, N, heads_q, ref->heads, ref->cap);
+    const size_t need = focr_rswa_tree_workspace_bytes(B, N, heads_q, ref->heads, ref->cap);
+    if (need && (!workspace || misaligned(workspace, 256) || ws_bytes < need))
+        return reportf(FOCR_ERR_INVALID_ARG, "workspace of %zu bytes (256-byte aligned) is needed, got %zu", need, ws_bytes);
+    p.out = out, p.B = B, p.N = N, p.hq = heads_q, p.hk = ref->heads, p.G = G;
+    p.part = pl.ctas ? reinterpret_cast<float*>(workspace) : nullptr;
     const bool wide = N * G > 8, int4 = ref->type == FOCR_W_INT4;
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = int4 ? (wide ? launch_tree<true, true>(p, B, st) : launch_tree<true, false>(p, B, st))
-                               : (wide ? launch_tree<false, true>(p, B, st) : launch_tree<false, false>(p, B, st));
+    const cudaError_t e = int4 ? (wide ? launch_tree<true, true>(p, pl, st) : launch_tree<true, false>(p, pl, st))
+                               : (wide ? launch_tree<false, true>(p, pl, st) : launch_tree<false, false>(p, pl, st));
     return report_launch(e, "rswa_tree_kernel");
 }
