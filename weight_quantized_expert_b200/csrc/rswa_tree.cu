@@ -48,7 +48,7 @@ constexpr int RD = FOCR_RSWA_DIM, RW = FOCR_RSWA_RING;
 constexpr int TREE_MAX = FOCR_TREE_NODES_MAX;
 constexpr int COLS = 16;                        // columns of a CTA: the rows of one MMA tile
 constexpr int BLK = 64;                         // keys of a block
-constexpr int WARPS = 4, PT = 32 * WARPS;
+constexpr int JT = 128;                         // threads of the joining kernel
 constexpr int PAD = RD + 8;                     // floats per row of a warp's partial output: no bank conflicts
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float SCALE = 0.08838834764831845f;   // 1 / sqrt(128)
@@ -77,11 +77,12 @@ struct Stage {   // a warp's part of shared memory: one block of keys; later its
     static constexpr int BYTES = LOADS > COLS * PAD * 4 ? LOADS : COLS * PAD * 4;
 };
 
+template <int WARPS>
 struct Shared {
     uint4 qf[4 * 3][32];               // query digits as A fragments: [k-step * 3 + digit][lane]
     float part[COLS][RD];              // the drafted keys' part, then the CTA's
     float part_m[COLS], part_l[COLS];
-    float warp_m[WARPS][COLS], warp_l[WARPS][COLS];
+    float warp_m[WARPS][COLS], warp_l[WARPS][COLS], warp_f[WARPS + 1][COLS];   // f: a part's factor (the last: drafted keys)
     float step[COLS];                  // a score in units of log2 is (integer dot) * key scale * step
     int ages[COLS];                    // ring slots younger than this are seen (0 for a column without a node)
     unsigned long long line[TREE_MAX];
@@ -99,6 +100,7 @@ struct Place {   // a block in the row of all units' blocks
     int b, unit, block;   // sequence, unit of the sequence, block of the unit
 };
 // Sums over all threads of the CTA; the threads' inclusive prefix in `mine`.
+template <int WARPS>
 __device__ __forceinline__ int cta_scan(int& mine, int* scan) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -118,19 +120,21 @@ __device__ __forceinline__ int cta_scan(int& mine, int* scan) {
     return total;
 }
 // All blocks of the call.
+template <int WARPS>
 __device__ int all_blocks(const TreeParams& p, int* scan) {
     int mine = 0;
-    for (int b = threadIdx.x; b < p.B; b += PT) mine += sequence_blocks(p, b);
-    return cta_scan(mine, scan) * p.hk * p.groups;
+    for (int b = threadIdx.x; b < p.B; b += 32 * WARPS) mine += sequence_blocks(p, b);
+    return cta_scan<WARPS>(mine, scan) * p.hk * p.groups;
 }
 // Where block `at` of the row is.
+template <int WARPS>
 __device__ Place find_block(const TreeParams& p, int at, int* scan) {
     const int per = p.hk * p.groups;
     int before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += PT) {
+    for (int b0 = 0; b0 < p.B; b0 += 32 * WARPS) {
         const int b = b0 + threadIdx.x, own = b < p.B ? sequence_blocks(p, b) : 0;
         int sum = own;
-        const int total = cta_scan(sum, scan);
+        const int total = cta_scan<WARPS>(sum, scan);
         if ((int64_t)(before + total) * per > at) {
             const int64_t first = (int64_t)(before + sum - own) * per;
             if (at >= first && at < first + (int64_t)own * per) scan[WARPS] = b, scan[WARPS + 1] = (int)(at - first), scan[WARPS + 2] = own;
@@ -238,11 +242,12 @@ __device__ __forceinline__ void load_scales(uint32_t dst, const float* src, int 
 }
 
 // W16: more than eight columns, so both row halves of the MMA tiles are used.
-template <bool INT4, bool W16>
-__global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant__ TreeParams p) {
+template <bool INT4, bool W16, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 12 / WARPS > 2 ? 2 : 1) rswa_tree_kernel(const __grid_constant__ TreeParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     using St = Stage<INT4>;
-    Shared& sh = *reinterpret_cast<Shared*>(smem + WARPS * St::BYTES);
+    constexpr int PT = 32 * WARPS, MINE = (COLS + WARPS - 1) / WARPS;   // MINE: columns a warp prepares
+    Shared<WARPS>& sh = *reinterpret_cast<Shared<WARPS>*>(smem + WARPS * St::BYTES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, c = lane & 3;
     const int rank = p.S > 1 ? (int)cluster_rank() : 0;
     uint8_t* stage = smem + warp * St::BYTES;
@@ -251,19 +256,19 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
     Place at{(int)(blockIdx.x / p.S) / (p.hk * p.groups), (int)(blockIdx.x / p.S) % (p.hk * p.groups), 0};
     int left = 1 << 30;   // blocks of this CTA's range
     if (p.part) {
-        const int all = all_blocks(p, sh.scan), per = (all + gridDim.x - 1) / gridDim.x;
+        const int all = all_blocks<WARPS>(p, sh.scan), per = (all + gridDim.x - 1) / gridDim.x;
         left = min(per, all - (int)min((int64_t)blockIdx.x * per, (int64_t)all));
         if (left == 0) return;
-        at = find_block(p, blockIdx.x * per, sh.scan);
+        at = find_block<WARPS>(p, blockIdx.x * per, sh.scan);
     }
   for (bool again = true; again;) {
     const int b = at.b, h = at.unit / p.groups, col0 = at.unit % p.groups * COLS, cols = min(COLS, p.N * p.G - col0);
     // ---- everything that depends on nothing, at once: lengths, parents, queries
     const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b), L = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
     const int par = tid < p.N && p.parent ? __ldg(p.parent + (size_t)b * p.N + tid) : tid - 1;
-    float4 q[COLS / WARPS];
+    float4 q[MINE];
 #pragma unroll
-    for (int i = 0; i < COLS / WARPS; ++i) {
+    for (int i = 0; i < MINE; ++i) {
         const int col = warp + i * WARPS, node = (col0 + col) / p.G, x = h * p.G + (col0 + col) % p.G;
         q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (col < cols) q[i] = __ldg(reinterpret_cast<const float4*>(p.q + (((size_t)b * p.N + node) * p.hq + x) * RD) + lane);
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         const int live = L < 0 || L > p.N ? p.N : L;
         for (int col = rank; col < cols; col += p.S) {
             const int node = (col0 + col) / p.G;
-            if (node < live)
+            if (node < live && tid < RD)
                 p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = __int_as_float(0x7fc00000);
         }
     }
@@ -318,13 +323,37 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         sh.line[tid] = line;
     }
     __syncthreads();
-    // ---- query digits and per-column constants; the drafted keys' part
-#pragma unroll 1
-    for (int i = 0; i < COLS / WARPS; ++i) {
+    // ---- query digits, per-column constants, and the drafted keys' part: the CTA that has the unit's first block has
+    // them, in a cluster every S-th column's.  Four keys at a time; the first four of all columns are loaded at once.
+    unsigned long long line[MINE];
+    float4 kk[MINE][4], vv[MINE][4];
+    auto draft_load = [&](unsigned long long& rest, float4 (&k4)[4], float4 (&v4)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            k4[j] = v4[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (rest) {
+                const size_t r = (((size_t)b * p.N + __ffsll(rest) - 1) * p.hk + h) * (RD / 4) + lane;
+                k4[j] = __ldg(reinterpret_cast<const float4*>(p.k_new) + r);
+                v4[j] = __ldg(reinterpret_cast<const float4*>(p.v_new) + r);
+            }
+            rest &= rest - 1;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
         const int col = warp + i * WARPS, node = (col0 + col) / p.G;
         const bool live = col < cols && node < L;
-        float4 x = i == 0 ? q[0] : i == 1 ? q[1] : i == 2 ? q[2] : q[3];
-        if (!live) x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!live) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        line[i] = live && head && col % p.S == rank ? sh.line[node] : 0ull;
+        unsigned long long rest = line[i];
+        draft_load(rest, kk[i], vv[i]);
+        if (lane == 0 && col < COLS) sh.ages[col] = live ? min(n, RW - __popcll(sh.line[node])) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+        const int col = warp + i * WARPS;
+        if (col >= COLS) break;
+        const float4 x = q[i];
         float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
@@ -345,54 +374,40 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
                 reinterpret_cast<uint32_t*>(&sh.qf[s * 3 + d][tl + cc])[2 * (lane & 1) + hi] = v0 | v1 << 8 | v2 << 16 | v3 << 24;
             }
         }
-        if (lane == 0) {
-            sh.step[col] = a / Q_TOP * (SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
-            sh.ages[col] = live ? min(n, RW - __popcll(sh.line[node])) : 0;
-        }
-        // The CTA that has the unit's first block has the drafted keys; a CTA of a cluster takes every S-th column's
-        // line.  Four keys at a time.
+        if (lane == 0) sh.step[col] = a / Q_TOP * (SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
         float m = NONE, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live && head && col % p.S == rank) {
-            const float k2 = SCALE * LOG2E;
-            const float4 qs = make_float4(x.x * k2, x.y * k2, x.z * k2, x.w * k2);
-            for (unsigned long long line = sh.line[node]; line;) {
-                float4 kk[4], vv[4];
-                float sc[4];
+        const float k2 = SCALE * LOG2E;
+        const float4 qs = make_float4(x.x * k2, x.y * k2, x.z * k2, x.w * k2);
+        for (bool more = line[i] != 0; more;) {
+            float sc[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sc[j] = line ? 0.f : -INFINITY;
-                    if (line) {
-                        const size_t r = (((size_t)b * p.N + __ffsll(line) - 1) * p.hk + h) * (RD / 4) + lane;
-                        kk[j] = __ldg(reinterpret_cast<const float4*>(p.k_new) + r);
-                        vv[j] = __ldg(reinterpret_cast<const float4*>(p.v_new) + r);
-                    } else {
-                        kk[j] = vv[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-                    line &= line - 1;
-                }
-                float dot[4];
+            for (int j = 0; j < 4; ++j) sc[j] = qs.x * kk[i][j].x + qs.y * kk[i][j].y + qs.z * kk[i][j].z + qs.w * kk[i][j].w;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) dot[j] = qs.x * kk[j].x + qs.y * kk[j].y + qs.z * kk[j].z + qs.w * kk[j].w;
+            for (int e = 16; e >= 1; e >>= 1)
 #pragma unroll
-                for (int e = 16; e >= 1; e >>= 1)
+                for (int j = 0; j < 4; ++j) sc[j] += __shfl_xor_sync(0xffffffffu, sc[j], e);
+            float mn = m;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], e);
-                float mn = m;
+            for (int j = 0; j < 4; ++j) {
+                if (!line[i]) sc[j] = -INFINITY;
+                line[i] &= line[i] - 1;
+                mn = fmaxf(mn, sc[j]);
+            }
+            const float al = ex2(m - mn);
+            l *= al, o.x *= al, o.y *= al, o.z *= al, o.w *= al;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sc[j] += dot[j];
-                    mn = fmaxf(mn, sc[j]);
-                }
-                const float al = ex2(m - mn);
-                l *= al, o.x *= al, o.y *= al, o.z *= al, o.w *= al;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float w = ex2(sc[j] - mn);
-                    l += w;
-                    o.x = fmaf(w, vv[j].x, o.x), o.y = fmaf(w, vv[j].y, o.y), o.z = fmaf(w, vv[j].z, o.z), o.w = fmaf(w, vv[j].w, o.w);
-                }
-                m = mn;
+            for (int j = 0; j < 4; ++j) {
+                const float w = ex2(sc[j] - mn);
+                const float4 v = vv[i][j];
+                l += w;
+                o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+            }
+            m = mn;
+            more = line[i] != 0;
+            if (more) {
+                unsigned long long rest = line[i];
+                draft_load(rest, kk[i], vv[i]);
             }
         }
         reinterpret_cast<float4*>(sh.part[col])[lane] = o;
@@ -553,49 +568,38 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         }
         cp_wait1();
         __syncwarp();
-        // values: dim 16 g + t of tile t, from the bytes of the lane's sixteen keys
-        uint32_t vb[2][16][2];
+        // values: dim 16 gr + t of tile t, from the bytes of the lane's sixteen keys; eight tiles at a time
+        auto load_values = [&](int dh, uint32_t (&vb)[2][8][2]) {
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+            for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int r0 = 32 * kk + 16 * g + 2 * c;
-                if (INT4) {
-                    uint2 w[4];
+                for (int g = 0; g < 2; ++g) {
+                    const int r0 = 32 * kk + 16 * g + 2 * c;
+                    uint32_t o[4];
+                    if (INT4) {
+                        uint32_t w[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r0 + (i & 1) + 8 * (i >> 1);
-                        w[i] = *reinterpret_cast<const uint2*>(stage + St::V + v_off<true>(r, gr >> 1) + (gr & 1) * 8);
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = r0 + (i & 1) + 8 * (i >> 1);
+                            w[i] = *reinterpret_cast<const uint32_t*>(stage + St::V + v_off<true>(r, gr >> 1) + (gr & 1) * 8 + 4 * dh);
+                        }
+                        transpose4(w[0], w[1], w[2], w[3], o);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) vb[kk][2 * i][g] = (o[i] << 4) & 0xF0F0F0F0u, vb[kk][2 * i + 1][g] = o[i] & 0xF0F0F0F0u;
+                    } else {
+                        uint2 w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = *reinterpret_cast<const uint2*>(stage + St::V + v_off<false>(r0 + (i & 1) + 8 * (i >> 1), gr) + 8 * dh);
+                        transpose4(w[0].x, w[1].x, w[2].x, w[3].x, o);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) vb[kk][i][g] = o[i];
+                        transpose4(w[0].y, w[1].y, w[2].y, w[3].y, o);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) vb[kk][4 + i][g] = o[i];
                     }
-                    uint32_t o[4];
-                    transpose4(w[0].x, w[1].x, w[2].x, w[3].x, o);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) vb[kk][2 * i][g] = (o[i] << 4) & 0xF0F0F0F0u, vb[kk][2 * i + 1][g] = o[i] & 0xF0F0F0F0u;
-                    transpose4(w[0].y, w[1].y, w[2].y, w[3].y, o);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) vb[kk][8 + 2 * i][g] = (o[i] << 4) & 0xF0F0F0F0u, vb[kk][8 + 2 * i + 1][g] = o[i] & 0xF0F0F0F0u;
-                } else {
-                    uint4 w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = lds128(stage + St::V + v_off<false>(r0 + (i & 1) + 8 * (i >> 1), gr));
-                    uint32_t o[4];
-                    transpose4(w[0].x, w[1].x, w[2].x, w[3].x, o);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) vb[kk][i][g] = o[i];
-                    transpose4(w[0].y, w[1].y, w[2].y, w[3].y, o);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) vb[kk][4 + i][g] = o[i];
-                    transpose4(w[0].z, w[1].z, w[2].z, w[3].z, o);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) vb[kk][8 + i][g] = o[i];
-                    transpose4(w[0].w, w[1].w, w[2].w, w[3].w, o);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) vb[kk][12 + i][g] = o[i];
                 }
-            }
-        __syncwarp();
-        if (next < end) load_codes<INT4>(st + St::V, nxt.v, nxt.rows, true, lane);
-        cp_commit();
+        };
         bool moved = false;   // a new maximum rescales what there is; mostly there is none
 #pragma unroll
         for (int e = 0; e < HALVES; ++e) moved |= alpha[e] != 1.f;
@@ -606,15 +610,25 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
                 for (int i = 0; i < (W16 ? 4 : 2); ++i) O[t][i] *= alpha[i >> 1];
         }
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-            int acc[3][4];
+        for (int dh = 0; dh < 2; ++dh) {
+            uint32_t vb[2][8][2];
+            load_values(dh, vb);
+            __syncwarp();
+            if (dh == 1) {   // the values have been read: the next block's take their place
+                if (next < end) load_codes<INT4>(st + St::V, nxt.v, nxt.rows, true, lane);
+                cp_commit();
+            }
 #pragma unroll
-            for (int d = 0; d < 3; ++d) mma<false, true>(acc[d], pd[0][d], vb[0][t][0], vb[0][t][1]);
+            for (int t = 0; t < 8; ++t) {
+                int acc[3][4];
 #pragma unroll
-            for (int d = 0; d < 3; ++d) mma<false, false>(acc[d], pd[1][d], vb[1][t][0], vb[1][t][1]);
+                for (int d = 0; d < 3; ++d) mma<false, true>(acc[d], pd[0][d], vb[0][t][0], vb[0][t][1]);
 #pragma unroll
-            for (int i = 0; i < (W16 ? 4 : 2); ++i)
-                O[t][i] = fmaf(upper(acc[2][i]), gain[i >> 1], fmaf(lower(acc[1][i], acc[0][i]), gain[i >> 1], O[t][i]));
+                for (int d = 0; d < 3; ++d) mma<false, false>(acc[d], pd[1][d], vb[1][t][0], vb[1][t][1]);
+#pragma unroll
+                for (int i = 0; i < (W16 ? 4 : 2); ++i)
+                    O[8 * dh + t][i] = fmaf(upper(acc[2][i]), gain[i >> 1], fmaf(lower(acc[1][i], acc[0][i]), gain[i >> 1], O[8 * dh + t][i]));
+            }
         }
         cur = nxt;
     }
@@ -634,45 +648,59 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         }
     }
     __syncthreads();
-    for (int col = 0; col < cols; ++col) {
+    float* mine = p.part ? p.part + ((size_t)blockIdx.x * 2 + head) * PART_FLOATS : nullptr;   // ranges' partial result
+    if (tid < cols) {   // a column's maximum, the parts' factors, its sum
+        const int col = tid;
         const float pm = sh.part_m[col];
         float M = pm;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sh.warp_m[w][col]);
-        float f = ex2(pm - M), l = f * sh.part_l[col], o = f * sh.part[col][tid];
+        float f = ex2(pm - M), l = f * sh.part_l[col];
+        sh.warp_f[WARPS][col] = f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
-            const float g = ex2(sh.warp_m[w][col] - M);
-            l = fmaf(g, sh.warp_l[w][col], l);
-            o = fmaf(g, reinterpret_cast<const float*>(smem + w * St::BYTES)[col * PAD + (tid & 15) * 8 + (tid >> 4)], o);
+            f = ex2(sh.warp_m[w][col] - M);
+            sh.warp_f[w][col] = f;
+            l = fmaf(f, sh.warp_l[w][col], l);
         }
-        if (p.S == 1 && complete) {
+        sh.part_m[col] = M, sh.part_l[col] = l;
+        if (p.part && !complete) mine[col] = M, mine[PART_L + col] = l;
+    }
+    __syncthreads();
+    for (int i = tid; i < cols * RD; i += PT) {
+        const int col = i / RD, d = i % RD;
+        float o = sh.warp_f[WARPS][col] * sh.part[col][d];
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w)
+            o = fmaf(sh.warp_f[w][col], reinterpret_cast<const float*>(smem + w * St::BYTES)[col * PAD + (d & 15) * 8 + (d >> 4)], o);
+        if (p.S > 1) {
+            sh.part[col][d] = o;
+        } else if (complete) {
             const int node = (col0 + col) / p.G;
-            if (node < L) p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = o / l;
-        } else if (p.S == 1) {
-            float* mine = p.part + ((size_t)blockIdx.x * 2 + head) * PART_FLOATS;
-            mine[PART_O + col * RD + tid] = o;
-            if (tid == 0) mine[col] = M, mine[PART_L + col] = l;
+            if (node < L) p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + d] = o / sh.part_l[col];
         } else {
-            sh.part[col][tid] = o;
-            __syncthreads();   // everybody has read the column's old maximum and sum
-            if (tid == 0) sh.part_m[col] = M, sh.part_l[col] = l;
+            mine[PART_O + i] = o;
         }
     }
     if (p.S > 1) {
         // ---- join the CTAs of the cluster: each takes every S-th column
         cluster_sync();
-        for (int col = rank; col < cols; col += p.S) {
-            const int node = (col0 + col) / p.G;
+        for (int i = tid; i < (cols - rank + p.S - 1) / p.S * RD; i += PT) {
+            const int col = rank + i / RD * p.S, d = i % RD, node = (col0 + col) / p.G;
             if (node >= L) continue;
-            float M = NONE, l = 0.f, o = 0.f;
-            for (int r = 0; r < p.S; ++r) M = fmaxf(M, ld_cluster(&sh.part_m[col], r));
-            for (int r = 0; r < p.S; ++r) {
-                const float f = ex2(ld_cluster(&sh.part_m[col], r) - M);
-                l = fmaf(f, ld_cluster(&sh.part_l[col], r), l);
-                o = fmaf(f, ld_cluster(&sh.part[col][tid], r), o);
-            }
-            p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = o / l;
+            float m[8], M = NONE, l = 0.f, o = 0.f;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) m[r] = r < p.S ? ld_cluster(&sh.part_m[col], r) : NONE;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) M = fmaxf(M, m[r]);
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < p.S) {
+                    const float f = ex2(m[r] - M);
+                    l = fmaf(f, ld_cluster(&sh.part_l[col], r), l);
+                    o = fmaf(f, ld_cluster(&sh.part[col][d], r), o);
+                }
+            p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + d] = o / l;
         }
         cluster_sync();   // no CTA leaves while another reads its shared memory
     }
@@ -687,19 +715,19 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
 }
 
 // Joins the partial results of the units that the ranges' cuts divide.
-__global__ void __launch_bounds__(PT) rswa_tree_join_kernel(const __grid_constant__ TreeParams p, int ctas) {
-    __shared__ int scan[WARPS + 4];
+__global__ void __launch_bounds__(JT) rswa_tree_join_kernel(const __grid_constant__ TreeParams p, int ctas) {
+    __shared__ int scan[JT / 32 + 4];
     const int tid = threadIdx.x, per_b = p.hk * p.groups, b = blockIdx.x / per_b, unit = blockIdx.x % per_b;
     pdl_wait();
     // the unit's blocks in the row of all blocks, and the CTAs that had them
     int all = 0, before = 0;
-    for (int i = tid; i < p.B; i += PT) {
+    for (int i = tid; i < p.B; i += JT) {
         const int own = sequence_blocks(p, i);
         all += own;
         if (i < b) before += own;
     }
-    all = cta_scan(all, scan) * per_b;
-    before = cta_scan(before, scan);
+    all = cta_scan<JT / 32>(all, scan) * per_b;
+    before = cta_scan<JT / 32>(before, scan);
     const int own = sequence_blocks(p, b), per = (all + ctas - 1) / ctas;
     const int64_t from = (int64_t)before * per_b + (int64_t)unit * own;
     const int c0 = (int)(from / per), c1 = (int)((from + own - 1) / per);
@@ -723,29 +751,30 @@ __global__ void __launch_bounds__(PT) rswa_tree_join_kernel(const __grid_constan
     }
 }
 
-// How a call is split, from its sizes alone: ranges once a cluster for each unit would not fit the device at once.
+// How a call is split, from its sizes alone: clusters of CTAs of four warps (two resident per SM) while all units fit the
+// device at once with two blocks a warp, else ranges, one CTA of twelve warps per SM.
+constexpr int FEW = 4, MANY = 4;
 struct TreePlan {
     int groups, S, ctas;   // ctas: of the ranges, or 0 for clusters
 };
 TreePlan tree_plan(int B, int N, int heads_q, int heads, int cap) {
-    const int sms = device_sms() > 0 ? device_sms() : 148, resident = 2 * sms;
+    const int sms = device_sms() > 0 ? device_sms() : 148;
     TreePlan pl;
     pl.groups = (N * (heads_q / heads) + COLS - 1) / COLS;
     const int64_t units = (int64_t)B * heads * pl.groups;
     const int blocks = (cap + BLK - 1) / BLK + RW / BLK;
     pl.S = 1;
-    while (pl.S < 8 && pl.S * WARPS < blocks) pl.S *= 2;
+    while (pl.S < 8 && pl.S * FEW < blocks) pl.S *= 2;
     pl.ctas = 0;
-    while (pl.S > 1 && units * pl.S > resident) pl.S /= 2;
-    // two blocks a warp and more: cut all of it evenly instead
-    if (blocks > 2 * pl.S * WARPS) pl.S = 1, pl.ctas = resident;
+    while (pl.S > 1 && units * pl.S > 2 * sms) pl.S /= 2;
+    if (blocks > 2 * pl.S * FEW) pl.S = 1, pl.ctas = 2 * sms;
     return pl;
 }
 
-template <bool INT4, bool W16>
+template <bool INT4, bool W16, int WARPS>
 cudaError_t launch_tree(TreeParams& p, const TreePlan& pl, cudaStream_t st) {
-    const void* fn = (const void*)rswa_tree_kernel<INT4, W16>;
-    const size_t smem = WARPS * Stage<INT4>::BYTES + sizeof(Shared);
+    const void* fn = (const void*)rswa_tree_kernel<INT4, W16, WARPS>;
+    const size_t smem = WARPS * Stage<INT4>::BYTES + sizeof(Shared<WARPS>);
     cudaError_t e = once_per_device(fn, [&] {
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
@@ -753,13 +782,17 @@ cudaError_t launch_tree(TreeParams& p, const TreePlan& pl, cudaStream_t st) {
     p.groups = pl.groups, p.S = pl.S;
     const unsigned units = (unsigned)p.B * p.hk * p.groups;
     void* args[] = {&p};
-    if (!pl.ctas) return launch_kernel(fn, dim3(units * p.S), dim3(PT), smem, p.S, args, st);
-    e = launch_kernel(fn, dim3((unsigned)pl.ctas), dim3(PT), smem, 1, args, st);
+    if (!pl.ctas) return launch_kernel(fn, dim3(units * p.S), dim3(32 * WARPS), smem, p.S, args, st);
+    e = launch_kernel(fn, dim3((unsigned)pl.ctas), dim3(32 * WARPS), smem, 1, args, st);
     if (e != cudaSuccess) return e;
     int ctas = pl.ctas;
     void* more[] = {&p, &ctas};
     const int cols = p.N * p.G < COLS ? p.N * p.G : COLS;
-    return launch_kernel((const void*)rswa_tree_join_kernel, dim3(units, cols < 4 ? cols : 4), dim3(PT), 0, 1, more, st);
+    return launch_kernel((const void*)rswa_tree_join_kernel, dim3(units, cols < 4 ? cols : 4), dim3(JT), 0, 1, more, st);
+}
+template <bool INT4, bool W16>
+cudaError_t launch_tree(TreeParams& p, const TreePlan& pl, cudaStream_t st) {
+    return pl.ctas ? launch_tree<INT4, W16, MANY>(p, pl, st) : launch_tree<INT4, W16, FEW>(p, pl, st);
 }
 
 }  // namespace
