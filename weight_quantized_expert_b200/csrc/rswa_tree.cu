@@ -26,8 +26,10 @@
 // Drafted keys and values stay fp32 and are few: a warp takes a column and walks its line on the CUDA cores.
 //
 // Work split: a unit is one kv head of one sequence with up to 16 columns; its keys are blocks of 64 (reference rows,
-// then the ring), which the four warps of a CTA take in turn, each with its own copies in flight (cp.async into its part
-// of shared memory: the next block's K loads while P V runs, its V while Q K runs).  Warps join in shared memory.
+// then the ring), which the four pairs of warps of a CTA take in turn, each with its own copies in flight (cp.async into
+// its part of shared memory: the next block's K loads while P V runs, its V while Q K runs).  In a pair each warp has the
+// scores of half the keys and the values of half the dims, so 128 registers hold its accumulators and four warps per
+// scheduler hide each other's latencies (one warp per block needed 255: two per scheduler, half the issue rate).
 //   few units   a cluster of S CTAs has a unit and joins through distributed shared memory: one launch.
 //   many units  all blocks of all units in one row, cut into equal ranges, one per resident CTA (the lengths are read
 //               on the device, so ragged batches stay balanced); units that a cut divides leave partial results in
@@ -48,6 +50,7 @@ constexpr int RD = FOCR_RSWA_DIM, RW = FOCR_RSWA_RING;
 constexpr int TREE_MAX = FOCR_TREE_NODES_MAX;
 constexpr int COLS = 16;                        // columns of a CTA: the rows of one MMA tile
 constexpr int BLK = 64;                         // keys of a block
+constexpr int WARPS = 8, PAIRS = WARPS / 2, PT = 32 * WARPS;   // two warps work on a block
 constexpr int JT = 128;                         // threads of the joining kernel
 constexpr int PAD = RD + 8;                     // floats per row of a warp's partial output: no bank conflicts
 constexpr float LOG2E = 1.4426950408889634f;
@@ -71,18 +74,19 @@ struct TreeParams {
 constexpr int PART_L = COLS, PART_O = 2 * COLS, PART_FLOATS = 2 * COLS + COLS * RD;
 
 template <bool INT4>
-struct Stage {   // a warp's part of shared memory: one block of keys; later its partial output
+struct Stage {   // a pair's part of shared memory: one block of keys; later its partial output
     static constexpr int ROW = INT4 ? RD / 2 : RD;
     static constexpr int V = BLK * ROW, KS = 2 * BLK * ROW, VS = KS + 4 * BLK, LOADS = VS + 4 * BLK;
     static constexpr int BYTES = LOADS > COLS * PAD * 4 ? LOADS : COLS * PAD * 4;
 };
 
-template <int WARPS>
 struct Shared {
     uint4 qf[4 * 3][32];               // query digits as A fragments: [k-step * 3 + digit][lane]
     float part[COLS][RD];              // the drafted keys' part, then the CTA's
     float part_m[COLS], part_l[COLS];
-    float warp_m[WARPS][COLS], warp_l[WARPS][COLS], warp_f[WARPS + 1][COLS];   // f: a part's factor (the last: drafted keys)
+    uint4 px[PAIRS][2][3][32];         // a pair's weight digits as A fragments: [32 keys][digit][lane]
+    float mx[PAIRS][2][COLS + 4];      // each warp's largest scores of a block, and its largest value scale
+    float pair_m[PAIRS][COLS], warp_l[WARPS][COLS], pair_f[PAIRS + 1][COLS];   // f: a part's factor (the last: drafted keys)
     float step[COLS];                  // a score in units of log2 is (integer dot) * key scale * step
     int ages[COLS];                    // ring slots younger than this are seen (0 for a column without a node)
     unsigned long long line[TREE_MAX];
@@ -100,7 +104,7 @@ struct Place {   // a block in the row of all units' blocks
     int b, unit, block;   // sequence, unit of the sequence, block of the unit
 };
 // Sums over all threads of the CTA; the threads' inclusive prefix in `mine`.
-template <int WARPS>
+template <int NW>
 __device__ __forceinline__ int cta_scan(int& mine, int* scan) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -113,25 +117,23 @@ __device__ __forceinline__ int cta_scan(int& mine, int* scan) {
     __syncthreads();
     int total = 0;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
+    for (int w = 0; w < NW; ++w) {
         if (w < warp) mine += scan[w];
         total += scan[w];
     }
     return total;
 }
 // All blocks of the call.
-template <int WARPS>
 __device__ int all_blocks(const TreeParams& p, int* scan) {
     int mine = 0;
-    for (int b = threadIdx.x; b < p.B; b += 32 * WARPS) mine += sequence_blocks(p, b);
+    for (int b = threadIdx.x; b < p.B; b += PT) mine += sequence_blocks(p, b);
     return cta_scan<WARPS>(mine, scan) * p.hk * p.groups;
 }
 // Where block `at` of the row is.
-template <int WARPS>
 __device__ Place find_block(const TreeParams& p, int at, int* scan) {
     const int per = p.hk * p.groups;
     int before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32 * WARPS) {
+    for (int b0 = 0; b0 < p.B; b0 += PT) {
         const int b = b0 + threadIdx.x, own = b < p.B ? sequence_blocks(p, b) : 0;
         int sum = own;
         const int total = cta_scan<WARPS>(sum, scan);
@@ -209,57 +211,51 @@ __device__ __forceinline__ int v_off(int r, int j) {
     return INT4 ? (r >> 1) * 128 + ((((r & 1) << 2 | j) ^ x) << 4) : r * 128 + ((j ^ x) << 4);
 }
 
-struct Block {   // where a block's rows are
-    const uint8_t *k, *v;
-    const float *ks, *vs;
-    int rows;        // rows that hold a key; later ones are read from the last such row and masked
-    int ring_slot;   // first ring slot, or -1 for reference rows
-};
-
-// Starts the copies of a block's codes; a whole block's addresses are one base and constants.
+// Starts the copies of a warp's 32 rows of a block's codes; a whole block's addresses are one base and constants.
 template <bool INT4>
-__device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* src, int rows, bool is_v, int lane) {
+__device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t* src, int rows, bool is_v, int half, int lane) {
     constexpr int CH = INT4 ? 4 : 8, STEP = 32 / CH;   // STEP rows a round: a multiple of 4, so the swizzle repeats
-    const int j = lane % CH, r0 = lane / CH;
+    const int j = lane % CH, r0 = 32 * half + lane / CH;
     if (rows == BLK) {
-        const uint8_t* from = src + lane * 16;
+        const uint8_t* from = src + half * (32 * CH * 16) + lane * 16;
 #pragma unroll
-        for (int i = 0; i < BLK / STEP; ++i) {
+        for (int i = 0; i < 32 / STEP; ++i) {
             const int r = r0 + STEP * i;
             cp16(dst + (is_v ? v_off<INT4>(r, j) : k_off<INT4>(r, j)), from + STEP * i * (CH * 16));
         }
     } else {
 #pragma unroll 1
-        for (int i = 0; i < BLK / STEP; ++i) {
+        for (int i = 0; i < 32 / STEP; ++i) {
             const int r = r0 + STEP * i;
             cp16(dst + (is_v ? v_off<INT4>(r, j) : k_off<INT4>(r, j)), src + (size_t)min(r, rows - 1) * (CH * 16) + j * 16);
         }
     }
 }
-__device__ __forceinline__ void load_scales(uint32_t dst, const float* src, int rows, int lane) {
-    cp4(dst + 4 * lane, src + min(lane, rows - 1));
-    cp4(dst + 4 * (lane + 32), src + min(lane + 32, rows - 1));
+__device__ __forceinline__ void load_scales(uint32_t dst, const float* src, int rows, int half, int lane) {
+    const int r = 32 * half + lane;
+    cp4(dst + 4 * r, src + min(r, rows - 1));
 }
 
 // W16: more than eight columns, so both row halves of the MMA tiles are used.
-template <bool INT4, bool W16, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, 12 / WARPS > 2 ? 2 : 1) rswa_tree_kernel(const __grid_constant__ TreeParams p) {
+template <bool INT4, bool W16>
+__global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant__ TreeParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     using St = Stage<INT4>;
-    constexpr int PT = 32 * WARPS, MINE = (COLS + WARPS - 1) / WARPS;   // MINE: columns a warp prepares
-    Shared<WARPS>& sh = *reinterpret_cast<Shared<WARPS>*>(smem + WARPS * St::BYTES);
+    constexpr int MINE = COLS / WARPS;   // columns a warp prepares
+    Shared& sh = *reinterpret_cast<Shared*>(smem + PAIRS * St::BYTES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, c = lane & 3;
     const int rank = p.S > 1 ? (int)cluster_rank() : 0;
-    uint8_t* stage = smem + warp * St::BYTES;
+    const int pair = warp >> 1, half = warp & 1;
+    uint8_t* stage = smem + pair * St::BYTES;
     const uint32_t st = smem_u32(stage);
     pdl_wait();
     Place at{(int)(blockIdx.x / p.S) / (p.hk * p.groups), (int)(blockIdx.x / p.S) % (p.hk * p.groups), 0};
     int left = 1 << 30;   // blocks of this CTA's range
     if (p.part) {
-        const int all = all_blocks<WARPS>(p, sh.scan), per = (all + gridDim.x - 1) / gridDim.x;
+        const int all = all_blocks(p, sh.scan), per = (all + gridDim.x - 1) / gridDim.x;
         left = min(per, all - (int)min((int64_t)blockIdx.x * per, (int64_t)all));
         if (left == 0) return;
-        at = find_block<WARPS>(p, blockIdx.x * per, sh.scan);
+        at = find_block(p, blockIdx.x * per, sh.scan);
     }
   for (bool again = true; again;) {
     const int b = at.b, h = at.unit / p.groups, col0 = at.unit % p.groups * COLS, cols = min(COLS, p.N * p.G - col0);
@@ -279,7 +275,7 @@ __global__ void __launch_bounds__(32 * WARPS, 12 / WARPS > 2 ? 2 : 1) rswa_tree_
     // ---- this CTA's blocks of the unit; its first ones are on their way while the query is prepared
     const int nref = bad ? 0 : (R + BLK - 1) / BLK, nring = bad ? 0 : (min(n, RW) + BLK - 1) / BLK, nblk = nref + nring;
     const int whole = p.part ? sequence_blocks(p, b) : nblk;   // of the unit, as the ranges count it
-    const int first = at.block, last = min(whole, first + min(left, whole)), stride = p.S * WARPS;
+    const int first = at.block, last = min(whole, first + min(left, whole)), stride = p.S * PAIRS;
     const bool head = first == 0, complete = head && last == whole;
     const bool dead = bad || col0 / p.G >= L;   // nothing to compute, for the whole cluster
     if (bad && head) {
@@ -293,27 +289,25 @@ __global__ void __launch_bounds__(32 * WARPS, 12 / WARPS > 2 ? 2 : 1) rswa_tree_
     if (!dead) {
     const int end = min(last, nblk);
     const size_t ref0 = ((size_t)b * p.hk + h) * p.ref.cap, ring0 = ((size_t)b * p.hk + h) * RW;
-    auto block_at = [&](int i) {
-        Block x;
-        const bool ring = i >= nref;
-        const KvView& v = ring ? p.ring : p.ref;
-        const int from = (ring ? i - nref : i) * BLK;
-        const size_t row = (ring ? ring0 : ref0) + from;
-        x.k = v.k + row * St::ROW, x.v = v.v + row * St::ROW, x.ks = v.ks + row, x.vs = v.vs + row;
-        x.rows = min(BLK, (ring ? min(n, RW) : R) - from);
-        x.ring_slot = ring ? from : -1;
-        return x;
+    // Rows of block i that hold a key (later ones are read from the last such row and masked), and its copies' start.
+    auto rows_of = [&](int i) { return min(BLK, i >= nref ? min(n, RW) - (i - nref) * BLK : R - i * BLK); };
+    auto fetch_k = [&](int i) {
+        const KvView& v = i >= nref ? p.ring : p.ref;
+        const size_t row = (i >= nref ? ring0 - nref * BLK : ref0) + (size_t)i * BLK;
+        const int rows = rows_of(i);
+        load_codes<INT4>(st, v.k + row * St::ROW, rows, false, half, lane);
+        load_scales(st + St::KS, v.ks + row, rows, half, lane);
+        load_scales(st + St::VS, v.vs + row, rows, half, lane);
     };
-    int blk = first + rank * WARPS + warp;
-    Block cur{};
-    if (blk < end) {
-        cur = block_at(blk);
-        load_codes<INT4>(st, cur.k, cur.rows, false, lane);
-        load_scales(st + St::KS, cur.ks, cur.rows, lane);
-        load_scales(st + St::VS, cur.vs, cur.rows, lane);
-    }
+    auto fetch_v = [&](int i) {
+        const KvView& v = i >= nref ? p.ring : p.ref;
+        const size_t row = (i >= nref ? ring0 - nref * BLK : ref0) + (size_t)i * BLK;
+        load_codes<INT4>(st + St::V, v.v + row * St::ROW, rows_of(i), true, half, lane);
+    };
+    int blk = first + rank * PAIRS + pair;
+    if (blk < end) fetch_k(blk);
     cp_commit();
-    if (blk < end) load_codes<INT4>(st + St::V, cur.v, cur.rows, true, lane);
+    if (blk < end) fetch_v(blk);
     cp_commit();
 
     // ---- lines of the tree
@@ -415,13 +409,14 @@ __global__ void __launch_bounds__(32 * WARPS, 12 / WARPS > 2 ? 2 : 1) rswa_tree_
     }
     __syncthreads();
 
-    // ---- the blocks.  Lane (gr, c) has columns gr and gr + 8 and, of each 8 keys, keys 2 c and 2 c + 1.
-    float O[16][W16 ? 4 : 2];
+    // ---- the blocks.  A warp of a pair has the scores of 32 of the 64 keys, and of the values the dims 16 g + t with t in
+    // its half of the 16 tiles.  Lane (gr, c) has columns gr and gr + 8 and, of each 8 keys, keys 2 c and 2 c + 1.
+    constexpr int HALVES = W16 ? 2 : 1, VALS = 2 * HALVES;
+    float O[8][VALS];
 #pragma unroll
-    for (int t = 0; t < 16; ++t)
+    for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int j = 0; j < (W16 ? 4 : 2); ++j) O[t][j] = 0.f;
-    constexpr int HALVES = W16 ? 2 : 1;
+        for (int j = 0; j < VALS; ++j) O[t][j] = 0.f;
     float run_m[HALVES], run_l[HALVES], step[HALVES];
     int ages[HALVES];
 #pragma unroll
@@ -432,17 +427,18 @@ __global__ void __launch_bounds__(32 * WARPS, 12 / WARPS > 2 ? 2 : 1) rswa_tree_
     for (; blk < end; blk += stride) {
         cp_wait1();
         __syncwarp();
-        // scores, without the column's step: T[j][..] for keys 8 j + 2 c, + 1
-        float T[8][W16 ? 4 : 2], vs[8][2];
-        const bool unmasked = cur.rows == BLK && cur.ring_slot < 0;
+        // scores of the warp's own keys, without the column's step: T[j][..] for keys 8 j + 2 c, + 1 of its 32
+        float T[4][VALS], vs[4][2];
+        const int rows = rows_of(blk), ring_slot = blk >= nref ? (blk - nref) * BLK : -1;
+        const bool unmasked = rows == BLK && ring_slot < 0;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            __syncwarp();   // keeps the second half's loads from being drawn ahead of the first half's use of registers
-            int acc[4][3][4];
-            uint32_t kb[4][8];
+        for (int jp = 0; jp < 2; ++jp) {
+            __syncwarp();   // keeps the second part's loads from being drawn ahead of the first part's use of registers
+            int acc[2][3][4];
+            uint32_t kb[2][8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = 32 * half + 8 * j + gr;
+            for (int j = 0; j < 2; ++j) {
+                const int r = 32 * half + 16 * jp + 8 * j + gr;
                 if (INT4) {
                     const uint4 w = lds128(stage + k_off<true>(r, c));
                     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -461,37 +457,31 @@ __global__ void __launch_bounds__(32 * WARPS, 12 / WARPS > 2 ? 2 : 1) rswa_tree_
                     const uint4 q4 = lds128(&sh.qf[s * 3 + d][lane]);
                     const uint32_t a[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (s == 0) {
-                            if (d == 2)
-                                mma<true, true>(acc[j][d], a, kb[j][2 * s], kb[j][2 * s + 1]);
-                            else
-                                mma<false, true>(acc[j][d], a, kb[j][2 * s], kb[j][2 * s + 1]);
-                        } else {
-                            if (d == 2)
-                                mma<true, false>(acc[j][d], a, kb[j][2 * s], kb[j][2 * s + 1]);
-                            else
-                                mma<false, false>(acc[j][d], a, kb[j][2 * s], kb[j][2 * s + 1]);
-                        }
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t b0 = kb[j][2 * s], b1 = kb[j][2 * s + 1];
+                        if (d == 2)
+                            s == 0 ? mma<true, true>(acc[j][d], a, b0, b1) : mma<true, false>(acc[j][d], a, b0, b1);
+                        else
+                            s == 0 ? mma<false, true>(acc[j][d], a, b0, b1) : mma<false, false>(acc[j][d], a, b0, b1);
                     }
                 }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int key = 32 * half + 8 * j + 2 * c, jj = 4 * half + j;
-                float2 ks = *reinterpret_cast<const float2*>(stage + St::KS + 4 * key);
-                float2 v2 = *reinterpret_cast<const float2*>(stage + St::VS + 4 * key);
+            for (int j = 0; j < 2; ++j) {
+                const int jj = 2 * jp + j, key = 32 * half + 8 * jj + 2 * c;
+                const float2 ks = *reinterpret_cast<const float2*>(stage + St::KS + 4 * key);
+                const float2 v2 = *reinterpret_cast<const float2*>(stage + St::VS + 4 * key);
                 vs[jj][0] = v2.x, vs[jj][1] = v2.y;
 #pragma unroll
-                for (int i = 0; i < (W16 ? 4 : 2); ++i)
+                for (int i = 0; i < VALS; ++i)
                     T[jj][i] = (upper(acc[j][2][i]) + lower(acc[j][1][i], acc[j][0][i])) * (i & 1 ? ks.y : ks.x);
                 if (!unmasked) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const bool in = key + i < cur.rows;
+                        const bool in = key + i < rows;
                         if (!in) vs[jj][i] = 0.f;
 #pragma unroll
                         for (int e = 0; e < HALVES; ++e) {
-                            const bool seen = in && (cur.ring_slot < 0 || ((n - 1 - cur.ring_slot - key - i) & (RW - 1)) < ages[e]);
+                            const bool seen = in && (ring_slot < 0 || ((n - 1 - ring_slot - key - i) & (RW - 1)) < ages[e]);
                             if (!seen) T[jj][2 * e + i] = -INFINITY;
                         }
                     }
@@ -501,38 +491,40 @@ __global__ void __launch_bounds__(32 * WARPS, 12 / WARPS > 2 ? 2 : 1) rswa_tree_
         __syncwarp();
         // the next block's K and scales take this block's place
         const int next = blk + stride;
-        Block nxt{};
-        if (next < end) {
-            nxt = block_at(next);
-            load_codes<INT4>(st, nxt.k, nxt.rows, false, lane);
-            load_scales(st + St::KS, nxt.ks, nxt.rows, lane);
-            load_scales(st + St::VS, nxt.vs, nxt.rows, lane);
-        }
+        if (next < end) fetch_k(next);
         cp_commit();
-        // softmax of the block: weights relative to its largest score and value scale, as digits
-        float vmax = TINY;
+        // softmax of the block: weights relative to its largest score and value scale, over both warps' keys
+        float vmax = TINY, tm[HALVES];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) vmax = fmaxf(vmax, fmaxf(vs[j][0], vs[j][1]));
+        for (int j = 0; j < 4; ++j) vmax = fmaxf(vmax, fmaxf(vs[j][0], vs[j][1]));
         vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
         vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-        const float vinv = P_TOP / vmax;
-        float alpha[HALVES], gain[HALVES];
-        uint32_t pd[2][3][4];   // digits as A fragments: [32 keys][digit]
-#pragma unroll
-        for (int j = 0; j < 8; ++j) vs[j][0] *= vinv, vs[j][1] *= vinv;
 #pragma unroll
         for (int e = 0; e < HALVES; ++e) {
-            float tm = T[0][2 * e];
+            tm[e] = fmaxf(T[0][2 * e], T[0][2 * e + 1]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) tm = fmaxf(tm, fmaxf(T[j][2 * e], T[j][2 * e + 1]));
-            tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
-            tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
-            const bool any = tm != -INFINITY;
-            const float mb = any ? tm * step[e] : 0.f;
+            for (int j = 1; j < 4; ++j) tm[e] = fmaxf(tm[e], fmaxf(T[j][2 * e], T[j][2 * e + 1]));
+            tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], 1));
+            tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], 2));
+            if (c == 0) sh.mx[pair][half][gr + 8 * e] = tm[e];
+        }
+        if (lane == 0) sh.mx[pair][half][COLS] = vmax;
+        named_bar_sync(1 + pair, 64);
+        vmax = fmaxf(vmax, sh.mx[pair][half ^ 1][COLS]);
+        const float vinv = P_TOP / vmax;
+        float alpha[HALVES], gain[HALVES];
+        uint32_t pd[3][4];   // digits of the warp's keys as an A fragment
+#pragma unroll
+        for (int j = 0; j < 4; ++j) vs[j][0] *= vinv, vs[j][1] *= vinv;
+#pragma unroll
+        for (int e = 0; e < HALVES; ++e) {
+            tm[e] = fmaxf(tm[e], sh.mx[pair][half ^ 1][gr + 8 * e]);
+            const bool any = tm[e] != -INFINITY;
+            const float mb = any ? tm[e] * step[e] : 0.f;
             float sum = 0.f;
-            uint32_t u[8][2];
+            uint32_t u[4][2];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float w = ex2(fminf(fmaf(T[j][2 * e + i], step[e], -mb), 0.f));
@@ -540,17 +532,14 @@ __global__ void __launch_bounds__(32 * WARPS, 12 / WARPS > 2 ? 2 : 1) rswa_tree_
                     u[j][i] = __float2uint_rn(w * vs[j][i]);
                 }
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const int j = 4 * kk + 2 * g;
-                    const uint32_t t0 = __byte_perm(u[j][0], u[j][1], 0x5140), t1 = __byte_perm(u[j + 1][0], u[j + 1][1], 0x5140);
-                    const uint32_t t2 = __byte_perm(u[j][0], u[j][1], 0x0062), t3 = __byte_perm(u[j + 1][0], u[j + 1][1], 0x0062);
-                    // fragment words: (row gr, keys g = 0), (row gr + 8, g = 0), (gr, g = 1), (gr + 8, g = 1)
-                    pd[kk][0][2 * g + e] = __byte_perm(t0, t1, 0x5410);
-                    pd[kk][1][2 * g + e] = __byte_perm(t0, t1, 0x7632);
-                    pd[kk][2][2 * g + e] = __byte_perm(t2, t3, 0x5410);
-                }
+            for (int g = 0; g < 2; ++g) {
+                const uint32_t t0 = __byte_perm(u[2 * g][0], u[2 * g][1], 0x5140), t1 = __byte_perm(u[2 * g + 1][0], u[2 * g + 1][1], 0x5140);
+                const uint32_t t2 = __byte_perm(u[2 * g][0], u[2 * g][1], 0x0062), t3 = __byte_perm(u[2 * g + 1][0], u[2 * g + 1][1], 0x0062);
+                // fragment words: (row gr, keys g = 0), (row gr + 8, g = 0), (gr, g = 1), (gr + 8, g = 1)
+                pd[0][2 * g + e] = __byte_perm(t0, t1, 0x5410);
+                pd[1][2 * g + e] = __byte_perm(t0, t1, 0x7632);
+                pd[2][2 * g + e] = __byte_perm(t2, t3, 0x5410);
+            }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             const float mn = any ? fmaxf(run_m[e], mb) : run_m[e];
@@ -560,91 +549,90 @@ __global__ void __launch_bounds__(32 * WARPS, 12 / WARPS > 2 ? 2 : 1) rswa_tree_
             gain[e] = beta * vmax * ((INT4 ? 1.f / 16.f : 1.f) / P_TOP);
             run_m[e] = mn;
         }
-        if (!W16) {
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int d = 0; d < 3; ++d) pd[kk][d][1] = pd[kk][d][3] = 0u;
+        for (int d = 0; d < 3; ++d) {
+            if (!W16) pd[d][1] = pd[d][3] = 0u;
+            sh.px[pair][half][d][lane] = make_uint4(pd[d][0], pd[d][1], pd[d][2], pd[d][3]);
         }
         cp_wait1();
-        __syncwarp();
-        // values: dim 16 gr + t of tile t, from the bytes of the lane's sixteen keys; eight tiles at a time
-        auto load_values = [&](int dh, uint32_t (&vb)[2][8][2]) {
+        named_bar_sync(1 + pair, 64);   // both warps' digits and values are there
+        uint32_t pa[2][3][4];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const int r0 = 32 * kk + 16 * g + 2 * c;
-                    uint32_t o[4];
-                    if (INT4) {
-                        uint32_t w[4];
+            for (int d = 0; d < 3; ++d) {
+                const uint4 w = lds128(&sh.px[pair][kk][d][lane]);
+                pa[kk][d][0] = w.x, pa[kk][d][1] = w.y, pa[kk][d][2] = w.z, pa[kk][d][3] = w.w;
+            }
+        // values: dim 16 gr + 8 half + t of tile t, from the bytes of the lane's sixteen keys
+        uint32_t vb[2][8][2];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = r0 + (i & 1) + 8 * (i >> 1);
-                            w[i] = *reinterpret_cast<const uint32_t*>(stage + St::V + v_off<true>(r, gr >> 1) + (gr & 1) * 8 + 4 * dh);
-                        }
-                        transpose4(w[0], w[1], w[2], w[3], o);
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) vb[kk][2 * i][g] = (o[i] << 4) & 0xF0F0F0F0u, vb[kk][2 * i + 1][g] = o[i] & 0xF0F0F0F0u;
-                    } else {
-                        uint2 w[4];
+            for (int g = 0; g < 2; ++g) {
+                const int r0 = 32 * kk + 16 * g + 2 * c;
+                uint32_t o[4];
+                if (INT4) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            w[i] = *reinterpret_cast<const uint2*>(stage + St::V + v_off<false>(r0 + (i & 1) + 8 * (i >> 1), gr) + 8 * dh);
-                        transpose4(w[0].x, w[1].x, w[2].x, w[3].x, o);
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = *reinterpret_cast<const uint32_t*>(stage + St::V + v_off<true>(r0 + (i & 1) + 8 * (i >> 1), gr >> 1) + (gr & 1) * 8 + 4 * half);
+                    transpose4(w[0], w[1], w[2], w[3], o);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) vb[kk][i][g] = o[i];
-                        transpose4(w[0].y, w[1].y, w[2].y, w[3].y, o);
+                    for (int i = 0; i < 4; ++i) vb[kk][2 * i][g] = (o[i] << 4) & 0xF0F0F0F0u, vb[kk][2 * i + 1][g] = o[i] & 0xF0F0F0F0u;
+                } else {
+                    uint2 w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) vb[kk][4 + i][g] = o[i];
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = *reinterpret_cast<const uint2*>(stage + St::V + v_off<false>(r0 + (i & 1) + 8 * (i >> 1), gr) + 8 * half);
+                    transpose4(w[0].x, w[1].x, w[2].x, w[3].x, o);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vb[kk][i][g] = o[i];
+                    transpose4(w[0].y, w[1].y, w[2].y, w[3].y, o);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vb[kk][4 + i][g] = o[i];
                 }
-        };
+            }
+        named_bar_sync(1 + pair, 64);   // both have read the values: the next block's take their place
+        if (next < end) fetch_v(next);
+        cp_commit();
         bool moved = false;   // a new maximum rescales what there is; mostly there is none
 #pragma unroll
         for (int e = 0; e < HALVES; ++e) moved |= alpha[e] != 1.f;
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-            for (int t = 0; t < 16; ++t)
+            for (int t = 0; t < 8; ++t)
 #pragma unroll
-                for (int i = 0; i < (W16 ? 4 : 2); ++i) O[t][i] *= alpha[i >> 1];
+                for (int i = 0; i < VALS; ++i) O[t][i] *= alpha[i >> 1];
         }
 #pragma unroll
-        for (int dh = 0; dh < 2; ++dh) {
-            uint32_t vb[2][8][2];
-            load_values(dh, vb);
-            __syncwarp();
-            if (dh == 1) {   // the values have been read: the next block's take their place
-                if (next < end) load_codes<INT4>(st + St::V, nxt.v, nxt.rows, true, lane);
-                cp_commit();
-            }
+        for (int t = 0; t < 8; ++t) {
+            int acc[3][4];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                int acc[3][4];
+            for (int d = 0; d < 3; ++d) mma<false, true>(acc[d], pa[0][d], vb[0][t][0], vb[0][t][1]);
 #pragma unroll
-                for (int d = 0; d < 3; ++d) mma<false, true>(acc[d], pd[0][d], vb[0][t][0], vb[0][t][1]);
+            for (int d = 0; d < 3; ++d) mma<false, false>(acc[d], pa[1][d], vb[1][t][0], vb[1][t][1]);
 #pragma unroll
-                for (int d = 0; d < 3; ++d) mma<false, false>(acc[d], pd[1][d], vb[1][t][0], vb[1][t][1]);
-#pragma unroll
-                for (int i = 0; i < (W16 ? 4 : 2); ++i)
-                    O[8 * dh + t][i] = fmaf(upper(acc[2][i]), gain[i >> 1], fmaf(lower(acc[1][i], acc[0][i]), gain[i >> 1], O[8 * dh + t][i]));
-            }
+            for (int i = 0; i < VALS; ++i)
+                O[t][i] = fmaf(upper(acc[2][i]), gain[i >> 1], fmaf(lower(acc[1][i], acc[0][i]), gain[i >> 1], O[t][i]));
         }
-        cur = nxt;
     }
-    // ---- join the warps: partial outputs at [column][t * 8 + dim / 16], dim = 16 * (dim / 16) + t
+    // ---- join the pairs: partial outputs at [column][t * 8 + dim / 16], dim = 16 * (dim / 16) + t
     cp_wait0();
-    __syncwarp();
+    named_bar_sync(1 + pair, 64);
     {
         float* po = reinterpret_cast<float*>(stage);
 #pragma unroll
-        for (int t = 0; t < 16; ++t)
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int e = 0; e < HALVES; ++e)
-                *reinterpret_cast<float2*>(po + (gr + 8 * e) * PAD + t * 8 + 2 * c) = make_float2(O[t][2 * e], O[t][2 * e + 1]);
+                *reinterpret_cast<float2*>(po + (gr + 8 * e) * PAD + (8 * half + t) * 8 + 2 * c) = make_float2(O[t][2 * e], O[t][2 * e + 1]);
         if (c == 0) {
 #pragma unroll
-            for (int e = 0; e < HALVES; ++e) sh.warp_m[warp][gr + 8 * e] = run_m[e], sh.warp_l[warp][gr + 8 * e] = run_l[e];
+            for (int e = 0; e < HALVES; ++e) {
+                if (half == 0) sh.pair_m[pair][gr + 8 * e] = run_m[e];
+                sh.warp_l[warp][gr + 8 * e] = run_l[e];
+            }
         }
     }
     __syncthreads();
@@ -654,14 +642,14 @@ __global__ void __launch_bounds__(32 * WARPS, 12 / WARPS > 2 ? 2 : 1) rswa_tree_
         const float pm = sh.part_m[col];
         float M = pm;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sh.warp_m[w][col]);
+        for (int w = 0; w < PAIRS; ++w) M = fmaxf(M, sh.pair_m[w][col]);
         float f = ex2(pm - M), l = f * sh.part_l[col];
-        sh.warp_f[WARPS][col] = f;
+        sh.pair_f[PAIRS][col] = f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            f = ex2(sh.warp_m[w][col] - M);
-            sh.warp_f[w][col] = f;
-            l = fmaf(f, sh.warp_l[w][col], l);
+        for (int w = 0; w < PAIRS; ++w) {
+            f = ex2(sh.pair_m[w][col] - M);
+            sh.pair_f[w][col] = f;
+            l = fmaf(f, sh.warp_l[2 * w][col] + sh.warp_l[2 * w + 1][col], l);
         }
         sh.part_m[col] = M, sh.part_l[col] = l;
         if (p.part && !complete) mine[col] = M, mine[PART_L + col] = l;
@@ -669,10 +657,10 @@ __global__ void __launch_bounds__(32 * WARPS, 12 / WARPS > 2 ? 2 : 1) rswa_tree_
     __syncthreads();
     for (int i = tid; i < cols * RD; i += PT) {
         const int col = i / RD, d = i % RD;
-        float o = sh.warp_f[WARPS][col] * sh.part[col][d];
+        float o = sh.pair_f[PAIRS][col] * sh.part[col][d];
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w)
-            o = fmaf(sh.warp_f[w][col], reinterpret_cast<const float*>(smem + w * St::BYTES)[col * PAD + (d & 15) * 8 + (d >> 4)], o);
+        for (int w = 0; w < PAIRS; ++w)
+            o = fmaf(sh.pair_f[w][col], reinterpret_cast<const float*>(smem + w * St::BYTES)[col * PAD + (d & 15) * 8 + (d >> 4)], o);
         if (p.S > 1) {
             sh.part[col][d] = o;
         } else if (complete) {
@@ -751,9 +739,8 @@ __global__ void __launch_bounds__(JT) rswa_tree_join_kernel(const __grid_constan
     }
 }
 
-// How a call is split, from its sizes alone: clusters of CTAs of four warps (two resident per SM) while all units fit the
-// device at once with two blocks a warp, else ranges, one CTA of twelve warps per SM.
-constexpr int FEW = 4, MANY = 4;
+// How a call is split, from its sizes alone: a cluster for each unit while all of them fit the device at once (two CTAs
+// per SM) with at most two blocks a pair, else ranges, one for each resident CTA.
 struct TreePlan {
     int groups, S, ctas;   // ctas: of the ranges, or 0 for clusters
 };
@@ -764,17 +751,17 @@ TreePlan tree_plan(int B, int N, int heads_q, int heads, int cap) {
     const int64_t units = (int64_t)B * heads * pl.groups;
     const int blocks = (cap + BLK - 1) / BLK + RW / BLK;
     pl.S = 1;
-    while (pl.S < 8 && pl.S * FEW < blocks) pl.S *= 2;
+    while (pl.S < 8 && pl.S * PAIRS < blocks) pl.S *= 2;
     pl.ctas = 0;
     while (pl.S > 1 && units * pl.S > 2 * sms) pl.S /= 2;
-    if (blocks > 2 * pl.S * FEW) pl.S = 1, pl.ctas = 2 * sms;
+    if (blocks > 2 * pl.S * PAIRS) pl.S = 1, pl.ctas = 2 * sms;
     return pl;
 }
 
-template <bool INT4, bool W16, int WARPS>
+template <bool INT4, bool W16>
 cudaError_t launch_tree(TreeParams& p, const TreePlan& pl, cudaStream_t st) {
-    const void* fn = (const void*)rswa_tree_kernel<INT4, W16, WARPS>;
-    const size_t smem = WARPS * Stage<INT4>::BYTES + sizeof(Shared<WARPS>);
+    const void* fn = (const void*)rswa_tree_kernel<INT4, W16>;
+    const size_t smem = PAIRS * Stage<INT4>::BYTES + sizeof(Shared);
     cudaError_t e = once_per_device(fn, [&] {
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
@@ -782,19 +769,14 @@ cudaError_t launch_tree(TreeParams& p, const TreePlan& pl, cudaStream_t st) {
     p.groups = pl.groups, p.S = pl.S;
     const unsigned units = (unsigned)p.B * p.hk * p.groups;
     void* args[] = {&p};
-    if (!pl.ctas) return launch_kernel(fn, dim3(units * p.S), dim3(32 * WARPS), smem, p.S, args, st);
-    e = launch_kernel(fn, dim3((unsigned)pl.ctas), dim3(32 * WARPS), smem, 1, args, st);
+    if (!pl.ctas) return launch_kernel(fn, dim3(units * p.S), dim3(PT), smem, p.S, args, st);
+    e = launch_kernel(fn, dim3((unsigned)pl.ctas), dim3(PT), smem, 1, args, st);
     if (e != cudaSuccess) return e;
     int ctas = pl.ctas;
     void* more[] = {&p, &ctas};
     const int cols = p.N * p.G < COLS ? p.N * p.G : COLS;
     return launch_kernel((const void*)rswa_tree_join_kernel, dim3(units, cols < 4 ? cols : 4), dim3(JT), 0, 1, more, st);
 }
-template <bool INT4, bool W16>
-cudaError_t launch_tree(TreeParams& p, const TreePlan& pl, cudaStream_t st) {
-    return pl.ctas ? launch_tree<INT4, W16, MANY>(p, pl, st) : launch_tree<INT4, W16, FEW>(p, pl, st);
-}
-
 }  // namespace
 }  // namespace focr
 
