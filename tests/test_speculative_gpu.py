@@ -254,6 +254,62 @@ def test_long_reference_block(int4):
     check_tree(34, 2, 5, 4, 2, 8192, [8191, 4100], [900, 40], int4)
 
 
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("N,hq,hk", [(1, 2, 2), (3, 4, 1), (16, 2, 2), (17, 1, 1), (16, 4, 2), (21, 2, 1), (33, 1, 1), (64, 1, 1), (16, 8, 2)])
+def test_many_units_kernel_head_layouts(N, hq, hk, int4):
+    # few units but a capacity that splits into ranges; lengths around its tiles of 128
+    check_tree(400 + N, 3, N, hq, hk, 4300, [4300, 257, 128], [600, 127, 1], int4)
+
+
+@pytest.mark.parametrize("int4", [False, True])
+def test_many_units_kernel_on_a_ragged_batch(int4):
+    rng = np.random.default_rng(44)
+    B = 170
+    lens = [int(x) for x in rng.integers(0, 520, B)]
+    lens[:8] = [0, 1, 127, 128, 129, 255, 256, 520]
+    gen = [int(x) for x in rng.integers(0, 300, B)]
+    gen[:4] = [0, 0, 1, 5]
+    nodes = [int(x) for x in rng.integers(0, 4, B)]
+    nodes[:4] = [3, 1, 0, 2]
+    check_tree(45, B, 3, 2, 2, 520, lens, gen, int4, n_nodes=nodes)
+
+
+def test_many_units_kernel_when_the_scores_keep_rising():
+    import torch
+    # keys ordered so that every tile has a new maximum: the bounds move all the time, and value scales grow too
+    rng = np.random.default_rng(46)
+    R, N = 4300, 4
+    q = f32(rng, 1, N, 2, 128)
+    k = f32(rng, 1, 2, R, 128) * 0.05 + q[:, 0][:, :, None] * np.linspace(0, 2, R, dtype=np.float32)[None, None, :, None]
+    v = f32(rng, 1, 2, R, 128) * np.linspace(0.01, 3, R, dtype=np.float32)[None, None, :, None]
+    for int4 in (False, True):
+        ref = [x for y in (k, v) for x in sp.quantise(y, int4)]
+        ring = np_cache(rng, 1, 2, 128, int4)
+        kn, vn = f32(rng, 1, N, 2, 128), f32(rng, 1, N, 2, 128)
+        got = api.focr_rswa_tree(dev(q), dev(kn), dev(vn), dev_cache(ref), ints([R]), dev_cache(ring), ints([40])).cpu().numpy()
+        val = lambda c: (sp.values(c[0], c[1]), sp.values(c[2], c[3]))  # noqa: E731
+        want = sp.rswa_tree(q, kn, vn, val(ref), [R], val(ring), [40])
+        assert np.abs(got - want).max() <= TOL_TREE * np.abs(v).max()
+
+
+def test_many_units_kernel_marks_invalid_sequences():
+    import torch
+    rng = np.random.default_rng(47)
+    B, N, cap = 6, 3, 4300
+    q, k = f32(rng, B, N, 2, 128), f32(rng, B, N, 2, 128)
+    ref, ring = np_cache(rng, B, 2, cap, False), np_cache(rng, B, 2, 128, False)
+    ref_len, n_gen, n_nodes = [cap + 1, -1, 900, 4300, 4300, 1200], [5, 5, -1, 5, 5, 5], [3, 2, 3, 4, 3, 3]
+    parent = [[-1, 0, 1]] * 4 + [[-1, 1, 0]] + [[-1, 0, -1]]
+    out = torch.full((B, N, 2, 128), 7.0, device="cuda")
+    api.focr_rswa_tree(dev(q), dev(k), dev(k), dev_cache(ref), ints(ref_len), dev_cache(ring), ints(n_gen), ints(parent),
+                       ints(n_nodes), out=out)
+    got = out.cpu().numpy()
+    assert np.isnan(got[[0, 2, 3, 4]]).all() and np.isnan(got[1, :2]).all() and (got[1, 2] == 7.0).all()
+    val = lambda c: (sp.values(c[0], c[1])[5:], sp.values(c[2], c[3])[5:])  # noqa: E731
+    want = sp.rswa_tree(q[5:], k[5:], k[5:], val(ref), ref_len[5:], val(ring), n_gen[5:], parent[5:], n_nodes[5:])
+    assert np.abs(got[5] - want[0]).max() <= TOL_TREE * 6
+
+
 def test_many_sequences():
     check_tree(35, 70, 2, 2, 2, 40, [b % 41 for b in range(70)], [b * 7 for b in range(70)])
 

@@ -42,36 +42,16 @@
 #include "common.cuh"
 #include "kv_cache.h"
 #include "launch_state.h"
+#include "rswa_tree.cuh"
 
 namespace focr {
 namespace {
 
-constexpr int RD = FOCR_RSWA_DIM, RW = FOCR_RSWA_RING;
-constexpr int TREE_MAX = FOCR_TREE_NODES_MAX;
+constexpr int RD = TREE_DIM, RW = TREE_RING;
 constexpr int COLS = 16;                        // columns of a CTA: the rows of one MMA tile
 constexpr int BLK = 64;                         // keys of a block
 constexpr int WARPS = 8, PAIRS = WARPS / 2, PT = 32 * WARPS;   // two warps work on a block
-constexpr int JT = 128;                         // threads of the joining kernel
-constexpr int PAD = RD + 8;                     // floats per row of a warp's partial output: no bank conflicts
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float SCALE = 0.08838834764831845f;   // 1 / sqrt(128)
-constexpr float Q_TOP = 8323072.f;              // 127 * 2^16: the largest fixed-point query value
-constexpr float P_TOP = 16711680.f;             // 255 * 2^16: the largest fixed-point weight
-constexpr float MAGIC = 12582912.f;             // 1.5 * 2^23
-constexpr int MAGIC_BITS = 0x4B400000;
-constexpr float NONE = -1e30f;                  // running maximum of a column that has seen no key
-constexpr float TINY = 1e-30f;                  // magnitudes below this share its step
-
-struct TreeParams {
-    const float *q, *k_new, *v_new;
-    KvView ref, ring;
-    const int32_t *ref_len, *n_gen, *parent, *n_nodes;
-    float* out;
-    int B, N, hq, hk, G, S, groups;   // S: CTAs of a cluster; groups: column groups of 16 per kv head
-    float* part;                      // ranges: two partial results per CTA, or nullptr (clusters)
-};
-// A partial result: 16 columns' maxima, sums and unnormalised outputs.
-constexpr int PART_L = COLS, PART_O = 2 * COLS, PART_FLOATS = 2 * COLS + COLS * RD;
+constexpr int PAD = RD + 8;                     // floats per row of a pair's partial output: no bank conflicts
 
 template <bool INT4>
 struct Stage {   // a pair's part of shared memory: one block of keys; later its partial output
@@ -91,79 +71,7 @@ struct Shared {
     int ages[COLS];                    // ring slots younger than this are seen (0 for a column without a node)
     unsigned long long line[TREE_MAX];
     int par[TREE_MAX];
-    int scan[WARPS + 4];
 };
-
-// Blocks of a sequence (one at least: the drafted keys need a CTA too).
-__device__ __forceinline__ int sequence_blocks(const TreeParams& p, int b) {
-    const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b);
-    if (R < 0 || R > p.ref.cap || n < 0) return 1;
-    return max(1, (R + BLK - 1) / BLK + (min(n, RW) + BLK - 1) / BLK);
-}
-struct Place {   // a block in the row of all units' blocks
-    int b, unit, block;   // sequence, unit of the sequence, block of the unit
-};
-// Sums over all threads of the CTA; the threads' inclusive prefix in `mine`.
-template <int NW>
-__device__ __forceinline__ int cta_scan(int& mine, int* scan) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, mine, o);
-        if (lane >= o) mine += up;
-    }
-    __syncthreads();
-    if (lane == 31) scan[warp] = mine;
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        if (w < warp) mine += scan[w];
-        total += scan[w];
-    }
-    return total;
-}
-// All blocks of the call.
-__device__ int all_blocks(const TreeParams& p, int* scan) {
-    int mine = 0;
-    for (int b = threadIdx.x; b < p.B; b += PT) mine += sequence_blocks(p, b);
-    return cta_scan<WARPS>(mine, scan) * p.hk * p.groups;
-}
-// Where block `at` of the row is.
-__device__ Place find_block(const TreeParams& p, int at, int* scan) {
-    const int per = p.hk * p.groups;
-    int before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += PT) {
-        const int b = b0 + threadIdx.x, own = b < p.B ? sequence_blocks(p, b) : 0;
-        int sum = own;
-        const int total = cta_scan<WARPS>(sum, scan);
-        if ((int64_t)(before + total) * per > at) {
-            const int64_t first = (int64_t)(before + sum - own) * per;
-            if (at >= first && at < first + (int64_t)own * per) scan[WARPS] = b, scan[WARPS + 1] = (int)(at - first), scan[WARPS + 2] = own;
-            __syncthreads();
-            const Place x{scan[WARPS], scan[WARPS + 1] / scan[WARPS + 2], scan[WARPS + 1] % scan[WARPS + 2]};
-            __syncthreads();
-            return x;
-        }
-        before += total;
-    }
-    return Place{p.B, 0, 0};
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait0() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // d = a (16 x 32) * b (32 x 8) + c.  A_S8: a is signed like b (the query's top digit); else a holds unsigned digits.
 template <bool A_S8>
@@ -185,12 +93,6 @@ __device__ __forceinline__ void mma(int (&d)[4], const uint32_t (&a)[4], uint32_
     else
         mma<A_S8>(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
-// 65536 d2 + 256 d1 + d0 of three accumulators that started at MAGIC_BITS, as two parts: lower() + upper().  The
-// products with the constants are exact (multiples of 256 and 65536 below 2^24 of them), the sums round once each.
-__device__ __forceinline__ float lower(int d1, int d0) {
-    return fmaf(__int_as_float(d1), 256.f, -257.f * MAGIC) + __int_as_float(d0);
-}
-__device__ __forceinline__ float upper(int d2) { return fmaf(__int_as_float(d2), 65536.f, -65536.f * MAGIC); }
 // bytes of four words, transposed: o[i] = byte i of a, b, c, d
 __device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&o)[4]) {
     const uint32_t t0 = __byte_perm(a, b, 0x5140), t1 = __byte_perm(c, d, 0x5140);
@@ -249,16 +151,8 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
     uint8_t* stage = smem + pair * St::BYTES;
     const uint32_t st = smem_u32(stage);
     pdl_wait();
-    Place at{(int)(blockIdx.x / p.S) / (p.hk * p.groups), (int)(blockIdx.x / p.S) % (p.hk * p.groups), 0};
-    int left = 1 << 30;   // blocks of this CTA's range
-    if (p.part) {
-        const int all = all_blocks(p, sh.scan), per = (all + gridDim.x - 1) / gridDim.x;
-        left = min(per, all - (int)min((int64_t)blockIdx.x * per, (int64_t)all));
-        if (left == 0) return;
-        at = find_block(p, blockIdx.x * per, sh.scan);
-    }
-  for (bool again = true; again;) {
-    const int b = at.b, h = at.unit / p.groups, col0 = at.unit % p.groups * COLS, cols = min(COLS, p.N * p.G - col0);
+    const int per = p.hk * p.groups, b = (int)(blockIdx.x / p.S) / per, unit = (int)(blockIdx.x / p.S) % per;
+    const int h = unit / p.groups, col0 = unit % p.groups * COLS, cols = min(COLS, p.N * p.G - col0);
     // ---- everything that depends on nothing, at once: lengths, parents, queries
     const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b), L = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
     const int par = tid < p.N && p.parent ? __ldg(p.parent + (size_t)b * p.N + tid) : tid - 1;
@@ -274,20 +168,16 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
     const bool bad = __syncthreads_or(!lengths || (tid < L && (par < -1 || par >= tid)));
     // ---- this CTA's blocks of the unit; its first ones are on their way while the query is prepared
     const int nref = bad ? 0 : (R + BLK - 1) / BLK, nring = bad ? 0 : (min(n, RW) + BLK - 1) / BLK, nblk = nref + nring;
-    const int whole = p.part ? sequence_blocks(p, b) : nblk;   // of the unit, as the ranges count it
-    const int first = at.block, last = min(whole, first + min(left, whole)), stride = p.S * PAIRS;
-    const bool head = first == 0, complete = head && last == whole;
-    const bool dead = bad || col0 / p.G >= L;   // nothing to compute, for the whole cluster
-    if (bad && head) {
+    if (bad) {
         const int live = L < 0 || L > p.N ? p.N : L;
         for (int col = rank; col < cols; col += p.S) {
             const int node = (col0 + col) / p.G;
             if (node < live && tid < RD)
                 p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = __int_as_float(0x7fc00000);
         }
+        return;
     }
-    if (!dead) {
-    const int end = min(last, nblk);
+    if (col0 / p.G >= L) return;   // no live node in this group, in any CTA of the cluster
     const size_t ref0 = ((size_t)b * p.hk + h) * p.ref.cap, ring0 = ((size_t)b * p.hk + h) * RW;
     // Rows of block i that hold a key (later ones are read from the last such row and masked), and its copies' start.
     auto rows_of = [&](int i) { return min(BLK, i >= nref ? min(n, RW) - (i - nref) * BLK : R - i * BLK); };
@@ -304,10 +194,11 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         const size_t row = (i >= nref ? ring0 - nref * BLK : ref0) + (size_t)i * BLK;
         load_codes<INT4>(st + St::V, v.v + row * St::ROW, rows_of(i), true, half, lane);
     };
-    int blk = first + rank * PAIRS + pair;
-    if (blk < end) fetch_k(blk);
+    int blk = rank * PAIRS + pair;
+    const int stride = p.S * PAIRS;
+    if (blk < nblk) fetch_k(blk);
     cp_commit();
-    if (blk < end) fetch_v(blk);
+    if (blk < nblk) fetch_v(blk);
     cp_commit();
 
     // ---- lines of the tree
@@ -317,36 +208,23 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         sh.line[tid] = line;
     }
     __syncthreads();
-    // ---- query digits, per-column constants, and the drafted keys' part: the CTA that has the unit's first block has
-    // them, in a cluster every S-th column's.  Four keys at a time; the first four of all columns are loaded at once.
+    // ---- query digits, per-column constants, and the drafted keys' part (a CTA of the cluster takes every S-th column's):
+    // four keys at a time, the first four of all columns loaded at once
     unsigned long long line[MINE];
     float4 kk[MINE][4], vv[MINE][4];
-    auto draft_load = [&](unsigned long long& rest, float4 (&k4)[4], float4 (&v4)[4]) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            k4[j] = v4[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (rest) {
-                const size_t r = (((size_t)b * p.N + __ffsll(rest) - 1) * p.hk + h) * (RD / 4) + lane;
-                k4[j] = __ldg(reinterpret_cast<const float4*>(p.k_new) + r);
-                v4[j] = __ldg(reinterpret_cast<const float4*>(p.v_new) + r);
-            }
-            rest &= rest - 1;
-        }
-    };
 #pragma unroll
     for (int i = 0; i < MINE; ++i) {
         const int col = warp + i * WARPS, node = (col0 + col) / p.G;
         const bool live = col < cols && node < L;
         if (!live) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        line[i] = live && head && col % p.S == rank ? sh.line[node] : 0ull;
+        line[i] = live && col % p.S == rank ? sh.line[node] : 0ull;
         unsigned long long rest = line[i];
-        draft_load(rest, kk[i], vv[i]);
-        if (lane == 0 && col < COLS) sh.ages[col] = live ? min(n, RW - __popcll(sh.line[node])) : 0;
+        draft_load(p, b, h, lane, rest, kk[i], vv[i]);
+        if (lane == 0) sh.ages[col] = live ? min(n, RW - __popcll(sh.line[node])) : 0;
     }
 #pragma unroll
     for (int i = 0; i < MINE; ++i) {
         const int col = warp + i * WARPS;
-        if (col >= COLS) break;
         const float4 x = q[i];
         float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
@@ -368,44 +246,10 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
                 reinterpret_cast<uint32_t*>(&sh.qf[s * 3 + d][tl + cc])[2 * (lane & 1) + hi] = v0 | v1 << 8 | v2 << 16 | v3 << 24;
             }
         }
-        if (lane == 0) sh.step[col] = a / Q_TOP * (SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
-        float m = NONE, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float k2 = SCALE * LOG2E;
-        const float4 qs = make_float4(x.x * k2, x.y * k2, x.z * k2, x.w * k2);
-        for (bool more = line[i] != 0; more;) {
-            float sc[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sc[j] = qs.x * kk[i][j].x + qs.y * kk[i][j].y + qs.z * kk[i][j].z + qs.w * kk[i][j].w;
-#pragma unroll
-            for (int e = 16; e >= 1; e >>= 1)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sc[j] += __shfl_xor_sync(0xffffffffu, sc[j], e);
-            float mn = m;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (!line[i]) sc[j] = -INFINITY;
-                line[i] &= line[i] - 1;
-                mn = fmaxf(mn, sc[j]);
-            }
-            const float al = ex2(m - mn);
-            l *= al, o.x *= al, o.y *= al, o.z *= al, o.w *= al;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float w = ex2(sc[j] - mn);
-                const float4 v = vv[i][j];
-                l += w;
-                o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
-            }
-            m = mn;
-            more = line[i] != 0;
-            if (more) {
-                unsigned long long rest = line[i];
-                draft_load(rest, kk[i], vv[i]);
-            }
-        }
-        reinterpret_cast<float4*>(sh.part[col])[lane] = o;
-        if (lane == 0) sh.part_m[col] = m, sh.part_l[col] = l;
+        if (lane == 0) sh.step[col] = a / Q_TOP * (SCORE_SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
+        const DraftPart a4 = draft_attend(p, b, h, lane, x, line[i], kk[i], vv[i]);
+        reinterpret_cast<float4*>(sh.part[col])[lane] = a4.o;
+        if (lane == 0) sh.part_m[col] = a4.m, sh.part_l[col] = a4.l;
     }
     __syncthreads();
 
@@ -424,8 +268,8 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         run_m[e] = NONE, run_l[e] = 0.f;
         step[e] = sh.step[gr + 8 * e], ages[e] = sh.ages[gr + 8 * e];
     }
-    for (; blk < end; blk += stride) {
-        cp_wait1();
+    for (; blk < nblk; blk += stride) {
+        cp_wait<1>();
         __syncwarp();
         // scores of the warp's own keys, without the column's step: T[j][..] for keys 8 j + 2 c, + 1 of its 32
         float T[4][VALS], vs[4][2];
@@ -491,7 +335,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         __syncwarp();
         // the next block's K and scales take this block's place
         const int next = blk + stride;
-        if (next < end) fetch_k(next);
+        if (next < nblk) fetch_k(next);
         cp_commit();
         // softmax of the block: weights relative to its largest score and value scale, over both warps' keys
         float vmax = TINY, tm[HALVES];
@@ -554,7 +398,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
             if (!W16) pd[d][1] = pd[d][3] = 0u;
             sh.px[pair][half][d][lane] = make_uint4(pd[d][0], pd[d][1], pd[d][2], pd[d][3]);
         }
-        cp_wait1();
+        cp_wait<1>();
         named_bar_sync(1 + pair, 64);   // both warps' digits and values are there
         uint32_t pa[2][3][4];
 #pragma unroll
@@ -594,7 +438,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
                 }
             }
         named_bar_sync(1 + pair, 64);   // both have read the values: the next block's take their place
-        if (next < end) fetch_v(next);
+        if (next < nblk) fetch_v(next);
         cp_commit();
         bool moved = false;   // a new maximum rescales what there is; mostly there is none
 #pragma unroll
@@ -618,7 +462,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         }
     }
     // ---- join the pairs: partial outputs at [column][t * 8 + dim / 16], dim = 16 * (dim / 16) + t
-    cp_wait0();
+    cp_wait<0>();
     named_bar_sync(1 + pair, 64);
     {
         float* po = reinterpret_cast<float*>(stage);
@@ -636,7 +480,6 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         }
     }
     __syncthreads();
-    float* mine = p.part ? p.part + ((size_t)blockIdx.x * 2 + head) * PART_FLOATS : nullptr;   // ranges' partial result
     if (tid < cols) {   // a column's maximum, the parts' factors, its sum
         const int col = tid;
         const float pm = sh.part_m[col];
@@ -652,7 +495,6 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
             l = fmaf(f, sh.warp_l[2 * w][col] + sh.warp_l[2 * w + 1][col], l);
         }
         sh.part_m[col] = M, sh.part_l[col] = l;
-        if (p.part && !complete) mine[col] = M, mine[PART_L + col] = l;
     }
     __syncthreads();
     for (int i = tid; i < cols * RD; i += PT) {
@@ -663,11 +505,9 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
             o = fmaf(sh.pair_f[w][col], reinterpret_cast<const float*>(smem + w * St::BYTES)[col * PAD + (d & 15) * 8 + (d >> 4)], o);
         if (p.S > 1) {
             sh.part[col][d] = o;
-        } else if (complete) {
+        } else {
             const int node = (col0 + col) / p.G;
             if (node < L) p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + d] = o / sh.part_l[col];
-        } else {
-            mine[PART_O + i] = o;
         }
     }
     if (p.S > 1) {
@@ -692,57 +532,13 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         }
         cluster_sync();   // no CTA leaves while another reads its shared memory
     }
-    }
-    // ---- the range's next unit
-    left -= last - first;
-    again = p.part && left > 0;
-    at.block = 0;
-    if (++at.unit == p.hk * p.groups) at.unit = 0, ++at.b;
-    __syncthreads();
-  }
-}
-
-// Joins the partial results of the units that the ranges' cuts divide.
-__global__ void __launch_bounds__(JT) rswa_tree_join_kernel(const __grid_constant__ TreeParams p, int ctas) {
-    __shared__ int scan[JT / 32 + 4];
-    const int tid = threadIdx.x, per_b = p.hk * p.groups, b = blockIdx.x / per_b, unit = blockIdx.x % per_b;
-    pdl_wait();
-    // the unit's blocks in the row of all blocks, and the CTAs that had them
-    int all = 0, before = 0;
-    for (int i = tid; i < p.B; i += JT) {
-        const int own = sequence_blocks(p, i);
-        all += own;
-        if (i < b) before += own;
-    }
-    all = cta_scan<JT / 32>(all, scan) * per_b;
-    before = cta_scan<JT / 32>(before, scan);
-    const int own = sequence_blocks(p, b), per = (all + ctas - 1) / ctas;
-    const int64_t from = (int64_t)before * per_b + (int64_t)unit * own;
-    const int c0 = (int)(from / per), c1 = (int)((from + own - 1) / per);
-    const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b), L = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
-    const int par = tid < p.N && p.parent ? __ldg(p.parent + (size_t)b * p.N + tid) : tid - 1;
-    const bool bad = __syncthreads_or(R < 0 || R > p.ref.cap || n < 0 || L < 0 || L > p.N || (tid < L && (par < -1 || par >= tid)));
-    if (bad || c0 == c1) return;
-    const int h = unit / p.groups, col0 = unit % p.groups * COLS, cols = min(COLS, p.N * p.G - col0);
-    for (int col = blockIdx.y; col < cols; col += gridDim.y) {
-        const int node = (col0 + col) / p.G;
-        if (node >= L) return;
-        float M = NONE, l = 0.f, o = 0.f;
-        for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part + ((size_t)c * 2 + (c == c0)) * PART_FLOATS + col));
-        for (int c = c0; c <= c1; ++c) {
-            const float* part = p.part + ((size_t)c * 2 + (c == c0)) * PART_FLOATS;
-            const float f = ex2(__ldcg(part + col) - M);
-            l = fmaf(f, __ldcg(part + PART_L + col), l);
-            o = fmaf(f, __ldcg(part + PART_O + col * RD + tid), o);
-        }
-        p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = o / l;
-    }
 }
 
 // How a call is split, from its sizes alone: a cluster for each unit while all of them fit the device at once (two CTAs
-// per SM) with at most two blocks a pair, else ranges, one for each resident CTA.
+// per SM) with at most two blocks a pair, else the many-units kernel.
 struct TreePlan {
-    int groups, S, ctas;   // ctas: of the ranges, or 0 for clusters
+    int groups, S;
+    bool wide;
 };
 TreePlan tree_plan(int B, int N, int heads_q, int heads, int cap) {
     const int sms = device_sms() > 0 ? device_sms() : 148;
@@ -752,9 +548,8 @@ TreePlan tree_plan(int B, int N, int heads_q, int heads, int cap) {
     const int blocks = (cap + BLK - 1) / BLK + RW / BLK;
     pl.S = 1;
     while (pl.S < 8 && pl.S * PAIRS < blocks) pl.S *= 2;
-    pl.ctas = 0;
     while (pl.S > 1 && units * pl.S > 2 * sms) pl.S /= 2;
-    if (blocks > 2 * pl.S * PAIRS) pl.S = 1, pl.ctas = 2 * sms;
+    pl.wide = blocks > 2 * pl.S * PAIRS;
     return pl;
 }
 
@@ -762,21 +557,15 @@ template <bool INT4, bool W16>
 cudaError_t launch_tree(TreeParams& p, const TreePlan& pl, cudaStream_t st) {
     const void* fn = (const void*)rswa_tree_kernel<INT4, W16>;
     const size_t smem = PAIRS * Stage<INT4>::BYTES + sizeof(Shared);
-    cudaError_t e = once_per_device(fn, [&] {
+    const cudaError_t e = once_per_device(fn, [&] {
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess) return e;
     p.groups = pl.groups, p.S = pl.S;
-    const unsigned units = (unsigned)p.B * p.hk * p.groups;
     void* args[] = {&p};
-    if (!pl.ctas) return launch_kernel(fn, dim3(units * p.S), dim3(PT), smem, p.S, args, st);
-    e = launch_kernel(fn, dim3((unsigned)pl.ctas), dim3(PT), smem, 1, args, st);
-    if (e != cudaSuccess) return e;
-    int ctas = pl.ctas;
-    void* more[] = {&p, &ctas};
-    const int cols = p.N * p.G < COLS ? p.N * p.G : COLS;
-    return launch_kernel((const void*)rswa_tree_join_kernel, dim3(units, cols < 4 ? cols : 4), dim3(JT), 0, 1, more, st);
+    return launch_kernel(fn, dim3((unsigned)p.B * p.hk * p.groups * p.S), dim3(PT), smem, p.S, args, st);
 }
+
 }  // namespace
 }  // namespace focr
 
@@ -785,8 +574,7 @@ extern "C" size_t focr_rswa_tree_workspace_bytes(int32_t B, int32_t N, int32_t h
     if (B < 1 || N < 1 || heads < 1 || heads_q < heads || heads_q > FOCR_HEADS_MAX || B > FOCR_RSWA_B_MAX ||
         ref_cap > FOCR_RSWA_RCAP_MAX || N > TREE_MAX)
         return 0;
-    const TreePlan pl = tree_plan(B, N, heads_q, heads, ref_cap);
-    return ((size_t)pl.ctas * 2 * PART_FLOATS * sizeof(float) + 255) & ~(size_t)255;
+    return tree_plan(B, N, heads_q, heads, ref_cap).wide ? wide_part_bytes() : 0;
 }
 
 extern "C" focr_status focr_rswa_tree(const float* q, const float* k_new, const float* v_new, int32_t B, int32_t N,
@@ -824,10 +612,11 @@ extern "C" focr_status focr_rswa_tree(const float* q, const float* k_new, const 
     if (need && (!workspace || misaligned(workspace, 256) || ws_bytes < need))
         return reportf(FOCR_ERR_INVALID_ARG, "workspace of %zu bytes (256-byte aligned) is needed, got %zu", need, ws_bytes);
     p.out = out, p.B = B, p.N = N, p.hq = heads_q, p.hk = ref->heads, p.G = G;
-    p.part = pl.ctas ? reinterpret_cast<float*>(workspace) : nullptr;
+    p.part = reinterpret_cast<float*>(workspace);
     const bool wide = N * G > 8, int4 = ref->type == FOCR_W_INT4;
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = int4 ? (wide ? launch_tree<true, true>(p, pl, st) : launch_tree<true, false>(p, pl, st))
-                               : (wide ? launch_tree<false, true>(p, pl, st) : launch_tree<false, false>(p, pl, st));
+    const cudaError_t e = pl.wide ? launch_wide(p, int4, st)
+                          : int4  ? (wide ? launch_tree<true, true>(p, pl, st) : launch_tree<true, false>(p, pl, st))
+                                  : (wide ? launch_tree<false, true>(p, pl, st) : launch_tree<false, false>(p, pl, st));
     return report_launch(e, "rswa_tree_kernel");
 }
