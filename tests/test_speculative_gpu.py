@@ -206,14 +206,14 @@ def check_tree(seed, B, N, hq, hk, Rcap, ref_len, n_gen, int4=False, parent="ran
     out = torch.full((B, N, hq, 128), 7.0, device="cuda")
     api.focr_rswa_tree(dev(q), dev(k), dev(v), dev_cache(ref), ints(ref_len), dev_cache(ring), ints(n_gen), ints(parent),
                        ints(n_nodes), out=out)
-    val = lambda c: tuple(np.nan_to_num(sp.values(c[i], c[i + 1])) for i in (0, 2))  # noqa: E731
-    want = sp.rswa_tree(q, k, v, val(ref), ref_len, val(ring), n_gen, parent, n_nodes)
+    ref, ring = (tuple(np.nan_to_num(sp.values(c[i], c[i + 1])) for i in (0, 2)) for c in (ref, ring))
+    want = sp.rswa_tree(q, k, v, ref, ref_len, ring, n_gen, parent, n_nodes)
     got = out.cpu().numpy().astype(np.float64)
     for b in range(B):
         L = N if n_nodes is None else n_nodes[b]
         assert (got[b, L:] == 7.0).all()
         if L:
-            vmax = max(np.abs(val(ref)[1][b]).max(initial=0.0), np.abs(val(ring)[1][b]).max(), np.abs(v[b, :L]).max())
+            vmax = max(np.abs(ref[1][b]).max(initial=0.0), np.abs(ring[1][b]).max(), np.abs(v[b, :L]).max())
             assert np.abs(got[b, :L] - want[b, :L]).max() <= TOL_TREE * max(1.0, qscale) * vmax, b
     return got
 

@@ -10,16 +10,18 @@
 // rows x 16 bytes, 128 bytes each, chunk j of row r at (r / 8) * (row group) + j * 128 + (r % 8) * 16.
 //
 // The softmax has no maximum per tile: a column's reference m is a bound that its scores (base 2) may not exceed; a
-// tile with a larger score (or value scale) first moves the bound to MARGIN above it and brings O and the sum along.
-// The weight 2^(s - m) vs / vref is then at most 1 and is written with 24 bits, so a weight is off by 2^-25 of the
-// bound, at most 2^-23.8 of the largest weight.  O stays in s32 while the bounds stand (at most 65536 keys a unit: |sum| <=
-// 33024 * 255 * 128 < 2^31) and is added to fp32 registers when they move and at the unit's end.
+// tile with a larger score (or value scale) first moves the bound above it and brings O and the sum along.  The weight
+// 2^(s - m) vs / vref is then at most 1 and is written with 24 bits.  The first bound of a column leaves two bits, as the
+// largest of many scores lies about that far above the largest of a tile's; later ones leave one.  O stays in s32 while
+// the bounds stand (at most 33024 keys a unit: |sum| <= 33024 * 255 * 128 < 2^31) and is added to fp32 when they move
+// and at the unit's end.
 //
-// Roles of a CTA (one per SM): warps 0-7 softmax (thread = key row of S, dim row of O; warps 0-3 have the first half of
-// the columns, 4-7 the second), warps 8-11 load (cp.async; int4 is unpacked to bytes 16 q on the way), warp 12 issues
-// the MMAs.  All tiles of all units form one row, cut into equal ranges, one per CTA (the lengths are read on the
-// device, so ragged batches stay balanced); units that a cut divides leave partial results in the workspace, and a
-// second kernel joins them.  Every wait is bounded; one that runs out turns the CTA's results into NaN.
+// Roles of a CTA (one per SM): warps 0-3 and 4-7 are two softmax workers (thread = key row of S, dim row of O), which
+// take the tiles in turn, each with its own S, O, bounds and sums, so one's latencies run under the other's work; warps
+// 8-11 load (cp.async; int4 is unpacked to bytes 16 q on the way); warp 12 issues the MMAs.  A unit is one kv head of one
+// sequence with up to 32 columns.  All tiles of all units form one row, cut into equal ranges, one per CTA (the lengths
+// are read on the device, so ragged batches stay balanced); units that a cut divides leave partial results in the
+// workspace, and a second kernel joins them.  Every wait is bounded; one that runs out turns the CTA's results into NaN.
 #include <math.h>
 
 #include "abi_util.h"
@@ -35,11 +37,11 @@ constexpr int RD = TREE_DIM, RW = TREE_RING, TILE = 128;
 constexpr int SOFT = 8, LOADERS = 4, WARPS = SOFT + LOADERS + 1, PT = 32 * WARPS;
 constexpr int ST = 32 * SOFT, LT = 32 * LOADERS;
 constexpr int JT = 128;                       // threads of the joining kernel
-constexpr int CMAX = TREE_MAX;                // columns of a unit
-constexpr float MARGIN = 1.f;                 // bounds are set this far (log2) above the largest score seen
-constexpr float V_MARGIN = 1.125f;            // and the value scales' bound this factor above the largest one
+constexpr int CMAX = 32;                      // columns of a unit
+constexpr float MARGIN_FIRST = 2.f, MARGIN = 1.f;   // log2 that a bound leaves above the largest score seen
+constexpr float V_MARGIN = 1.125f;            // and the value scales' bound above the largest one
 constexpr uint64_t LIMIT_NS = 2000000000ull;  // bound of every wait
-// A partial result: the columns' bounds, sums and unnormalised outputs.
+// A partial result: the columns' references, sums and unnormalised outputs.
 constexpr int PART_L = CMAX, PART_O = 2 * CMAX, PART_FLOATS = 2 * CMAX + CMAX * RD;
 
 // kind::i8: D s32, A s8, B s8 or u8 (b_signed); ta, tb: operand read along its other axis.
@@ -66,36 +68,55 @@ __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.
 __device__ __forceinline__ void st8(uint32_t taddr, int v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%1,%1,%1,%1,%1,%1,%1};" ::"r"(taddr), "r"(v) : "memory");
 }
-// a barrier of the softmax threads that also tells whether any of them said so
-__device__ __forceinline__ bool any_of_softmax(bool mine) {
+__device__ __forceinline__ void st8(uint32_t taddr, const float (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+// a barrier of a worker's threads that also tells whether any of them said so
+__device__ __forceinline__ bool any_of_worker(int worker, bool mine) {
     uint32_t r;
     __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 q, %1, 0;\n\t"
-        "barrier.cta.red.or.pred p, 1, 256, q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "barrier.cta.red.or.pred p, %1, 128, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)mine)
+        : "r"(2 + worker), "r"((uint32_t)mine)
         : "memory");
     __syncwarp();
     return r != 0;
 }
-__device__ __forceinline__ void softmax_sync() {
+__device__ __forceinline__ void worker_sync(int worker) {
+    __syncwarp();
+    named_bar_sync(2 + worker, ST / 2);
+}
+__device__ __forceinline__ void softmax_sync() {   // both workers
     __syncwarp();
     named_bar_sync(1, ST);
+}
+// the largest of the warp's values (integers that order as the floats do)
+__device__ __forceinline__ float warp_max(float x) {
+    int i = __float_as_int(x);
+    i ^= (i >> 31) & 0x7fffffff;
+    i = __reduce_max_sync(0xffffffffu, i);
+    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
 }
 
 template <bool INT4, int CP>
 struct Sizes {
     static constexpr int N = 3 * CP;                                  // columns in digits
-    static constexpr int STAGES = INT4 ? 2 : CP <= 32 ? 4 : 3;        // tiles of bytes
-    static constexpr int PACKED = INT4 ? 4 : 1;                       // tiles of nibbles on their way
-    static constexpr int SBUF = 3 * N <= 512 ? 2 : 1;                 // score buffers in tensor memory
+    static constexpr int STAGES = INT4 ? 3 : 4;                       // tiles of bytes (3 at least: S runs two tiles ahead of P V)
+    static constexpr int PACKED = 3;                                  // int4: tiles of nibbles on their way
     static constexpr int KV = TILE * RD;                              // bytes of K (or V) of a tile
     static constexpr int STAGE = 2 * KV;
     static constexpr int PACK = 2 * KV / 2 + 8 * TILE;                // nibbles of K and V, and scales
-    static constexpr int Q_OFF = STAGES * STAGE + (INT4 ? PACKED * PACK : 0), P_OFF = Q_OFF + N * RD, S_OFF = P_OFF + N * TILE;
+    static constexpr int Q_OFF = STAGES * STAGE + (INT4 ? PACKED * PACK : 0), P_OFF = Q_OFF + N * RD, S_OFF = P_OFF + 2 * N * TILE;
+    // tensor memory: each worker's S, O and fp32 sums
+    static constexpr int T_O = 2 * N, T_ACC = 4 * N;
+    static_assert(4 * N + 2 * CP <= 512, "tensor memory");
+    static_assert(CP * RD * 4 <= 2 * N * TILE, "a worker's results fit where the weights were");
 };
 
 template <int CP>
@@ -103,16 +124,18 @@ struct Shared {
     float part[CP][RD];                  // the drafted keys' part
     float part_m[CP], part_l[CP];
     float scales[4][2][TILE];            // of the stages' tiles: ks, vs
-    float2 col[CP];                      // a column's step (score in log2 = dot * key scale * step) and bound
-    float alpha[CP];                     // what a moved bound does to the column's sums
-    float red[SOFT][CP / 2 + 1];
+    float2 col[2][CP];                   // a column's step (score in log2 = dot * key scale * step) and each worker's bound
+    float2 moved[2][CP];                 // bounds that moved: by how much, and the factor for the column's sums
+    float red[2][4][CP + 1];
+    float4 factor[CP];                   // of the workers' and the drafted keys' parts, and of the result
+    float total_m[CP], total_l[CP];
     int ages[CP];                        // ring slots younger than this are seen
     unsigned long long line[TREE_MAX];
     int par[TREE_MAX];
-    uint64_t full[4], empty[4], s_full[2], s_free[2], p_full, p_free, q_full;
+    uint64_t full[4], empty[4], s_full[2], s_free[2], p_full[2], p_free[2], q_full;
     int scan[WARPS + 4];
-    float vref;                          // bound of the value scales
-    int fresh;                           // the next P V starts O anew
+    float vref[2];                       // bounds of the value scales
+    int fresh[2];                        // the next P V starts O anew
     int gave_up;
     uint32_t tmem;
 };
@@ -144,22 +167,23 @@ __device__ __forceinline__ int cta_scan(int& mine, int* scan) {
     return total;
 }
 struct Place {   // a tile in the row of all units' tiles
-    int b, h, tile;
+    int b, unit, tile;   // unit of the sequence: kv head * groups + column group
 };
 __device__ int all_tiles(const TreeParams& p, int* scan) {
     int mine = 0;
     for (int b = threadIdx.x; b < p.B; b += PT) mine += sequence_tiles(p, b);
-    return cta_scan<WARPS>(mine, scan) * p.hk;
+    return cta_scan<WARPS>(mine, scan) * p.hk * p.groups;
 }
 __device__ Place find_tile(const TreeParams& p, int at, int* scan) {
+    const int per = p.hk * p.groups;
     int before = 0;
     for (int b0 = 0; b0 < p.B; b0 += PT) {
         const int b = b0 + threadIdx.x, own = b < p.B ? sequence_tiles(p, b) : 0;
         int sum = own;
         const int total = cta_scan<WARPS>(sum, scan);
-        if ((int64_t)(before + total) * p.hk > at) {
-            const int64_t first = (int64_t)(before + sum - own) * p.hk;
-            if (at >= first && at < first + (int64_t)own * p.hk) scan[WARPS] = b, scan[WARPS + 1] = (int)(at - first), scan[WARPS + 2] = own;
+        if ((int64_t)(before + total) * per > at) {
+            const int64_t first = (int64_t)(before + sum - own) * per;
+            if (at >= first && at < first + (int64_t)own * per) scan[WARPS] = b, scan[WARPS + 1] = (int)(at - first), scan[WARPS + 2] = own;
             __syncthreads();
             const Place x{scan[WARPS], scan[WARPS + 1] / scan[WARPS + 2], scan[WARPS + 1] % scan[WARPS + 2]};
             __syncthreads();
@@ -173,14 +197,15 @@ __device__ Place find_tile(const TreeParams& p, int at, int* scan) {
 // The part of a unit that a CTA has.  Every warp reads it for itself.
 struct Segment {
     int b, h, R, n, L;
+    int col0, cols;        // its columns
     int first, count;      // its tiles of keys
     int taken;             // tiles of the range that it uses up
-    bool bad, head, complete;
+    bool bad, dead, head, complete;   // dead: nothing to compute
 };
 __device__ Segment segment_at(const TreeParams& p, const Place& at, int left) {
     Segment s;
     const int lane = threadIdx.x & 31;
-    s.b = at.b, s.h = at.h;
+    s.b = at.b, s.h = at.unit / p.groups, s.col0 = at.unit % p.groups * CMAX, s.cols = min(CMAX, p.N * p.G - s.col0);
     s.R = __ldg(p.ref_len + s.b), s.n = __ldg(p.n_gen + s.b), s.L = p.n_nodes ? __ldg(p.n_nodes + s.b) : p.N;
     s.bad = s.R < 0 || s.R > p.ref.cap || s.n < 0 || s.L < 0 || s.L > p.N;
     if (p.parent) {
@@ -193,7 +218,8 @@ __device__ Segment segment_at(const TreeParams& p, const Place& at, int left) {
     }
     const int all = sequence_tiles(p, s.b);
     s.first = at.tile, s.taken = min(left, all - at.tile);
-    const int keys = s.bad || s.L == 0 ? 0 : (s.R + TILE - 1) / TILE + (s.n > 0);
+    s.dead = s.bad || s.col0 / p.G >= s.L;
+    const int keys = s.dead ? 0 : (s.R + TILE - 1) / TILE + (s.n > 0);
     s.count = max(0, min(s.first + s.taken, keys) - s.first);
     s.head = s.first == 0, s.complete = s.head && s.taken == all;
     return s;
@@ -201,7 +227,7 @@ __device__ Segment segment_at(const TreeParams& p, const Place& at, int left) {
 __device__ __forceinline__ void advance(const TreeParams& p, Place& at, int& left, const Segment& s) {
     left -= s.taken;
     at.tile = 0;
-    if (++at.h == p.hk) at.h = 0, ++at.b;
+    if (++at.unit == p.hk * p.groups) at.unit = 0, ++at.b;
 }
 // Row of the cache where tile t of a segment's unit starts, its rows that hold a key, and whether it is the ring.
 struct TileAt {
@@ -220,20 +246,20 @@ template <bool INT4, int CP>
 __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant__ TreeParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     using Z = Sizes<INT4, CP>;
-    constexpr int N = Z::N, STAGES = Z::STAGES, HALF = CP / 2;   // HALF: columns of a softmax thread
+    constexpr int N = Z::N, STAGES = Z::STAGES;
     Shared<CP>& sh = *reinterpret_cast<Shared<CP>*>(smem + Z::S_OFF);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int cols = p.N * p.G;
 
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) mbar_init(&sh.full[i], LT), mbar_init(&sh.empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.s_free[i], SOFT);
-        mbar_init(&sh.p_full, SOFT);
-        mbar_init(&sh.p_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1), mbar_init(&sh.s_free[i], SOFT / 2);
+            mbar_init(&sh.p_full[i], SOFT / 2), mbar_init(&sh.p_free[i], 1);
+            sh.fresh[i] = 1;
+        }
         mbar_init(&sh.q_full, SOFT);
         fence_barrier_init();
         sh.gave_up = 0;
-        sh.fresh = 1;
     }
     if (warp == SOFT + LOADERS) umma::tmem_alloc(smem_u32(&sh.tmem), 512);
     pdl_wait();
@@ -244,7 +270,7 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
-    const uint32_t tmem = sh.tmem, tmem_o = tmem + Z::SBUF * N;
+    const uint32_t tmem = sh.tmem;
     int left = mine;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (mbar_wait_bounded(bar, parity, LIMIT_NS)) return true;
@@ -254,52 +280,59 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
 
     if (warp < SOFT) {
         // ------------------------------------------------------------ softmax
-        const int wg = warp >> 2, row = (warp & 3) * 32 + lane, c0 = wg * HALF;
-        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const int me = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), t_s = lanes + me * N, t_o = lanes + Z::T_O + me * N,
+                       t_acc = lanes + Z::T_ACC + me * CP;
         const int dim = INT4 ? 32 * (row / 32) + 2 * (row % 16) + ((row / 16) & 1) : row;   // of the thread's lane of O
         uint8_t* sq = smem + Z::Q_OFF;
-        uint8_t* sp = smem + Z::P_OFF;
-        auto preset = [&](int buf) {   // S accumulates onto the pattern that reads as MAGIC + sum
+        uint8_t* sp = smem + Z::P_OFF + me * N * TILE;
+        auto preset = [&] {   // S accumulates onto the pattern that reads as MAGIC + sum
 #pragma unroll
-            for (int d = 0; d < 3; ++d)
-#pragma unroll
-                for (int c = 0; c < HALF; c += 8) st8(lanes + buf * N + d * CP + c0 + c, MAGIC_BITS);
+            for (int c = 0; c < N; c += 8) st8(t_s + c, MAGIC_BITS);
             umma::wait_st();
             umma::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.s_free[buf]);
+            if (lane == 0) mbar_arrive(&sh.s_free[me]);
         };
-        for (int i = 0; i < Z::SBUF; ++i) preset(i);
-        int it = 0;   // tiles so far
+        preset();
+        int it = 0, k = 0;   // tiles of the CTA before this segment; this worker's tiles so far
         bool ok = true;
-        while (left > 0 && ok) {
+        while (left > 0 && ok) {   // left by all threads at once
             const Segment s = segment_at(p, at, left);
-            const bool dead = s.bad || s.L == 0;
             if (s.bad && s.head) {
-                const int live = s.L < 0 || s.L > p.N ? p.N : s.L;
-                for (int i = tid; i < live * p.G * RD; i += ST)
-                    p.out[(((size_t)s.b * p.N + i / RD / p.G) * p.hq + s.h * p.G + i / RD % p.G) * RD + i % RD] = __int_as_float(0x7fc00000);
+                const int live = min(s.cols, (s.L < 0 || s.L > p.N ? p.N : s.L) * p.G - s.col0);
+                for (int i = tid; i < live * RD; i += ST) {
+                    const int c = s.col0 + i / RD;
+                    p.out[(((size_t)s.b * p.N + c / p.G) * p.hq + s.h * p.G + c % p.G) * RD + i % RD] = __int_as_float(0x7fc00000);
+                }
             }
-            if (!dead) {
+            if (!s.dead) {
                 // ---- lines of the tree, query digits, drafted keys
                 if (tid < s.L) sh.par[tid] = p.parent ? __ldg(p.parent + (size_t)s.b * p.N + tid) : tid - 1;
+                float4 q[CP / SOFT];
+#pragma unroll
+                for (int i = 0; i < CP / SOFT; ++i) {
+                    const int c = warp + i * SOFT, node = (s.col0 + c) / p.G;
+                    q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c < s.cols && node < s.L)
+                        q[i] = __ldg(reinterpret_cast<const float4*>(p.q + (((size_t)s.b * p.N + node) * p.hq + s.h * p.G + (s.col0 + c) % p.G) * RD) + lane);
+                }
                 softmax_sync();
                 if (tid < s.L) {
                     unsigned long long line = 0;
                     for (int j = tid; j >= 0; j = sh.par[j]) line |= 1ull << j;
                     sh.line[tid] = line;
                 }
-                if (tid == 0) sh.vref = TINY;
+                if (tid < 2) sh.vref[tid] = TINY;
                 softmax_sync();
-                for (int cb = warp; cb < CP; cb += 2 * SOFT) {   // two columns at a time
-                    float4 q[2], k4[2][4], v4[2][4];
+#pragma unroll
+                for (int i0 = 0; i0 < CP / SOFT; i0 += 2) {   // two columns at a time
+                    float4 k4[2][4], v4[2][4];
                     unsigned long long line[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int c = cb + i * SOFT, node = c / p.G;
-                        const bool live = c < cols && node < s.L;
-                        q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (live) q[i] = __ldg(reinterpret_cast<const float4*>(p.q + (((size_t)s.b * p.N + node) * p.hq + s.h * p.G + c % p.G) * RD) + lane);
+                        const int c = warp + (i0 + i) * SOFT, node = (s.col0 + c) / p.G;
+                        const bool live = c < s.cols && node < s.L;
                         line[i] = live && s.head ? sh.line[node] : 0ull;
                         unsigned long long rest = line[i];
                         draft_load(p, s.b, s.h, lane, rest, k4[i], v4[i]);
@@ -307,8 +340,8 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int c = cb + i * SOFT;
-                        const float4 x = q[i];
+                        const int c = warp + (i0 + i) * SOFT;
+                        const float4 x = q[i0 + i];
                         float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
                         for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
@@ -334,7 +367,8 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                                 *reinterpret_cast<uint32_t*>(at8 + (lane >> 2) * 128 + 4 * (lane & 3)) = v[0] | v[1] << 8 | v[2] << 16 | v[3] << 24;
                             }
                         }
-                        if (lane == 0) sh.col[c] = make_float2(a / Q_TOP * (SCORE_SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f)), NONE);
+                        if (lane == 0)
+                            sh.col[0][c] = sh.col[1][c] = make_float2(a / Q_TOP * (SCORE_SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f)), 0.f);
                         const DraftPart dp = draft_attend(p, s.b, s.h, lane, x, line[i], k4[i], v4[i]);
                         reinterpret_cast<float4*>(sh.part[c])[lane] = dp.o;
                         if (lane == 0) sh.part_m[c] = dp.m, sh.part_l[c] = dp.l;
@@ -344,180 +378,206 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                 softmax_sync();
                 if (lane == 0 && s.count > 0) mbar_arrive(&sh.q_full);
 
-                float acc[HALF], sum[HALF];
+                float sum[CP];
 #pragma unroll
-                for (int c = 0; c < HALF; ++c) acc[c] = sum[c] = 0.f;
-                bool filled = false;   // O holds something
-                // adds O to the fp32 accumulators (every P V so far has completed)
-                auto drain = [&](float vref) {
+                for (int c = 0; c < CP; ++c) sum[c] = 0.f;
+                bool filled = false, summed = false;   // O holds something; so do the fp32 sums
+                // eight columns' O (every P V so far has completed) and earlier sums, in fp32
+                auto gather = [&](int c, float vref, float (&a)[8]) {
                     const float gain = vref * ((INT4 ? 1.f / 16.f : 1.f) / P_TOP);
-                    umma::fence_after_sync();
+                    int o2[8], o1[8], o0[8], old[8];
+                    if (filled) {
+                        ld8(t_o + c, o0);
+                        ld8(t_o + CP + c, o1);
+                        ld8(t_o + 2 * CP + c, o2);
+                    }
+                    if (summed) ld8(t_acc + c, old);
+                    wait_ld();
 #pragma unroll
-                    for (int c = 0; c < HALF; c += 8) {
-                        int o2[8], o1[8], o0[8];
-                        const uint32_t t = tmem_o + ((uint32_t)((warp & 3) * 32) << 16) + c0 + c;
-                        ld8(t, o0);
-                        ld8(t + CP, o1);
-                        ld8(t + 2 * CP, o2);
-                        wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            acc[c + j] = fmaf(fmaf((float)o2[j], 65536.f, fmaf((float)o1[j], 256.f, (float)o0[j])), gain, acc[c + j]);
+                    for (int j = 0; j < 8; ++j) {
+                        a[j] = summed ? __int_as_float(old[j]) : 0.f;
+                        if (filled) a[j] = fmaf(fmaf((float)o2[j], 65536.f, fmaf((float)o1[j], 256.f, (float)o0[j])), gain, a[j]);
                     }
                 };
-                for (int t = s.first; t < s.first + s.count; ++t, ++it) {   // left by all threads at once
-                    const int stage = it % STAGES, buf = it % Z::SBUF;
-                    const TileAt ta = tile_at(p, s, t);
-                    ok = ok && wait(&sh.full[stage], it / STAGES & 1) && wait(&sh.s_full[buf], it / Z::SBUF & 1);
-                    if (any_of_softmax(!ok)) {
-                        ok = false;
-                        break;
-                    }
+                for (int i = me; i < s.count; i += 2, ++k) {   // left by all threads of the worker at once
+                    const int stage = (it + i) % STAGES;
+                    const TileAt ta = tile_at(p, s, s.first + i);
+                    ok = ok && wait(&sh.full[stage], (it + i) / STAGES & 1) && wait(&sh.s_full[me], k & 1);
+                    __syncwarp();
                     umma::fence_after_sync();
                     const bool in = row < ta.rows;
                     const float ks = in ? sh.scales[stage][0][row] : 0.f, vs = in ? sh.scales[stage][1][row] : 0.f;
-                    float x[HALF];   // scores without the column's step
+                    float x[CP], top = -INFINITY;   // scores relative to the bounds, base 2
 #pragma unroll
-                    for (int c = 0; c < HALF; c += 8) {
+                    for (int c = 0; c < CP; c += 8) {
                         int d2[8], d1[8], d0[8];
-                        const uint32_t tc = lanes + buf * N + c0 + c;
-                        ld8(tc, d0);
-                        ld8(tc + CP, d1);
-                        ld8(tc + 2 * CP, d2);
+                        ld8(t_s + c, d0);
+                        ld8(t_s + CP + c, d1);
+                        ld8(t_s + 2 * CP + c, d2);
                         wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) x[c + j] = (upper(d2[j]) + lower(d1[j], d0[j])) * ks;
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 b = sh.col[me][c + j];
+                            x[c + j] = fmaf((upper(d2[j]) + lower(d1[j], d0[j])) * ks, b.x, -b.y);
+                        }
                     }
-                    preset(buf);
+                    preset();
                     if (ta.ring) {
                         const int age = (s.n - 1 - row) & (RW - 1);
 #pragma unroll
-                        for (int c = 0; c < HALF; ++c)
-                            if (!in || age >= sh.ages[c0 + c]) x[c] = -INFINITY;
+                        for (int c = 0; c < CP; ++c)
+                            if (!in || age >= sh.ages[c]) x[c] = -INFINITY;
                     } else if (!in) {
 #pragma unroll
-                        for (int c = 0; c < HALF; ++c) x[c] = -INFINITY;
+                        for (int c = 0; c < CP; ++c) x[c] = -INFINITY;
                     }
-                    float vref = sh.vref;
-                    bool over = vs > vref;
 #pragma unroll
-                    for (int c = 0; c < HALF; ++c) {
-                        const float2 k = sh.col[c0 + c];
-                        over |= fmaf(x[c], k.x, -k.y) > 0.f;
-                    }
-                    if (any_of_softmax(over)) {
+                    for (int c = 0; c < CP; ++c) top = fmaxf(top, x[c]);
+                    const bool first = !filled && !summed;   // the worker's first tile of the unit sets the bounds
+                    if (any_of_worker(me, first || top > 0.f || vs > sh.vref[me] || !ok)) {
                         // ---- bounds move: columns' and scales' largest values of the tile
+                        const float vref = sh.vref[me];
 #pragma unroll
-                        for (int c = 0; c < HALF; ++c) {
-                            float m = x[c];
+                        for (int c = 0; c < CP; ++c) {
+                            const float m = warp_max(x[c]);
+                            if (lane == 0) sh.red[me][warp & 3][c] = m;
+                        }
+                        const float vm = warp_max(vs);
+                        if (lane == 0) sh.red[me][warp & 3][CP] = vm;
+                        if (filled) ok = wait(&sh.p_free[me], (k - 1) & 1) && ok;
+                        __syncwarp();
+                        umma::fence_after_sync();
+                        if (any_of_worker(me, !ok)) {
+                            ok = false;
+                            break;
+                        }
+                        if (row < CP) {
+                            const float (*r)[CP + 1] = sh.red[me];
+                            const float over = fmaxf(fmaxf(r[0][row], r[1][row]), fmaxf(r[2][row], r[3][row]));   // above the bound
+                            const float2 b = sh.col[me][row];
+                            float by = over > 0.f ? over + MARGIN : 0.f;
+                            if (first) by = over == -INFINITY ? 0.f : over + MARGIN_FIRST;   // (a column without a node sees nothing)
+                            sh.moved[me][row] = make_float2(by, ex2(-by));
+                            sh.col[me][row] = make_float2(b.x, b.y + by);
+                        }
+                        if (row == 0) {
+                            const float v = fmaxf(fmaxf(sh.red[me][0][CP], sh.red[me][1][CP]), fmaxf(sh.red[me][2][CP], sh.red[me][3][CP]));
+                            if (v > vref) sh.vref[me] = V_MARGIN * v;
+                            sh.fresh[me] = 1;
+                        }
+                        worker_sync(me);
 #pragma unroll
-                            for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                            if (lane == 0) sh.red[warp][c] = m;
+                        for (int c = 0; c < CP; ++c) {
+                            const float2 by = sh.moved[me][c];
+                            x[c] -= by.x;
+                            sum[c] *= by.y;
                         }
-                        float vm = vs;
+                        if (filled || summed) {
 #pragma unroll
-                        for (int o = 16; o >= 1; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-                        if (lane == 0) sh.red[warp][HALF] = vm;
-                        if (filled) {
-                            ok = wait(&sh.p_free, (it - 1) & 1) && ok;
-                            __syncwarp();
-                            drain(vref);
-                        }
-                        softmax_sync();
-                        if (tid < CP) {
-                            const int w = tid / HALF * 4, c = tid % HALF;
-                            const float m = fmaxf(fmaxf(sh.red[w][c], sh.red[w + 1][c]), fmaxf(sh.red[w + 2][c], sh.red[w + 3][c]));
-                            const float2 k = sh.col[tid];
-                            const float now = m == -INFINITY ? NONE : m * k.x, to = now > k.y ? now + MARGIN : k.y;
-                            sh.alpha[tid] = ex2(k.y - to);
-                            sh.col[tid] = make_float2(k.x, to);
-                        }
-                        if (tid == 0) {
-                            const float v = fmaxf(fmaxf(sh.red[0][HALF], sh.red[1][HALF]), fmaxf(sh.red[2][HALF], sh.red[3][HALF]));
-                            if (v > sh.vref) sh.vref = V_MARGIN * v;
-                            sh.fresh = 1;
-                        }
-                        softmax_sync();
-                        vref = sh.vref;
+                            for (int c = 0; c < CP; c += 8) {
+                                float a[8];
+                                gather(c, vref, a);
 #pragma unroll
-                        for (int c = 0; c < HALF; ++c) {
-                            const float al = sh.alpha[c0 + c];
-                            acc[c] *= al, sum[c] *= al;
+                                for (int j = 0; j < 8; ++j) a[j] *= sh.moved[me][c + j].y;
+                                st8(t_acc + c, a);
+                            }
+                            umma::wait_st();
+                            summed = true;
                         }
                         filled = false;
                     }
                     // ---- weights: 24 bits, as three digits, [key][column] for the second product
-                    const float vn = vs * (P_TOP / vref);
-                    uint32_t w[3][HALF / 4];
+                    const float vn = vs * (P_TOP / sh.vref[me]);
+                    if (k > 0) ok = wait(&sh.p_free[me], (k - 1) & 1) && ok;   // the weights of the tile before have been used
+                    uint8_t* at8 = sp + (row >> 3) * (N / 16 * 128) + (row & 7) * 16;
 #pragma unroll
-                    for (int c = 0; c < HALF; c += 4) {
-                        uint32_t u[4];
+                    for (int c = 0; c < CP; c += 16) {
+                        uint32_t w[3][4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 k = sh.col[c0 + c + j];
-                            const float e = ex2(fmaf(x[c + j], k.x, -k.y));
-                            sum[c + j] += e;
-                            u[j] = __float2uint_rn(e * vn);
+                        for (int e = 0; e < 16; e += 4) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float y = ex2(x[c + e + j]);
+                                sum[c + e + j] += y;
+                                u[j] = __float2uint_rn(y * vn);
+                            }
+                            const uint32_t t0 = __byte_perm(u[0], u[1], 0x5140), t1 = __byte_perm(u[2], u[3], 0x5140);
+                            const uint32_t t2 = __byte_perm(u[0], u[1], 0x0062), t3 = __byte_perm(u[2], u[3], 0x0062);
+                            w[0][e / 4] = __byte_perm(t0, t1, 0x5410);
+                            w[1][e / 4] = __byte_perm(t0, t1, 0x7632);
+                            w[2][e / 4] = __byte_perm(t2, t3, 0x5410);
                         }
-                        const uint32_t t0 = __byte_perm(u[0], u[1], 0x5140), t1 = __byte_perm(u[2], u[3], 0x5140);
-                        const uint32_t t2 = __byte_perm(u[0], u[1], 0x0062), t3 = __byte_perm(u[2], u[3], 0x0062);
-                        w[0][c / 4] = __byte_perm(t0, t1, 0x5410);
-                        w[1][c / 4] = __byte_perm(t0, t1, 0x7632);
-                        w[2][c / 4] = __byte_perm(t2, t3, 0x5410);
-                    }
-                    if (it > 0) ok = wait(&sh.p_free, (it - 1) & 1) && ok;   // the weights of the tile before have been used
-                    {
-                        uint8_t* at8 = sp + (row >> 3) * (N / 16 * 128) + (row & 7) * 16;
 #pragma unroll
-                        for (int d = 0; d < 3; ++d) {
-                            const int n = d * CP + c0;   // a multiple of 8; 16 columns a chunk
-#pragma unroll
-                            for (int c = 0; c < HALF; c += 8)
-                                *reinterpret_cast<uint2*>(at8 + ((n + c) >> 4) * 128 + ((n + c) & 15)) = make_uint2(w[d][c / 4], w[d][c / 4 + 1]);
-                        }
+                        for (int d = 0; d < 3; ++d)
+                            *reinterpret_cast<uint4*>(at8 + (d * CP + c) / 16 * 128) = make_uint4(w[d][0], w[d][1], w[d][2], w[d][3]);
                     }
                     umma::fence_smem_to_async();
                     umma::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.p_full);
+                    if (lane == 0) mbar_arrive(&sh.p_full[me]);
                     filled = true;
                 }
-                if (filled && ok) {
-                    ok = wait(&sh.p_free, (it - 1) & 1);
-                    __syncwarp();
-                    drain(sh.vref);
-                }
-                if (any_of_softmax(!ok)) {
-                    ok = false;
-                    break;
-                }
                 // ---- the unit's sums, and the drafted keys
+                if (filled) ok = ok && wait(&sh.p_free[me], (k - 1) & 1);
+                __syncwarp();
+                umma::fence_after_sync();
 #pragma unroll
-                for (int c = 0; c < HALF; ++c) {
+                for (int c = 0; c < CP; ++c) {
                     float l = sum[c];
 #pragma unroll
                     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                    if (lane == 0) sh.red[warp][c] = l;
+                    if (lane == 0) sh.red[me][warp & 3][c] = l;
                 }
+                if (!ok) sh.gave_up = 1;
                 softmax_sync();
-                float* part = p.part + ((size_t)blockIdx.x * 2 + s.head) * PART_FLOATS;
+                ok = *(volatile int*)&sh.gave_up == 0;
+                float* other = reinterpret_cast<float*>(smem + Z::P_OFF);   // worker 1's results, where the weights were
+                if (tid < CP) {
+                    const int c = tid;
+                    const float m0 = s.count > 0 ? sh.col[0][c].y : NONE, m1 = s.count > 1 ? sh.col[1][c].y : NONE, pm = sh.part_m[c], M = fmaxf(fmaxf(m0, m1), pm);
+                    const float f0 = ex2(m0 - M), f1 = ex2(m1 - M), g = ex2(pm - M);
+                    const float l0 = (sh.red[0][0][c] + sh.red[0][1][c]) + (sh.red[0][2][c] + sh.red[0][3][c]);
+                    const float l1 = (sh.red[1][0][c] + sh.red[1][1][c]) + (sh.red[1][2][c] + sh.red[1][3][c]);
+                    const float l = fmaf(f0, l0, fmaf(f1, l1, g * sh.part_l[c])), r = s.complete ? 1.f / l : 1.f;
+                    sh.factor[c] = make_float4(f0 * r, f1 * r, g * r, 0.f);
+                    sh.total_m[c] = M, sh.total_l[c] = l;
+                }
+                if (me == 1) {
 #pragma unroll
-                for (int c = 0; c < HALF; ++c) {
-                    const int cc = c0 + c, node = cc / p.G;
-                    if (cc >= cols || node >= s.L) continue;
-                    const float l = (sh.red[4 * wg][c] + sh.red[4 * wg + 1][c]) + (sh.red[4 * wg + 2][c] + sh.red[4 * wg + 3][c]);
-                    const float m = sh.col[cc].y, pm = sh.part_m[cc], M = fmaxf(m, pm), f = ex2(m - M), g = ex2(pm - M);
-                    const float lt = fmaf(f, l, g * sh.part_l[cc]), o = fmaf(f, acc[c], g * sh.part[cc][dim]);
-                    if (s.complete) {
-                        p.out[(((size_t)s.b * p.N + node) * p.hq + s.h * p.G + cc % p.G) * RD + dim] = o / lt;
-                    } else {
-                        part[PART_O + cc * RD + dim] = o;
-                        if (row == 0) part[cc] = M, part[PART_L + cc] = lt;
+                    for (int c = 0; c < CP; c += 8) {
+                        float a[8];
+                        gather(c, sh.vref[1], a);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) other[(c + j) * RD + row] = a[j];
                     }
                 }
-                if (tid == 0) sh.fresh = 1;
+                softmax_sync();
+                if (me == 0) {
+                    float* part = p.part + ((size_t)blockIdx.x * 2 + s.head) * PART_FLOATS;
+#pragma unroll
+                    for (int c = 0; c < CP; c += 8) {
+                        float a[8];
+                        gather(c, sh.vref[0], a);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int cc = c + j, x = s.col0 + cc, node = x / p.G;
+                            if (cc >= s.cols || node >= s.L) continue;
+                            const float4 f = sh.factor[cc];
+                            const float o = fmaf(f.x, a[j], fmaf(f.y, other[cc * RD + row], f.z * sh.part[cc][dim]));
+                            if (s.complete) {
+                                p.out[(((size_t)s.b * p.N + node) * p.hq + s.h * p.G + x % p.G) * RD + dim] = o;
+                            } else {
+                                part[PART_O + cc * RD + dim] = o;
+                                if (row == 0) part[cc] = sh.total_m[cc], part[PART_L + cc] = sh.total_l[cc];
+                            }
+                        }
+                    }
+                }
+                if (tid < 2) sh.fresh[tid] = 1;
                 softmax_sync();
             }
+            it += s.count;
             advance(p, at, left, s);
         }
     } else if (warp < SOFT + LOADERS) {
@@ -613,7 +673,7 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                 for (int tile = s.first; tile < s.first + s.count && ok; ++tile, ++it) {
                     const int stage = it % STAGES;
                     issue();
-                    cp_wait<3>();   // PACKED - 1 younger tiles may be on their way
+                    cp_wait<Z::PACKED - 1>();   // that many younger tiles may be on their way
                     if (it >= STAGES) ok = wait(&sh.empty[stage], (it / STAGES - 1) & 1);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
@@ -641,22 +701,23 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
     } else {
         // ------------------------------------------------------------ products
         constexpr uint32_t IS = idesc_i8(N, true, false, false), IO = idesc_i8(N, false, true, true);
-        const uint32_t sq = smem_u32(smem) + Z::Q_OFF, sp = smem_u32(smem) + Z::P_OFF;
-        int it = 0, seg = 0;
+        const uint32_t sq = smem_u32(smem) + Z::Q_OFF;
+        int it = 0, seg = 0, scores[2] = {0, 0}, done[2] = {0, 0};   // tiles before the segment; each worker's so far
         bool ok = true;
-        auto values = [&](int i) {   // O += V^T P of tile i
-            const int stage = i % STAGES;
-            ok = wait(&sh.p_full, i & 1) && ok;
+        auto values = [&](int i) {   // O += V^T P of the segment's tile i
+            const int stage = (it + i) % STAGES, w = i & 1;
+            ok = ok && wait(&sh.p_full[w], done[w] & 1);
+            ++done[w];
             umma::fence_after_sync();
             if (lane == 0 && ok) {
-                const bool fresh = *(volatile int*)&sh.fresh != 0;
-                const uint32_t v = smem_u32(smem) + stage * Z::STAGE + Z::KV;
+                const bool fresh = *(volatile int*)&sh.fresh[w] != 0;
+                const uint32_t v = smem_u32(smem) + stage * Z::STAGE + Z::KV, sp = smem_u32(smem) + Z::P_OFF + w * N * TILE;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)   // 32 keys each: four groups of eight rows
-                    mma_i8(tmem_o, umma::sdesc_kmajor(v + 4096 * k, 1024, 128), umma::sdesc_kmajor(sp + 4 * (N / 16 * 128) * k, N / 16 * 128, 128), IO,
-                           !(fresh && k == 0));
-                sh.fresh = 0;
-                umma::commit(smem_u32(&sh.p_free));
+                    mma_i8(tmem + Z::T_O + w * N, umma::sdesc_kmajor(v + 4096 * k, 1024, 128),
+                           umma::sdesc_kmajor(sp + 4 * (N / 16 * 128) * k, N / 16 * 128, 128), IO, !(fresh && k == 0));
+                *(volatile int*)&sh.fresh[w] = 0;
+                umma::commit(smem_u32(&sh.p_free[w]));
                 umma::commit(smem_u32(&sh.empty[stage]));
             }
             __syncwarp();
@@ -666,24 +727,25 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
             if (s.count > 0) {
                 ok = wait(&sh.q_full, seg & 1);
                 ++seg;
-                for (int t = 0; t < s.count && ok; ++t, ++it) {
-                    const int stage = it % STAGES, buf = it % Z::SBUF;
-                    // with one score buffer the tile before has to be through first
-                    if (Z::SBUF == 1 && t > 0) values(it - 1);
-                    ok = ok && wait(&sh.full[stage], it / STAGES & 1) && wait(&sh.s_free[buf], it / Z::SBUF & 1);
+                for (int i = 0; i < s.count && ok; ++i) {
+                    const int stage = (it + i) % STAGES, w = i & 1;
+                    ok = wait(&sh.full[stage], (it + i) / STAGES & 1) && wait(&sh.s_free[w], scores[w] & 1);
+                    ++scores[w];
                     umma::fence_after_sync();
                     if (lane == 0 && ok) {
                         const uint32_t k0 = smem_u32(smem) + stage * Z::STAGE;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)   // 32 dims each: two chunks
-                            mma_i8(tmem + buf * N, umma::sdesc_kmajor(k0 + 256 * k, 128, 1024), umma::sdesc_kmajor(sq + 256 * k, 128, 1024), IS, true);
-                        umma::commit(smem_u32(&sh.s_full[buf]));
+                            mma_i8(tmem + w * N, umma::sdesc_kmajor(k0 + 256 * k, 128, 1024), umma::sdesc_kmajor(sq + 256 * k, 128, 1024), IS, true);
+                        umma::commit(smem_u32(&sh.s_full[w]));
                     }
                     __syncwarp();
-                    if (Z::SBUF == 2 && t > 0) values(it - 1);
+                    if (i > 1) values(i - 2);
                 }
-                if (ok) values(it - 1);
+                if (s.count > 1) values(s.count - 2);
+                values(s.count - 1);
             }
+            it += s.count;
             advance(p, at, left, s);
         }
     }
@@ -697,14 +759,14 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
         while (left > 0) {
             const Segment s = segment_at(p, at, left);
             float* part = p.part + ((size_t)blockIdx.x * 2 + s.head) * PART_FLOATS;
-            for (int i = tid; i < cols * RD; i += PT) {
-                const int c = i / RD, node = c / p.G;
+            for (int i = tid; i < s.cols * RD; i += PT) {
+                const int c = i / RD, x = s.col0 + c, node = x / p.G;
                 const float nan = __int_as_float(0x7fc00000);
                 if (!s.complete) {
                     part[PART_O + i] = nan;
                     if (i % RD == 0) part[c] = 0.f, part[PART_L + c] = nan;
                 } else if (s.bad || node < s.L) {
-                    p.out[(((size_t)s.b * p.N + node) * p.hq + s.h * p.G + c % p.G) * RD + i % RD] = nan;
+                    p.out[(((size_t)s.b * p.N + node) * p.hq + s.h * p.G + x % p.G) * RD + i % RD] = nan;
                 }
             }
             advance(p, at, left, s);
@@ -716,7 +778,7 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
 // Joins the partial results of the units that the ranges' cuts divide.
 __global__ void __launch_bounds__(JT) rswa_wide_join_kernel(const __grid_constant__ TreeParams p, int ctas) {
     __shared__ int scan[JT / 32 + 4];
-    const int tid = threadIdx.x, b = blockIdx.x / p.hk, h = blockIdx.x % p.hk;
+    const int tid = threadIdx.x, per_b = p.hk * p.groups, b = blockIdx.x / per_b, unit = blockIdx.x % per_b;
     pdl_wait();
     // the unit's tiles in the row of all tiles, and the CTAs that had them
     int all = 0, before = 0;
@@ -725,16 +787,16 @@ __global__ void __launch_bounds__(JT) rswa_wide_join_kernel(const __grid_constan
         all += own;
         if (i < b) before += own;
     }
-    all = cta_scan<JT / 32>(all, scan) * p.hk;
+    all = cta_scan<JT / 32>(all, scan) * per_b;
     before = cta_scan<JT / 32>(before, scan);
     const int own = sequence_tiles(p, b), per = (all + ctas - 1) / ctas;
-    const int64_t from = (int64_t)before * p.hk + (int64_t)h * own;
+    const int64_t from = (int64_t)before * per_b + (int64_t)unit * own;
     const int c0 = (int)(from / per), c1 = (int)((from + own - 1) / per);
     if (c0 == c1) return;
-    const Segment s = segment_at(p, Place{b, h, 0}, own);
+    const Segment s = segment_at(p, Place{b, unit, 0}, own);
     if (s.bad) return;
-    for (int c = blockIdx.y; c < p.N * p.G; c += gridDim.y) {
-        const int node = c / p.G;
+    for (int c = blockIdx.y; c < s.cols; c += gridDim.y) {
+        const int x = s.col0 + c, node = x / p.G;
         if (node >= s.L) return;
         float M = NONE, l = 0.f, o = 0.f;
         for (int i = c0; i <= c1; ++i) M = fmaxf(M, __ldcg(p.part + ((size_t)i * 2 + (i == c0)) * PART_FLOATS + c));
@@ -744,7 +806,7 @@ __global__ void __launch_bounds__(JT) rswa_wide_join_kernel(const __grid_constan
             l = fmaf(f, __ldcg(part + PART_L + c), l);
             o = fmaf(f, __ldcg(part + PART_O + c * RD + tid), o);
         }
-        p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + c % p.G) * RD + tid] = o / l;
+        p.out[(((size_t)b * p.N + node) * p.hq + s.h * p.G + x % p.G) * RD + tid] = o / l;
     }
 }
 
@@ -762,16 +824,14 @@ cudaError_t launch_wide_as(TreeParams& p, cudaStream_t st) {
     e = launch_kernel(fn, dim3((unsigned)ctas), dim3(PT), smem, 1, args, st);
     if (e != cudaSuccess) return e;
     void* more[] = {&p, &ctas};
-    const int cols = p.N * p.G;
-    return launch_kernel((const void*)rswa_wide_join_kernel, dim3((unsigned)p.B * p.hk, cols < 8 ? cols : 8), dim3(JT), 0, 1, more, st);
+    const int cols = p.N * p.G < CMAX ? p.N * p.G : CMAX;
+    return launch_kernel((const void*)rswa_wide_join_kernel, dim3((unsigned)p.B * p.hk * p.groups, cols < 8 ? cols : 8), dim3(JT), 0, 1,
+                         more, st);
 }
 template <bool INT4>
 cudaError_t launch_wide_for(TreeParams& p, cudaStream_t st) {
-    const int cols = p.N * p.G;
-    return cols <= 16   ? launch_wide_as<INT4, 16>(p, st)
-           : cols <= 32 ? launch_wide_as<INT4, 32>(p, st)
-           : cols <= 48 ? launch_wide_as<INT4, 48>(p, st)
-                        : launch_wide_as<INT4, 64>(p, st);
+    p.groups = (p.N * p.G + CMAX - 1) / CMAX;
+    return p.N * p.G <= 16 ? launch_wide_as<INT4, 16>(p, st) : launch_wide_as<INT4, 32>(p, st);
 }
 
 }  // namespace
