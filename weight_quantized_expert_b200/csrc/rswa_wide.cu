@@ -58,6 +58,22 @@ __device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(zero)
         : "memory");
 }
+// the thread's copies so far arrive on the barrier once they have landed
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// whether the barrier's phase of that parity is over (asked once, for the whole warp)
+__device__ __forceinline__ bool is_over(uint64_t* bar, uint32_t parity) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, r != 0);
+}
 // eight columns of the thread's tensor-memory lane; complete after wait_ld()
 __device__ __forceinline__ void ld8(uint32_t taddr, int (&v)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -107,7 +123,7 @@ __device__ __forceinline__ float warp_max(float x) {
 template <bool INT4, int CP>
 struct Sizes {
     static constexpr int N = 3 * CP;                                  // columns in digits
-    static constexpr int STAGES = INT4 ? 3 : 4;                       // tiles of bytes (3 at least: S runs two tiles ahead of P V)
+    static constexpr int STAGES = INT4 ? 3 : CP == 16 ? 6 : 5;        // tiles of bytes
     static constexpr int PACKED = 3;                                  // int4: tiles of nibbles on their way
     static constexpr int KV = TILE * RD;                              // bytes of K (or V) of a tile
     static constexpr int STAGE = 2 * KV;
@@ -119,11 +135,13 @@ struct Sizes {
     static_assert(CP * RD * 4 <= 2 * N * TILE, "a worker's results fit where the weights were");
 };
 
+constexpr int STAGES_MAX = 6;
+
 template <int CP>
 struct Shared {
     float part[CP][RD];                  // the drafted keys' part
     float part_m[CP], part_l[CP];
-    float scales[4][2][TILE];            // of the stages' tiles: ks, vs
+    float scales[STAGES_MAX][2][TILE];            // of the stages' tiles: ks, vs
     float2 col[2][CP];                   // a column's step (score in log2 = dot * key scale * step) and each worker's bound
     float2 moved[2][CP];                 // bounds that moved: by how much, and the factor for the column's sums
     float red[2][4][CP + 1];
@@ -132,7 +150,7 @@ struct Shared {
     int ages[CP];                        // ring slots younger than this are seen
     unsigned long long line[TREE_MAX];
     int par[TREE_MAX];
-    uint64_t full[4], empty[4], s_full[2], s_free[2], p_full[2], p_free[2], q_full;
+    uint64_t full[STAGES_MAX], empty[STAGES_MAX], s_full[2], s_free[2], p_full[2], p_free[2], q_full;
     int scan[WARPS + 4];
     float vref[2];                       // bounds of the value scales
     int fresh[2];                        // the next P V starts O anew
@@ -242,6 +260,138 @@ __device__ __forceinline__ TileAt tile_at(const TreeParams& p, const Segment& s,
     return {unit * p.ref.cap + (size_t)t * TILE, min(TILE, s.R - t * TILE), false};
 }
 
+// A worker's O (if `filled`; every P V so far has completed) joins its fp32 sums (if `summed`), times the columns' factors.
+// Rare, and kept out of line: inlined it would take registers from the tiles' loop.
+template <bool INT4, int CP>
+__device__ __noinline__ void drain(uint32_t t_o, uint32_t t_acc, float vref, bool filled, bool summed, const float2* moved) {
+    const float gain = vref * ((INT4 ? 1.f / 16.f : 1.f) / P_TOP);
+#pragma unroll 1
+    for (int c = 0; c < CP; c += 8) {
+        int o2[8], o1[8], o0[8], old[8];
+        float a[8];
+        ld8(t_o + c, o0);
+        ld8(t_o + CP + c, o1);
+        ld8(t_o + 2 * CP + c, o2);
+        ld8(t_acc + c, old);
+        wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            a[j] = summed ? __int_as_float(old[j]) : 0.f;
+            if (filled) a[j] = fmaf(fmaf((float)o2[j], 65536.f, fmaf((float)o1[j], 256.f, (float)o0[j])), gain, a[j]);
+            if (moved) a[j] *= moved[c + j].y;
+        }
+        st8(t_acc + c, a);
+    }
+    umma::wait_st();
+}
+
+// Query digits, columns' constants and the drafted keys' part of a unit; by the softmax warps.
+template <bool INT4, int CP>
+__device__ __noinline__ void prepare_columns(const TreeParams& p, const Segment& s, Shared<CP>& sh, uint8_t* sq) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int i0 = 0; i0 < CP / SOFT; i0 += 2) {   // two columns at a time
+        float4 q[2], k4[2][4], v4[2][4];
+        unsigned long long line[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = warp + (i0 + i) * SOFT, node = (s.col0 + c) / p.G;
+            const bool live = c < s.cols && node < s.L;
+            q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (live)
+                q[i] = __ldg(reinterpret_cast<const float4*>(p.q + (((size_t)s.b * p.N + node) * p.hq + s.h * p.G + (s.col0 + c) % p.G) * RD) + lane);
+            line[i] = live && s.head ? sh.line[node] : 0ull;
+            unsigned long long rest = line[i];
+            draft_load(p, s.b, s.h, lane, rest, k4[i], v4[i]);
+            if (lane == 0) sh.ages[c] = live ? min(s.n, RW - __popcll(sh.line[node])) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = warp + (i0 + i) * SOFT;
+            const float4 x = q[i];
+            float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            a = fmaxf(a, TINY);
+            const float inv = Q_TOP / a;
+            int f[4] = {__float2int_rn(x.x * inv), __float2int_rn(x.y * inv), __float2int_rn(x.z * inv), __float2int_rn(x.w * inv)};
+#pragma unroll
+            for (int d = 0; d < 3; ++d) {   // signed digits, the lowest first
+                uint32_t v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int digit = (int)(int8_t)f[j];
+                    v[j] = (uint32_t)digit & 255u;
+                    f[j] = (f[j] - digit) >> 8;
+                }
+                const int n = d * CP + c;
+                uint8_t* at8 = sq + (n >> 3) * 1024 + (n & 7) * 16;
+                if (INT4) {   // even dims of 32 in one chunk, odd ones in the next
+                    uint8_t* w = at8 + (lane >> 3) * 256 + 2 * (lane & 7);
+                    *reinterpret_cast<uint16_t*>(w) = (uint16_t)(v[0] | v[2] << 8);
+                    *reinterpret_cast<uint16_t*>(w + 128) = (uint16_t)(v[1] | v[3] << 8);
+                } else {
+                    *reinterpret_cast<uint32_t*>(at8 + (lane >> 2) * 128 + 4 * (lane & 3)) = v[0] | v[1] << 8 | v[2] << 16 | v[3] << 24;
+                }
+            }
+            if (lane == 0)
+                sh.col[0][c] = sh.col[1][c] = make_float2(a / Q_TOP * (SCORE_SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f)), 0.f);
+            const DraftPart dp = draft_attend(p, s.b, s.h, lane, x, line[i], k4[i], v4[i]);
+            reinterpret_cast<float4*>(sh.part[c])[lane] = dp.o;
+            if (lane == 0) sh.part_m[c] = dp.m, sh.part_l[c] = dp.l;
+        }
+    }
+}
+
+// A unit's result from both workers' sums and the drafted keys' part; by the softmax warps.
+template <int CP>
+__device__ __noinline__ void finish(const TreeParams& p, const Segment& s, Shared<CP>& sh, float* other, uint32_t t_acc, int dim) {
+    const int tid = threadIdx.x, me = tid / (ST / 2), row = tid % (ST / 2);
+    if (tid < CP) {
+        const int c = tid;
+        const float m0 = s.count > 0 ? sh.col[0][c].y : NONE, m1 = s.count > 1 ? sh.col[1][c].y : NONE, pm = sh.part_m[c];
+        const float M = fmaxf(fmaxf(m0, m1), pm), f0 = ex2(m0 - M), f1 = ex2(m1 - M), g = ex2(pm - M);
+        const float l0 = (sh.red[0][0][c] + sh.red[0][1][c]) + (sh.red[0][2][c] + sh.red[0][3][c]);
+        const float l1 = (sh.red[1][0][c] + sh.red[1][1][c]) + (sh.red[1][2][c] + sh.red[1][3][c]);
+        const float l = fmaf(f0, l0, fmaf(f1, l1, g * sh.part_l[c])), r = s.complete ? 1.f / l : 1.f;
+        sh.factor[c] = make_float4(f0 * r, f1 * r, g * r, 0.f);
+        sh.total_m[c] = M, sh.total_l[c] = l;
+    }
+    if (me == 1) {   // worker 1's results go where the weights were
+#pragma unroll 1
+        for (int c = 0; c < CP; c += 8) {
+            int a[8];
+            ld8(t_acc + c, a);
+            wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) other[(c + j) * RD + row] = s.count > 1 ? __int_as_float(a[j]) : 0.f;
+        }
+    }
+    softmax_sync();
+    if (me == 0) {
+        float* part = p.part + ((size_t)blockIdx.x * 2 + s.head) * PART_FLOATS;
+#pragma unroll 1
+        for (int c = 0; c < CP; c += 8) {
+            int a[8];
+            ld8(t_acc + c, a);
+            wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int cc = c + j, x = s.col0 + cc, node = x / p.G;
+                if (cc >= s.cols || node >= s.L) continue;
+                const float4 f = sh.factor[cc];
+                const float o = fmaf(f.x, s.count > 0 ? __int_as_float(a[j]) : 0.f, fmaf(f.y, other[cc * RD + row], f.z * sh.part[cc][dim]));
+                if (s.complete) {
+                    p.out[(((size_t)s.b * p.N + node) * p.hq + s.h * p.G + x % p.G) * RD + dim] = o;
+                } else {
+                    part[PART_O + cc * RD + dim] = o;
+                    if (row == 0) part[cc] = sh.total_m[cc], part[PART_L + cc] = sh.total_l[cc];
+                }
+            }
+        }
+    }
+}
+
 template <bool INT4, int CP>
 __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant__ TreeParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -251,7 +401,7 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(&sh.full[i], LT), mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < STAGES_MAX; ++i) mbar_init(&sh.full[i], LT), mbar_init(&sh.empty[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1), mbar_init(&sh.s_free[i], SOFT / 2);
             mbar_init(&sh.p_full[i], SOFT / 2), mbar_init(&sh.p_free[i], 1);
@@ -284,7 +434,6 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), t_s = lanes + me * N, t_o = lanes + Z::T_O + me * N,
                        t_acc = lanes + Z::T_ACC + me * CP;
         const int dim = INT4 ? 32 * (row / 32) + 2 * (row % 16) + ((row / 16) & 1) : row;   // of the thread's lane of O
-        uint8_t* sq = smem + Z::Q_OFF;
         uint8_t* sp = smem + Z::P_OFF + me * N * TILE;
         auto preset = [&] {   // S accumulates onto the pattern that reads as MAGIC + sum
 #pragma unroll
@@ -309,14 +458,6 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
             if (!s.dead) {
                 // ---- lines of the tree, query digits, drafted keys
                 if (tid < s.L) sh.par[tid] = p.parent ? __ldg(p.parent + (size_t)s.b * p.N + tid) : tid - 1;
-                float4 q[CP / SOFT];
-#pragma unroll
-                for (int i = 0; i < CP / SOFT; ++i) {
-                    const int c = warp + i * SOFT, node = (s.col0 + c) / p.G;
-                    q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (c < s.cols && node < s.L)
-                        q[i] = __ldg(reinterpret_cast<const float4*>(p.q + (((size_t)s.b * p.N + node) * p.hq + s.h * p.G + (s.col0 + c) % p.G) * RD) + lane);
-                }
                 softmax_sync();
                 if (tid < s.L) {
                     unsigned long long line = 0;
@@ -325,55 +466,7 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                 }
                 if (tid < 2) sh.vref[tid] = TINY;
                 softmax_sync();
-#pragma unroll
-                for (int i0 = 0; i0 < CP / SOFT; i0 += 2) {   // two columns at a time
-                    float4 k4[2][4], v4[2][4];
-                    unsigned long long line[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int c = warp + (i0 + i) * SOFT, node = (s.col0 + c) / p.G;
-                        const bool live = c < s.cols && node < s.L;
-                        line[i] = live && s.head ? sh.line[node] : 0ull;
-                        unsigned long long rest = line[i];
-                        draft_load(p, s.b, s.h, lane, rest, k4[i], v4[i]);
-                        if (lane == 0) sh.ages[c] = live ? min(s.n, RW - __popcll(sh.line[node])) : 0;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int c = warp + (i0 + i) * SOFT;
-                        const float4 x = q[i0 + i];
-                        float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
-#pragma unroll
-                        for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                        a = fmaxf(a, TINY);
-                        const float inv = Q_TOP / a;
-                        int f[4] = {__float2int_rn(x.x * inv), __float2int_rn(x.y * inv), __float2int_rn(x.z * inv), __float2int_rn(x.w * inv)};
-#pragma unroll
-                        for (int d = 0; d < 3; ++d) {   // signed digits, the lowest first
-                            uint32_t v[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int digit = (int)(int8_t)f[j];
-                                v[j] = (uint32_t)digit & 255u;
-                                f[j] = (f[j] - digit) >> 8;
-                            }
-                            const int n = d * CP + c;
-                            uint8_t* at8 = sq + (n >> 3) * 1024 + (n & 7) * 16;
-                            if (INT4) {   // even dims of 32 in one chunk, odd ones in the next
-                                uint8_t* w = at8 + (lane >> 3) * 256 + 2 * (lane & 7);
-                                *reinterpret_cast<uint16_t*>(w) = (uint16_t)(v[0] | v[2] << 8);
-                                *reinterpret_cast<uint16_t*>(w + 128) = (uint16_t)(v[1] | v[3] << 8);
-                            } else {
-                                *reinterpret_cast<uint32_t*>(at8 + (lane >> 2) * 128 + 4 * (lane & 3)) = v[0] | v[1] << 8 | v[2] << 16 | v[3] << 24;
-                            }
-                        }
-                        if (lane == 0)
-                            sh.col[0][c] = sh.col[1][c] = make_float2(a / Q_TOP * (SCORE_SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f)), 0.f);
-                        const DraftPart dp = draft_attend(p, s.b, s.h, lane, x, line[i], k4[i], v4[i]);
-                        reinterpret_cast<float4*>(sh.part[c])[lane] = dp.o;
-                        if (lane == 0) sh.part_m[c] = dp.m, sh.part_l[c] = dp.l;
-                    }
-                }
+                prepare_columns<INT4, CP>(p, s, sh, smem + Z::Q_OFF);
                 umma::fence_smem_to_async();
                 softmax_sync();
                 if (lane == 0 && s.count > 0) mbar_arrive(&sh.q_full);
@@ -382,23 +475,6 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
 #pragma unroll
                 for (int c = 0; c < CP; ++c) sum[c] = 0.f;
                 bool filled = false, summed = false;   // O holds something; so do the fp32 sums
-                // eight columns' O (every P V so far has completed) and earlier sums, in fp32
-                auto gather = [&](int c, float vref, float (&a)[8]) {
-                    const float gain = vref * ((INT4 ? 1.f / 16.f : 1.f) / P_TOP);
-                    int o2[8], o1[8], o0[8], old[8];
-                    if (filled) {
-                        ld8(t_o + c, o0);
-                        ld8(t_o + CP + c, o1);
-                        ld8(t_o + 2 * CP + c, o2);
-                    }
-                    if (summed) ld8(t_acc + c, old);
-                    wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        a[j] = summed ? __int_as_float(old[j]) : 0.f;
-                        if (filled) a[j] = fmaf(fmaf((float)o2[j], 65536.f, fmaf((float)o1[j], 256.f, (float)o0[j])), gain, a[j]);
-                    }
-                };
                 for (int i = me; i < s.count; i += 2, ++k) {   // left by all threads of the worker at once
                     const int stage = (it + i) % STAGES;
                     const TileAt ta = tile_at(p, s, s.first + i);
@@ -472,18 +548,8 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                             x[c] -= by.x;
                             sum[c] *= by.y;
                         }
-                        if (filled || summed) {
-#pragma unroll
-                            for (int c = 0; c < CP; c += 8) {
-                                float a[8];
-                                gather(c, vref, a);
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) a[j] *= sh.moved[me][c + j].y;
-                                st8(t_acc + c, a);
-                            }
-                            umma::wait_st();
-                            summed = true;
-                        }
+                        if (filled || summed) drain<INT4, CP>(t_o, t_acc, vref, filled, summed, sh.moved[me]);
+                        summed |= filled;
                         filled = false;
                     }
                     // ---- weights: 24 bits, as three digits, [key][column] for the second product
@@ -519,9 +585,12 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     filled = true;
                 }
                 // ---- the unit's sums, and the drafted keys
-                if (filled) ok = ok && wait(&sh.p_free[me], (k - 1) & 1);
-                __syncwarp();
-                umma::fence_after_sync();
+                if (filled) {
+                    ok = ok && wait(&sh.p_free[me], (k - 1) & 1);
+                    __syncwarp();
+                    umma::fence_after_sync();
+                    drain<INT4, CP>(t_o, t_acc, sh.vref[me], true, summed, nullptr);
+                }
 #pragma unroll
                 for (int c = 0; c < CP; ++c) {
                     float l = sum[c];
@@ -532,48 +601,7 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                 if (!ok) sh.gave_up = 1;
                 softmax_sync();
                 ok = *(volatile int*)&sh.gave_up == 0;
-                float* other = reinterpret_cast<float*>(smem + Z::P_OFF);   // worker 1's results, where the weights were
-                if (tid < CP) {
-                    const int c = tid;
-                    const float m0 = s.count > 0 ? sh.col[0][c].y : NONE, m1 = s.count > 1 ? sh.col[1][c].y : NONE, pm = sh.part_m[c], M = fmaxf(fmaxf(m0, m1), pm);
-                    const float f0 = ex2(m0 - M), f1 = ex2(m1 - M), g = ex2(pm - M);
-                    const float l0 = (sh.red[0][0][c] + sh.red[0][1][c]) + (sh.red[0][2][c] + sh.red[0][3][c]);
-                    const float l1 = (sh.red[1][0][c] + sh.red[1][1][c]) + (sh.red[1][2][c] + sh.red[1][3][c]);
-                    const float l = fmaf(f0, l0, fmaf(f1, l1, g * sh.part_l[c])), r = s.complete ? 1.f / l : 1.f;
-                    sh.factor[c] = make_float4(f0 * r, f1 * r, g * r, 0.f);
-                    sh.total_m[c] = M, sh.total_l[c] = l;
-                }
-                if (me == 1) {
-#pragma unroll
-                    for (int c = 0; c < CP; c += 8) {
-                        float a[8];
-                        gather(c, sh.vref[1], a);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) other[(c + j) * RD + row] = a[j];
-                    }
-                }
-                softmax_sync();
-                if (me == 0) {
-                    float* part = p.part + ((size_t)blockIdx.x * 2 + s.head) * PART_FLOATS;
-#pragma unroll
-                    for (int c = 0; c < CP; c += 8) {
-                        float a[8];
-                        gather(c, sh.vref[0], a);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int cc = c + j, x = s.col0 + cc, node = x / p.G;
-                            if (cc >= s.cols || node >= s.L) continue;
-                            const float4 f = sh.factor[cc];
-                            const float o = fmaf(f.x, a[j], fmaf(f.y, other[cc * RD + row], f.z * sh.part[cc][dim]));
-                            if (s.complete) {
-                                p.out[(((size_t)s.b * p.N + node) * p.hq + s.h * p.G + x % p.G) * RD + dim] = o;
-                            } else {
-                                part[PART_O + cc * RD + dim] = o;
-                                if (row == 0) part[cc] = sh.total_m[cc], part[PART_L + cc] = sh.total_l[cc];
-                            }
-                        }
-                    }
-                }
+                finish<CP>(p, s, sh, reinterpret_cast<float*>(smem + Z::P_OFF), t_acc, dim);
                 if (tid < 2) sh.fresh[tid] = 1;
                 softmax_sync();
             }
@@ -586,24 +614,12 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
         int it = 0;
         bool ok = true;
         if (!INT4) {
-            int signalled = 0;   // tiles whose arrival has been signalled
-            auto signal = [&](int upto) {
-                umma::fence_smem_to_async();
-                for (; signalled < upto; ++signalled) mbar_arrive(&sh.full[signalled % STAGES]);
-            };
             while (left > 0 && ok) {
                 const Segment s = segment_at(p, at, left);
                 for (int tile = s.first; tile < s.first + s.count && ok; ++tile, ++it) {
                     const int stage = it % STAGES;
                     const TileAt ta = tile_at(p, s, tile);
-                    if (it >= STAGES) {
-                        // nothing that has arrived may wait for a place that only its use sets free
-                        if (!mbar_try_wait(&sh.empty[stage], (it / STAGES - 1) & 1)) {
-                            cp_wait<0>();
-                            signal(it);
-                            ok = wait(&sh.empty[stage], (it / STAGES - 1) & 1);
-                        }
-                    }
+                    if (it >= STAGES) ok = wait(&sh.empty[stage], (it / STAGES - 1) & 1);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
@@ -625,16 +641,11 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     const size_t sr = ta.row + min(t, ta.rows - 1);
                     cp4(smem_u32(&sh.scales[stage][0][t]), v.ks + sr);
                     cp4(smem_u32(&sh.scales[stage][1][t]), v.vs + sr);
-                    cp_commit();
-                    if (it - signalled >= STAGES - 1) {
-                        cp_wait<STAGES - 2>();
-                        signal(it - (STAGES - 2) + 1);
-                    }
+                    cp_arrive(&sh.full[stage]);   // once they have landed; the reader passes them on to the tensor core
                 }
                 advance(p, at, left, s);
             }
-            cp_wait<0>();
-            signal(it);
+            asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
             // nibbles come ahead into places of their own; a thread unpacks what it copied itself
             Place ahead = at;
@@ -653,11 +664,11 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     const KvView& v = ta.ring ? p.ring : p.ref;
                     uint8_t* to = smem + STAGES * Z::STAGE + issued % Z::PACKED * Z::PACK;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // chunk (t % 4) of rows t / 4 + 32 i
-                        const int r = t / 4 + 32 * i, j = t & 3;
+                    for (int i = 0; i < 4; ++i) {   // eight lanes copy one chunk of eight rows
+                        const int r = (t >> 5 << 3 | (t & 7)) + 32 * i, j = (t >> 3) & 3;
                         const size_t src = (ta.row + min(r, ta.rows - 1)) * (RD / 2) + j * 16;
-                        cp16(smem_u32(to + r * 64 + j * 16), v.k + src);
-                        cp16(smem_u32(to + Z::KV / 2 + r * 64 + j * 16), v.v + src);
+                        cp16(smem_u32(to + (i * LT + t) * 16), v.k + src);
+                        cp16(smem_u32(to + Z::KV / 2 + (i * LT + t) * 16), v.v + src);
                     }
                     const size_t sr = ta.row + min(t, ta.rows - 1);
                     cp4(smem_u32(to + Z::KV + 4 * t), v.ks + sr);
@@ -683,8 +694,8 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     uint8_t* to = smem + stage * Z::STAGE;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int r = t / 4 + 32 * (i & 3), j = t & 3, kv = i >> 2;
-                        const uint4 n = lds128(fr + kv * (Z::KV / 2) + r * 64 + j * 16);
+                        const int r = (t >> 5 << 3 | (t & 7)) + 32 * (i & 3), j = (t >> 3) & 3, kv = i >> 2;
+                        const uint4 n = lds128(fr + kv * (Z::KV / 2) + ((i & 3) * LT + t) * 16);
                         uint8_t* dst = to + kv * Z::KV + (r >> 3) * 1024 + 2 * j * 128 + (r & 7) * 16;
                         *reinterpret_cast<uint4*>(dst) = make_uint4((n.x << 4) & 0xF0F0F0F0u, (n.y << 4) & 0xF0F0F0F0u, (n.z << 4) & 0xF0F0F0F0u, (n.w << 4) & 0xF0F0F0F0u);
                         *reinterpret_cast<uint4*>(dst + 128) = make_uint4(n.x & 0xF0F0F0F0u, n.y & 0xF0F0F0F0u, n.z & 0xF0F0F0F0u, n.w & 0xF0F0F0F0u);
@@ -704,46 +715,59 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
         const uint32_t sq = smem_u32(smem) + Z::Q_OFF;
         int it = 0, seg = 0, scores[2] = {0, 0}, done[2] = {0, 0};   // tiles before the segment; each worker's so far
         bool ok = true;
-        auto values = [&](int i) {   // O += V^T P of the segment's tile i
-            const int stage = (it + i) % STAGES, w = i & 1;
-            ok = ok && wait(&sh.p_full[w], done[w] & 1);
-            ++done[w];
-            umma::fence_after_sync();
-            if (lane == 0 && ok) {
-                const bool fresh = *(volatile int*)&sh.fresh[w] != 0;
-                const uint32_t v = smem_u32(smem) + stage * Z::STAGE + Z::KV, sp = smem_u32(smem) + Z::P_OFF + w * N * TILE;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)   // 32 keys each: four groups of eight rows
-                    mma_i8(tmem + Z::T_O + w * N, umma::sdesc_kmajor(v + 4096 * k, 1024, 128),
-                           umma::sdesc_kmajor(sp + 4 * (N / 16 * 128) * k, N / 16 * 128, 128), IO, !(fresh && k == 0));
-                *(volatile int*)&sh.fresh[w] = 0;
-                umma::commit(smem_u32(&sh.p_free[w]));
-                umma::commit(smem_u32(&sh.empty[stage]));
-            }
-            __syncwarp();
-        };
         while (left > 0 && ok) {
             const Segment s = segment_at(p, at, left);
             if (s.count > 0) {
                 ok = wait(&sh.q_full, seg & 1);
                 ++seg;
-                for (int i = 0; i < s.count && ok; ++i) {
-                    const int stage = (it + i) % STAGES, w = i & 1;
-                    ok = wait(&sh.full[stage], (it + i) / STAGES & 1) && wait(&sh.s_free[w], scores[w] & 1);
-                    ++scores[w];
-                    umma::fence_after_sync();
-                    if (lane == 0 && ok) {
-                        const uint32_t k0 = smem_u32(smem) + stage * Z::STAGE;
+                // whichever product is ready: S of tile ns (its codes have landed, its worker has read the S before), or
+                // P V of tile np (its weights are written)
+                int ns = 0, np = 0;
+                uint64_t since = globaltimer_ns();
+                while (ok && np < s.count) {
+                    bool moved = false;
+                    if (ns < s.count) {
+                        const int stage = (it + ns) % STAGES, w = ns & 1;
+                        if (is_over(&sh.full[stage], (it + ns) / STAGES & 1) && is_over(&sh.s_free[w], scores[w] & 1)) {
+                            umma::fence_smem_to_async();
+                            umma::fence_after_sync();
+                            if (lane == 0) {
+                                const uint32_t k0 = smem_u32(smem) + stage * Z::STAGE;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)   // 32 dims each: two chunks
-                            mma_i8(tmem + w * N, umma::sdesc_kmajor(k0 + 256 * k, 128, 1024), umma::sdesc_kmajor(sq + 256 * k, 128, 1024), IS, true);
-                        umma::commit(smem_u32(&sh.s_full[w]));
+                                for (int k = 0; k < 4; ++k)   // 32 dims each: two chunks
+                                    mma_i8(tmem + w * N, umma::sdesc_kmajor(k0 + 256 * k, 128, 1024), umma::sdesc_kmajor(sq + 256 * k, 128, 1024), IS, true);
+                                umma::commit(smem_u32(&sh.s_full[w]));
+                            }
+                            ++scores[w], ++ns;
+                            moved = true;
+                        }
                     }
-                    __syncwarp();
-                    if (i > 1) values(i - 2);
+                    if (np < ns) {
+                        const int stage = (it + np) % STAGES, w = np & 1;
+                        if (is_over(&sh.p_full[w], done[w] & 1)) {
+                            umma::fence_after_sync();
+                            if (lane == 0) {
+                                const bool fresh = *(volatile int*)&sh.fresh[w] != 0;
+                                const uint32_t v = smem_u32(smem) + stage * Z::STAGE + Z::KV, sp = smem_u32(smem) + Z::P_OFF + w * N * TILE;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)   // 32 keys each: four groups of eight rows
+                                    mma_i8(tmem + Z::T_O + w * N, umma::sdesc_kmajor(v + 4096 * k, 1024, 128),
+                                           umma::sdesc_kmajor(sp + 4 * (N / 16 * 128) * k, N / 16 * 128, 128), IO, !(fresh && k == 0));
+                                *(volatile int*)&sh.fresh[w] = 0;
+                                umma::commit(smem_u32(&sh.p_free[w]));
+                                umma::commit(smem_u32(&sh.empty[stage]));
+                            }
+                            ++done[w], ++np;
+                            moved = true;
+                        }
+                    }
+                    if (moved) {
+                        since = globaltimer_ns();
+                    } else if (__any_sync(0xffffffffu, globaltimer_ns() - since > LIMIT_NS || *(volatile int*)&sh.gave_up)) {
+                        sh.gave_up = 1;
+                        ok = false;
+                    }
                 }
-                if (s.count > 1) values(s.count - 2);
-                values(s.count - 1);
             }
             it += s.count;
             advance(p, at, left, s);
