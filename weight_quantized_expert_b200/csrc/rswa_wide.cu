@@ -16,9 +16,10 @@
 // the bounds stand (at most 33024 keys a unit: |sum| <= 33024 * 255 * 128 < 2^31) and is added to fp32 when they move
 // and at the unit's end.
 //
-// Roles of a CTA (one per SM): warps 0-3 and 4-7 are two softmax workers (thread = key row of S, dim row of O), which
-// take the tiles in turn, each with its own S, O, bounds and sums, so one's latencies run under the other's work; warps
-// 8-11 load (cp.async; int4 is unpacked to bytes 16 q on the way); warp 12 issues the MMAs.  A unit is one kv head of one
+// Roles of a CTA (one per SM): warps 0-7 and 8-15 are two softmax workers (thread = key row of S, dim row of O, and one
+// half of the columns), which take the tiles in turn, each with its own S, O, bounds and sums, so one's latencies run
+// under the other's work; warps 16-18 load (cp.async; int4 is unpacked to bytes 16 q on the way); warp 19 issues the MMAs.
+// Twenty warps leave a thread 96 registers, enough for its columns; with one more it would be 80.  A unit is one kv head of one
 // sequence with up to 32 columns.  All tiles of all units form one row, cut into equal ranges, one per CTA (the lengths
 // are read on the device, so ragged batches stay balanced); units that a cut divides leave partial results in the
 // workspace, and a second kernel joins them.  Every wait is bounded; one that runs out turns the CTA's results into NaN.
@@ -34,7 +35,7 @@ namespace focr {
 namespace {
 
 constexpr int RD = TREE_DIM, RW = TREE_RING, TILE = 128;
-constexpr int SOFT = 8, LOADERS = 4, WARPS = SOFT + LOADERS + 1, PT = 32 * WARPS;
+constexpr int SOFT = 16, LOADERS = 3, WARPS = SOFT + LOADERS + 1, PT = 32 * WARPS;
 constexpr int ST = 32 * SOFT, LT = 32 * LOADERS;
 constexpr int JT = 128;                       // threads of the joining kernel
 constexpr int CMAX = 32;                      // columns of a unit
@@ -96,7 +97,7 @@ __device__ __forceinline__ bool any_of_worker(int worker, bool mine) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 q, %2, 0;\n\t"
-        "barrier.cta.red.or.pred p, %1, 128, q;\n\t"
+        "barrier.cta.red.or.pred p, %1, 256, q;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
         : "r"(2 + worker), "r"((uint32_t)mine)
@@ -124,7 +125,7 @@ template <bool INT4, int CP>
 struct Sizes {
     static constexpr int N = 3 * CP;                                  // columns in digits
     static constexpr int STAGES = INT4 ? 3 : CP == 16 ? 6 : 5;        // tiles of bytes
-    static constexpr int PACKED = 3;                                  // int4: tiles of nibbles on their way
+    static constexpr int PACKED = CP == 16 ? 5 : 3;                   // int4: tiles of nibbles on their way
     static constexpr int KV = TILE * RD;                              // bytes of K (or V) of a tile
     static constexpr int STAGE = 2 * KV;
     static constexpr int PACK = 2 * KV / 2 + 8 * TILE;                // nibbles of K and V, and scales
@@ -144,7 +145,7 @@ struct Shared {
     float scales[STAGES_MAX][2][TILE];            // of the stages' tiles: ks, vs
     float2 col[2][CP];                   // a column's step (score in log2 = dot * key scale * step) and each worker's bound
     float2 moved[2][CP];                 // bounds that moved: by how much, and the factor for the column's sums
-    float red[2][4][CP + 1];
+    float red[2][8][CP / 2 + 1];           // by worker and warp
     float4 factor[CP];                   // of the workers' and the drafted keys' parts, and of the result
     float total_m[CP], total_l[CP];
     int ages[CP];                        // ring slots younger than this are seen
@@ -263,10 +264,10 @@ __device__ __forceinline__ TileAt tile_at(const TreeParams& p, const Segment& s,
 // A worker's O (if `filled`; every P V so far has completed) joins its fp32 sums (if `summed`), times the columns' factors.
 // Rare, and kept out of line: inlined it would take registers from the tiles' loop.
 template <bool INT4, int CP>
-__device__ __noinline__ void drain(uint32_t t_o, uint32_t t_acc, float vref, bool filled, bool summed, const float2* moved) {
+__device__ __noinline__ void drain(uint32_t t_o, uint32_t t_acc, float vref, bool filled, bool summed, const float2* moved) {   // half the columns
     const float gain = vref * ((INT4 ? 1.f / 16.f : 1.f) / P_TOP);
 #pragma unroll 1
-    for (int c = 0; c < CP; c += 8) {
+    for (int c = 0; c < CP / 2; c += 8) {
         int o2[8], o1[8], o0[8], old[8];
         float a[8];
         ld8(t_o + c, o0);
@@ -290,11 +291,11 @@ template <bool INT4, int CP>
 __device__ __noinline__ void prepare_columns(const TreeParams& p, const Segment& s, Shared<CP>& sh, uint8_t* sq) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll 1
-    for (int i0 = 0; i0 < CP / SOFT; i0 += 2) {   // two columns at a time
-        float4 q[2], k4[2][4], v4[2][4];
-        unsigned long long line[2];
+    for (int i0 = 0; i0 < CP / SOFT; ++i0) {
+        float4 q[1], k4[1][4], v4[1][4];
+        unsigned long long line[1];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 1; ++i) {
             const int c = warp + (i0 + i) * SOFT, node = (s.col0 + c) / p.G;
             const bool live = c < s.cols && node < s.L;
             q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -306,7 +307,7 @@ __device__ __noinline__ void prepare_columns(const TreeParams& p, const Segment&
             if (lane == 0) sh.ages[c] = live ? min(s.n, RW - __popcll(sh.line[node])) : 0;
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 1; ++i) {
             const int c = warp + (i0 + i) * SOFT;
             const float4 x = q[i];
             float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
@@ -346,22 +347,23 @@ __device__ __noinline__ void prepare_columns(const TreeParams& p, const Segment&
 // A unit's result from both workers' sums and the drafted keys' part; by the softmax warps.
 template <int CP>
 __device__ __noinline__ void finish(const TreeParams& p, const Segment& s, Shared<CP>& sh, float* other, uint32_t t_acc, int dim) {
-    const int tid = threadIdx.x, me = tid / (ST / 2), row = tid % (ST / 2);
+    const int tid = threadIdx.x, me = tid / (ST / 2), row = tid % TILE, c0 = tid / TILE % 2 * (CP / 2);
     if (tid < CP) {
         const int c = tid;
         const float m0 = s.count > 0 ? sh.col[0][c].y : NONE, m1 = s.count > 1 ? sh.col[1][c].y : NONE, pm = sh.part_m[c];
         const float M = fmaxf(fmaxf(m0, m1), pm), f0 = ex2(m0 - M), f1 = ex2(m1 - M), g = ex2(pm - M);
-        const float l0 = (sh.red[0][0][c] + sh.red[0][1][c]) + (sh.red[0][2][c] + sh.red[0][3][c]);
-        const float l1 = (sh.red[1][0][c] + sh.red[1][1][c]) + (sh.red[1][2][c] + sh.red[1][3][c]);
+        const int hf = c / (CP / 2) * 4, cr = c % (CP / 2);
+        const float (*r0)[CP / 2 + 1] = sh.red[0] + hf, (*r1)[CP / 2 + 1] = sh.red[1] + hf;
+        const float l0 = (r0[0][cr] + r0[1][cr]) + (r0[2][cr] + r0[3][cr]), l1 = (r1[0][cr] + r1[1][cr]) + (r1[2][cr] + r1[3][cr]);
         const float l = fmaf(f0, l0, fmaf(f1, l1, g * sh.part_l[c])), r = s.complete ? 1.f / l : 1.f;
         sh.factor[c] = make_float4(f0 * r, f1 * r, g * r, 0.f);
         sh.total_m[c] = M, sh.total_l[c] = l;
     }
     if (me == 1) {   // worker 1's results go where the weights were
 #pragma unroll 1
-        for (int c = 0; c < CP; c += 8) {
+        for (int c = c0; c < c0 + CP / 2; c += 8) {
             int a[8];
-            ld8(t_acc + c, a);
+            ld8(t_acc + c - c0, a);
             wait_ld();
 #pragma unroll
             for (int j = 0; j < 8; ++j) other[(c + j) * RD + row] = s.count > 1 ? __int_as_float(a[j]) : 0.f;
@@ -371,9 +373,9 @@ __device__ __noinline__ void finish(const TreeParams& p, const Segment& s, Share
     if (me == 0) {
         float* part = p.part + ((size_t)blockIdx.x * 2 + s.head) * PART_FLOATS;
 #pragma unroll 1
-        for (int c = 0; c < CP; c += 8) {
+        for (int c = c0; c < c0 + CP / 2; c += 8) {
             int a[8];
-            ld8(t_acc + c, a);
+            ld8(t_acc + c - c0, a);
             wait_ld();
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -430,14 +432,17 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
 
     if (warp < SOFT) {
         // ------------------------------------------------------------ softmax
-        const int me = warp >> 2, row = (warp & 3) * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), t_s = lanes + me * N, t_o = lanes + Z::T_O + me * N,
-                       t_acc = lanes + Z::T_ACC + me * CP;
+        constexpr int HALF = CP / 2;   // columns of a thread
+        const int me = warp >> 3, row = (warp & 3) * 32 + lane, c0 = (warp >> 2 & 1) * HALF;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16), t_s = lanes + me * N + c0, t_o = lanes + Z::T_O + me * N + c0,
+                       t_acc = lanes + Z::T_ACC + me * CP + c0;
         const int dim = INT4 ? 32 * (row / 32) + 2 * (row % 16) + ((row / 16) & 1) : row;   // of the thread's lane of O
         uint8_t* sp = smem + Z::P_OFF + me * N * TILE;
         auto preset = [&] {   // S accumulates onto the pattern that reads as MAGIC + sum
 #pragma unroll
-            for (int c = 0; c < N; c += 8) st8(t_s + c, MAGIC_BITS);
+            for (int d = 0; d < 3; ++d)
+#pragma unroll
+                for (int c = 0; c < HALF; c += 8) st8(t_s + d * CP + c, MAGIC_BITS);
             umma::wait_st();
             umma::fence_before_sync();
             __syncwarp();
@@ -471,9 +476,9 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                 softmax_sync();
                 if (lane == 0 && s.count > 0) mbar_arrive(&sh.q_full);
 
-                float sum[CP];
+                float sum[HALF];
 #pragma unroll
-                for (int c = 0; c < CP; ++c) sum[c] = 0.f;
+                for (int c = 0; c < HALF; ++c) sum[c] = 0.f;
                 bool filled = false, summed = false;   // O holds something; so do the fp32 sums
                 for (int i = me; i < s.count; i += 2, ++k) {   // left by all threads of the worker at once
                     const int stage = (it + i) % STAGES;
@@ -483,9 +488,9 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     umma::fence_after_sync();
                     const bool in = row < ta.rows;
                     const float ks = in ? sh.scales[stage][0][row] : 0.f, vs = in ? sh.scales[stage][1][row] : 0.f;
-                    float x[CP], top = -INFINITY;   // scores relative to the bounds, base 2
+                    float x[HALF], top = -INFINITY;   // scores relative to the bounds, base 2
 #pragma unroll
-                    for (int c = 0; c < CP; c += 8) {
+                    for (int c = 0; c < HALF; c += 8) {
                         int d2[8], d1[8], d0[8];
                         ld8(t_s + c, d0);
                         ld8(t_s + CP + c, d1);
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                         wait_ld();
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float2 b = sh.col[me][c + j];
+                            const float2 b = sh.col[me][c0 + c + j];
                             x[c + j] = fmaf((upper(d2[j]) + lower(d1[j], d0[j])) * ks, b.x, -b.y);
                         }
                     }
@@ -501,25 +506,25 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     if (ta.ring) {
                         const int age = (s.n - 1 - row) & (RW - 1);
 #pragma unroll
-                        for (int c = 0; c < CP; ++c)
-                            if (!in || age >= sh.ages[c]) x[c] = -INFINITY;
+                        for (int c = 0; c < HALF; ++c)
+                            if (!in || age >= sh.ages[c0 + c]) x[c] = -INFINITY;
                     } else if (!in) {
 #pragma unroll
-                        for (int c = 0; c < CP; ++c) x[c] = -INFINITY;
+                        for (int c = 0; c < HALF; ++c) x[c] = -INFINITY;
                     }
 #pragma unroll
-                    for (int c = 0; c < CP; ++c) top = fmaxf(top, x[c]);
+                    for (int c = 0; c < HALF; ++c) top = fmaxf(top, x[c]);
                     const bool first = !filled && !summed;   // the worker's first tile of the unit sets the bounds
                     if (any_of_worker(me, first || top > 0.f || vs > sh.vref[me] || !ok)) {
                         // ---- bounds move: columns' and scales' largest values of the tile
                         const float vref = sh.vref[me];
 #pragma unroll
-                        for (int c = 0; c < CP; ++c) {
+                        for (int c = 0; c < HALF; ++c) {
                             const float m = warp_max(x[c]);
-                            if (lane == 0) sh.red[me][warp & 3][c] = m;
+                            if (lane == 0) sh.red[me][warp & 7][c] = m;
                         }
                         const float vm = warp_max(vs);
-                        if (lane == 0) sh.red[me][warp & 3][CP] = vm;
+                        if (lane == 0) sh.red[me][warp & 7][HALF] = vm;
                         if (filled) ok = wait(&sh.p_free[me], (k - 1) & 1) && ok;
                         __syncwarp();
                         umma::fence_after_sync();
@@ -527,28 +532,28 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                             ok = false;
                             break;
                         }
-                        if (row < CP) {
-                            const float (*r)[CP + 1] = sh.red[me];
+                        if (row < HALF) {
+                            const float (*r)[HALF + 1] = sh.red[me] + (warp & 4);
                             const float over = fmaxf(fmaxf(r[0][row], r[1][row]), fmaxf(r[2][row], r[3][row]));   // above the bound
-                            const float2 b = sh.col[me][row];
+                            const float2 b = sh.col[me][c0 + row];
                             float by = over > 0.f ? over + MARGIN : 0.f;
                             if (first) by = over == -INFINITY ? 0.f : over + MARGIN_FIRST;   // (a column without a node sees nothing)
-                            sh.moved[me][row] = make_float2(by, ex2(-by));
-                            sh.col[me][row] = make_float2(b.x, b.y + by);
+                            sh.moved[me][c0 + row] = make_float2(by, ex2(-by));
+                            sh.col[me][c0 + row] = make_float2(b.x, b.y + by);
                         }
-                        if (row == 0) {
-                            const float v = fmaxf(fmaxf(sh.red[me][0][CP], sh.red[me][1][CP]), fmaxf(sh.red[me][2][CP], sh.red[me][3][CP]));
+                        if (row == 0 && c0 == 0) {
+                            const float v = fmaxf(fmaxf(sh.red[me][0][HALF], sh.red[me][1][HALF]), fmaxf(sh.red[me][2][HALF], sh.red[me][3][HALF]));
                             if (v > vref) sh.vref[me] = V_MARGIN * v;
                             sh.fresh[me] = 1;
                         }
                         worker_sync(me);
 #pragma unroll
-                        for (int c = 0; c < CP; ++c) {
-                            const float2 by = sh.moved[me][c];
+                        for (int c = 0; c < HALF; ++c) {
+                            const float2 by = sh.moved[me][c0 + c];
                             x[c] -= by.x;
                             sum[c] *= by.y;
                         }
-                        if (filled || summed) drain<INT4, CP>(t_o, t_acc, vref, filled, summed, sh.moved[me]);
+                        if (filled || summed) drain<INT4, CP>(t_o, t_acc, vref, filled, summed, sh.moved[me] + c0);
                         summed |= filled;
                         filled = false;
                     }
@@ -557,10 +562,10 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     if (k > 0) ok = wait(&sh.p_free[me], (k - 1) & 1) && ok;   // the weights of the tile before have been used
                     uint8_t* at8 = sp + (row >> 3) * (N / 16 * 128) + (row & 7) * 16;
 #pragma unroll
-                    for (int c = 0; c < CP; c += 16) {
-                        uint32_t w[3][4];
+                    for (int c = 0; c < HALF; c += 8) {
+                        uint32_t w[3][2];
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
+                        for (int e = 0; e < 8; e += 4) {
                             uint32_t u[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
@@ -575,8 +580,10 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                             w[2][e / 4] = __byte_perm(t2, t3, 0x5410);
                         }
 #pragma unroll
-                        for (int d = 0; d < 3; ++d)
-                            *reinterpret_cast<uint4*>(at8 + (d * CP + c) / 16 * 128) = make_uint4(w[d][0], w[d][1], w[d][2], w[d][3]);
+                        for (int d = 0; d < 3; ++d) {
+                            const int n = d * CP + c0 + c;   // a multiple of 8; 16 columns a chunk
+                            *reinterpret_cast<uint2*>(at8 + (n >> 4) * 128 + (n & 15)) = make_uint2(w[d][0], w[d][1]);
+                        }
                     }
                     umma::fence_smem_to_async();
                     umma::fence_before_sync();
@@ -592,11 +599,11 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     drain<INT4, CP>(t_o, t_acc, sh.vref[me], true, summed, nullptr);
                 }
 #pragma unroll
-                for (int c = 0; c < CP; ++c) {
+                for (int c = 0; c < HALF; ++c) {
                     float l = sum[c];
 #pragma unroll
                     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                    if (lane == 0) sh.red[me][warp & 3][c] = l;
+                    if (lane == 0) sh.red[me][warp & 7][c] = l;
                 }
                 if (!ok) sh.gave_up = 1;
                 softmax_sync();
@@ -610,7 +617,7 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
         }
     } else if (warp < SOFT + LOADERS) {
         // ------------------------------------------------------------ loads
-        const int t = tid - ST;   // thread of the loaders: row t of a tile's scales
+        const int t = tid - ST;
         int it = 0;
         bool ok = true;
         if (!INT4) {
@@ -626,21 +633,20 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     }
                     const KvView& v = ta.ring ? p.ring : p.ref;
                     const uint32_t to = smem_u32(smem) + stage * Z::STAGE;
-                    // eight lanes copy one chunk of eight rows: a core matrix
-                    const int r0 = t >> 5 << 3 | (t & 7), j0 = (t >> 3) & 3;
-#pragma unroll
-                    for (int i = 0; i < TILE / 32; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int r = r0 + 32 * i, ch = j0 + 4 * j;
-                            const size_t src = (ta.row + min(r, ta.rows - 1)) * RD + ch * 16;
-                            const uint32_t dst = to + (r >> 3) * 1024 + ch * 128 + (r & 7) * 16;
-                            cp16(dst, v.k + src);
-                            cp16(dst + Z::KV, v.v + src);
-                        }
-                    const size_t sr = ta.row + min(t, ta.rows - 1);
-                    cp4(smem_u32(&sh.scales[stage][0][t]), v.ks + sr);
-                    cp4(smem_u32(&sh.scales[stage][1][t]), v.vs + sr);
+                    // an instruction copies four chunks of eight rows, eight lanes a core matrix
+                    const int r0 = lane & 7, j0 = lane >> 3;
+                    for (int i = warp - SOFT; i < 2 * TILE / 8; i += LOADERS) {
+                        const int r = (i >> 1 << 3) + r0, ch = (i & 1) * 4 + j0;
+                        const size_t src = (ta.row + min(r, ta.rows - 1)) * RD + ch * 16;
+                        const uint32_t dst = to + (r >> 3) * 1024 + ch * 128 + r0 * 16;
+                        cp16(dst, v.k + src);
+                        cp16(dst + Z::KV, v.v + src);
+                    }
+                    for (int i = t; i < TILE; i += LT) {
+                        const size_t sr = ta.row + min(i, ta.rows - 1);
+                        cp4(smem_u32(&sh.scales[stage][0][i]), v.ks + sr);
+                        cp4(smem_u32(&sh.scales[stage][1][i]), v.vs + sr);
+                    }
                     cp_arrive(&sh.full[stage]);   // once they have landed; the reader passes them on to the tensor core
                 }
                 advance(p, at, left, s);
@@ -663,16 +669,17 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     const TileAt ta = tile_at(p, as, ahead_tile);
                     const KvView& v = ta.ring ? p.ring : p.ref;
                     uint8_t* to = smem + STAGES * Z::STAGE + issued % Z::PACKED * Z::PACK;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // eight lanes copy one chunk of eight rows
-                        const int r = (t >> 5 << 3 | (t & 7)) + 32 * i, j = (t >> 3) & 3;
-                        const size_t src = (ta.row + min(r, ta.rows - 1)) * (RD / 2) + j * 16;
-                        cp16(smem_u32(to + (i * LT + t) * 16), v.k + src);
-                        cp16(smem_u32(to + Z::KV / 2 + (i * LT + t) * 16), v.v + src);
+                    const int r0 = lane & 7, j = lane >> 3;
+                    for (int i = warp - SOFT; i < TILE / 8; i += LOADERS) {   // four chunks of eight rows
+                        const size_t src = (ta.row + min(8 * i + r0, ta.rows - 1)) * (RD / 2) + j * 16;
+                        cp16(smem_u32(to + (i * 32 + lane) * 16), v.k + src);
+                        cp16(smem_u32(to + Z::KV / 2 + (i * 32 + lane) * 16), v.v + src);
                     }
-                    const size_t sr = ta.row + min(t, ta.rows - 1);
-                    cp4(smem_u32(to + Z::KV + 4 * t), v.ks + sr);
-                    cp4(smem_u32(to + Z::KV + 4 * TILE + 4 * t), v.vs + sr);
+                    for (int i = t; i < TILE; i += LT) {
+                        const size_t sr = ta.row + min(i, ta.rows - 1);
+                        cp4(smem_u32(to + Z::KV + 4 * i), v.ks + sr);
+                        cp4(smem_u32(to + Z::KV + 4 * TILE + 4 * i), v.vs + sr);
+                    }
                     ++issued;
                     if (++ahead_tile == as.first + as.count) have = false;
                 }
@@ -692,16 +699,20 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     }
                     const uint8_t* fr = smem + STAGES * Z::STAGE + it % Z::PACKED * Z::PACK;
                     uint8_t* to = smem + stage * Z::STAGE;
+                    const int r0 = lane & 7, j = lane >> 3;
+                    for (int i = warp - SOFT; i < TILE / 8; i += LOADERS) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = (t >> 5 << 3 | (t & 7)) + 32 * (i & 3), j = (t >> 3) & 3, kv = i >> 2;
-                        const uint4 n = lds128(fr + kv * (Z::KV / 2) + ((i & 3) * LT + t) * 16);
-                        uint8_t* dst = to + kv * Z::KV + (r >> 3) * 1024 + 2 * j * 128 + (r & 7) * 16;
-                        *reinterpret_cast<uint4*>(dst) = make_uint4((n.x << 4) & 0xF0F0F0F0u, (n.y << 4) & 0xF0F0F0F0u, (n.z << 4) & 0xF0F0F0F0u, (n.w << 4) & 0xF0F0F0F0u);
-                        *reinterpret_cast<uint4*>(dst + 128) = make_uint4(n.x & 0xF0F0F0F0u, n.y & 0xF0F0F0F0u, n.z & 0xF0F0F0F0u, n.w & 0xF0F0F0F0u);
+                        for (int kv = 0; kv < 2; ++kv) {
+                            const uint4 n = lds128(fr + kv * (Z::KV / 2) + (i * 32 + lane) * 16);
+                            uint8_t* dst = to + kv * Z::KV + i * 1024 + 2 * j * 128 + r0 * 16;
+                            *reinterpret_cast<uint4*>(dst) = make_uint4((n.x << 4) & 0xF0F0F0F0u, (n.y << 4) & 0xF0F0F0F0u, (n.z << 4) & 0xF0F0F0F0u, (n.w << 4) & 0xF0F0F0F0u);
+                            *reinterpret_cast<uint4*>(dst + 128) = make_uint4(n.x & 0xF0F0F0F0u, n.y & 0xF0F0F0F0u, n.z & 0xF0F0F0F0u, n.w & 0xF0F0F0F0u);
+                        }
                     }
-                    sh.scales[stage][0][t] = *reinterpret_cast<const float*>(fr + Z::KV + 4 * t);
-                    sh.scales[stage][1][t] = *reinterpret_cast<const float*>(fr + Z::KV + 4 * TILE + 4 * t);
+                    for (int i = t; i < TILE; i += LT) {
+                        sh.scales[stage][0][i] = *reinterpret_cast<const float*>(fr + Z::KV + 4 * i);
+                        sh.scales[stage][1][i] = *reinterpret_cast<const float*>(fr + Z::KV + 4 * TILE + 4 * i);
+                    }
                     umma::fence_smem_to_async();
                     mbar_arrive(&sh.full[stage]);
                 }
@@ -761,6 +772,7 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                             moved = true;
                         }
                     }
+                    if (!moved) __nanosleep(32);
                     if (moved) {
                         since = globaltimer_ns();
                     } else if (__any_sync(0xffffffffu, globaltimer_ns() - since > LIMIT_NS || *(volatile int*)&sh.gave_up)) {
