@@ -63,18 +63,6 @@ __device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint3
 __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// whether the barrier's phase of that parity is over (asked once, for the whole warp)
-__device__ __forceinline__ bool is_over(uint64_t* bar, uint32_t parity) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return __all_sync(0xffffffffu, r != 0);
-}
 // eight columns of the thread's tensor-memory lane; complete after wait_ld()
 __device__ __forceinline__ void ld8(uint32_t taddr, int (&v)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -635,7 +623,10 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     const uint32_t to = smem_u32(smem) + stage * Z::STAGE;
                     // an instruction copies four chunks of eight rows, eight lanes a core matrix
                     const int r0 = lane & 7, j0 = lane >> 3;
-                    for (int i = warp - SOFT; i < 2 * TILE / 8; i += LOADERS) {
+#pragma unroll
+                    for (int e = 0; e < (2 * TILE / 8 + LOADERS - 1) / LOADERS; ++e) {
+                        const int i = warp - SOFT + e * LOADERS;
+                        if (i >= 2 * TILE / 8) break;
                         const int r = (i >> 1 << 3) + r0, ch = (i & 1) * 4 + j0;
                         const size_t src = (ta.row + min(r, ta.rows - 1)) * RD + ch * 16;
                         const uint32_t dst = to + (r >> 3) * 1024 + ch * 128 + r0 * 16;
@@ -670,7 +661,10 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     const KvView& v = ta.ring ? p.ring : p.ref;
                     uint8_t* to = smem + STAGES * Z::STAGE + issued % Z::PACKED * Z::PACK;
                     const int r0 = lane & 7, j = lane >> 3;
-                    for (int i = warp - SOFT; i < TILE / 8; i += LOADERS) {   // four chunks of eight rows
+#pragma unroll
+                    for (int e = 0; e < (TILE / 8 + LOADERS - 1) / LOADERS; ++e) {   // four chunks of eight rows
+                        const int i = warp - SOFT + e * LOADERS;
+                        if (i >= TILE / 8) break;
                         const size_t src = (ta.row + min(8 * i + r0, ta.rows - 1)) * (RD / 2) + j * 16;
                         cp16(smem_u32(to + (i * 32 + lane) * 16), v.k + src);
                         cp16(smem_u32(to + Z::KV / 2 + (i * 32 + lane) * 16), v.v + src);
@@ -700,13 +694,22 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
                     const uint8_t* fr = smem + STAGES * Z::STAGE + it % Z::PACKED * Z::PACK;
                     uint8_t* to = smem + stage * Z::STAGE;
                     const int r0 = lane & 7, j = lane >> 3;
-                    for (int i = warp - SOFT; i < TILE / 8; i += LOADERS) {
+                    constexpr int EACH = (TILE / 8 + LOADERS - 1) / LOADERS;
 #pragma unroll
-                        for (int kv = 0; kv < 2; ++kv) {
-                            const uint4 n = lds128(fr + kv * (Z::KV / 2) + (i * 32 + lane) * 16);
+                    for (int kv = 0; kv < 2; ++kv) {
+                        uint4 n[EACH];
+#pragma unroll
+                        for (int e = 0; e < EACH; ++e) {
+                            const int i = min(warp - SOFT + e * LOADERS, TILE / 8 - 1);   // (the last one twice by some warps)
+                            n[e] = lds128(fr + kv * (Z::KV / 2) + (i * 32 + lane) * 16);
+                        }
+#pragma unroll
+                        for (int e = 0; e < EACH; ++e) {
+                            const int i = warp - SOFT + e * LOADERS;
+                            if (i >= TILE / 8) break;
                             uint8_t* dst = to + kv * Z::KV + i * 1024 + 2 * j * 128 + r0 * 16;
-                            *reinterpret_cast<uint4*>(dst) = make_uint4((n.x << 4) & 0xF0F0F0F0u, (n.y << 4) & 0xF0F0F0F0u, (n.z << 4) & 0xF0F0F0F0u, (n.w << 4) & 0xF0F0F0F0u);
-                            *reinterpret_cast<uint4*>(dst + 128) = make_uint4(n.x & 0xF0F0F0F0u, n.y & 0xF0F0F0F0u, n.z & 0xF0F0F0F0u, n.w & 0xF0F0F0F0u);
+                            *reinterpret_cast<uint4*>(dst) = make_uint4((n[e].x << 4) & 0xF0F0F0F0u, (n[e].y << 4) & 0xF0F0F0F0u, (n[e].z << 4) & 0xF0F0F0F0u, (n[e].w << 4) & 0xF0F0F0F0u);
+                            *reinterpret_cast<uint4*>(dst + 128) = make_uint4(n[e].x & 0xF0F0F0F0u, n[e].y & 0xF0F0F0F0u, n[e].z & 0xF0F0F0F0u, n[e].w & 0xF0F0F0F0u);
                         }
                     }
                     for (int i = t; i < TILE; i += LT) {
@@ -722,66 +725,54 @@ __global__ void __launch_bounds__(PT, 1) rswa_wide_kernel(const __grid_constant_
         }
     } else {
         // ------------------------------------------------------------ products
+        // One thread, with as few instructions a tile as can be: it shares its scheduler with five other warps, and a
+        // tile is worth 1500 cycles of memory.
         constexpr uint32_t IS = idesc_i8(N, true, false, false), IO = idesc_i8(N, false, true, true);
-        const uint32_t sq = smem_u32(smem) + Z::Q_OFF;
-        int it = 0, seg = 0, scores[2] = {0, 0}, done[2] = {0, 0};   // tiles before the segment; each worker's so far
+        constexpr uint32_t P_GROUP = N / 16 * 128;   // bytes of eight keys' weights
+        const uint64_t k_desc = umma::sdesc_kmajor(smem_u32(smem), 128, 1024), v_desc = umma::sdesc_kmajor(smem_u32(smem) + Z::KV, 1024, 128);
+        const uint64_t q_desc = umma::sdesc_kmajor(smem_u32(smem) + Z::Q_OFF, 128, 1024);
+        const uint64_t p_desc = umma::sdesc_kmajor(smem_u32(smem) + Z::P_OFF, P_GROUP, 128);
+        const uint32_t empty0 = smem_u32(&sh.empty[0]);
+        int stage_s = 0, phase_s = 0, stage_p = 0, scores = 0, done = 0, seg = 0;   // scores, done: bit w is worker w's phase
         bool ok = true;
         while (left > 0 && ok) {
             const Segment s = segment_at(p, at, left);
-            if (s.count > 0) {
+            if (lane == 0 && s.count > 0) {
                 ok = wait(&sh.q_full, seg & 1);
                 ++seg;
-                // whichever product is ready: S of tile ns (its codes have landed, its worker has read the S before), or
-                // P V of tile np (its weights are written)
-                int ns = 0, np = 0;
-                uint64_t since = globaltimer_ns();
-                while (ok && np < s.count) {
-                    bool moved = false;
-                    if (ns < s.count) {
-                        const int stage = (it + ns) % STAGES, w = ns & 1;
-                        if (is_over(&sh.full[stage], (it + ns) / STAGES & 1) && is_over(&sh.s_free[w], scores[w] & 1)) {
-                            umma::fence_smem_to_async();
-                            umma::fence_after_sync();
-                            if (lane == 0) {
-                                const uint32_t k0 = smem_u32(smem) + stage * Z::STAGE;
+                for (int i = 0; i < s.count + 2 && ok; ++i) {
+                    const int w = i & 1;
+                    if (i > 1) {   // O += V^T P of tile i - 2, which frees its worker's weights and its place
+                        ok = wait(&sh.p_full[w], done >> w & 1);
+                        if (!ok) break;
+                        done ^= 1 << w;
+                        umma::fence_after_sync();
+                        const bool fresh = *(volatile int*)&sh.fresh[w] != 0;
+                        const uint64_t v = v_desc + (uint32_t)(stage_p * (Z::STAGE >> 4)), pw = p_desc + (uint32_t)(w * (N * TILE >> 4));
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)   // 32 dims each: two chunks
-                                    mma_i8(tmem + w * N, umma::sdesc_kmajor(k0 + 256 * k, 128, 1024), umma::sdesc_kmajor(sq + 256 * k, 128, 1024), IS, true);
-                                umma::commit(smem_u32(&sh.s_full[w]));
-                            }
-                            ++scores[w], ++ns;
-                            moved = true;
-                        }
+                        for (int k = 0; k < 4; ++k)   // 32 keys each: four groups of eight rows
+                            mma_i8(tmem + Z::T_O + w * N, v + (4096 >> 4) * k, pw + (4 * P_GROUP >> 4) * k, IO, k > 0 || !fresh);
+                        *(volatile int*)&sh.fresh[w] = 0;
+                        umma::commit(smem_u32(&sh.p_free[w]));
+                        umma::commit(empty0 + 8 * stage_p);
+                        if (++stage_p == STAGES) stage_p = 0;
                     }
-                    if (np < ns) {
-                        const int stage = (it + np) % STAGES, w = np & 1;
-                        if (is_over(&sh.p_full[w], done[w] & 1)) {
-                            umma::fence_after_sync();
-                            if (lane == 0) {
-                                const bool fresh = *(volatile int*)&sh.fresh[w] != 0;
-                                const uint32_t v = smem_u32(smem) + stage * Z::STAGE + Z::KV, sp = smem_u32(smem) + Z::P_OFF + w * N * TILE;
+                    if (i < s.count) {   // S of tile i
+                        ok = wait(&sh.full[stage_s], phase_s) && wait(&sh.s_free[w], scores >> w & 1);
+                        if (!ok) break;
+                        scores ^= 1 << w;
+                        if (!INT4) umma::fence_smem_to_async();   // (the loaders of int4 have done it)
+                        umma::fence_after_sync();
+                        const uint64_t kd = k_desc + (uint32_t)(stage_s * (Z::STAGE >> 4));
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)   // 32 keys each: four groups of eight rows
-                                    mma_i8(tmem + Z::T_O + w * N, umma::sdesc_kmajor(v + 4096 * k, 1024, 128),
-                                           umma::sdesc_kmajor(sp + 4 * (N / 16 * 128) * k, N / 16 * 128, 128), IO, !(fresh && k == 0));
-                                *(volatile int*)&sh.fresh[w] = 0;
-                                umma::commit(smem_u32(&sh.p_free[w]));
-                                umma::commit(smem_u32(&sh.empty[stage]));
-                            }
-                            ++done[w], ++np;
-                            moved = true;
-                        }
-                    }
-                    if (!moved) __nanosleep(32);
-                    if (moved) {
-                        since = globaltimer_ns();
-                    } else if (__any_sync(0xffffffffu, globaltimer_ns() - since > LIMIT_NS || *(volatile int*)&sh.gave_up)) {
-                        sh.gave_up = 1;
-                        ok = false;
+                        for (int k = 0; k < 4; ++k)   // 32 dims each: two chunks
+                            mma_i8(tmem + w * N, kd + (256 >> 4) * k, q_desc + (256 >> 4) * k, IS, true);
+                        umma::commit(smem_u32(&sh.s_full[w]));
+                        if (++stage_s == STAGES) stage_s = 0, phase_s ^= 1;
                     }
                 }
             }
-            it += s.count;
+            ok = __all_sync(0xffffffffu, ok);
             advance(p, at, left, s);
         }
     }
