@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfocr_moe.so")
 SOURCES = ["api.cu", "router.cu", "expert_tc.cu", "tcgen05_selftest.cu", "expert_decode.cu", "decode_small.cu", "noalloc.cu", "lm_head.cu", "rmsnorm.cu", "w8a8.cu", "rswa.cu", "qk_rope.cu", "kv_cache.cu",
-           "rswa_tree.cu", "rswa_wide.cu", "spec_verify.cu", "pack.cpp"]
+           "rswa_tree.cu", "rswa_ranges.cu", "spec_verify.cu", "pack.cpp"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

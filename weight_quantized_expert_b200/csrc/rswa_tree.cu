@@ -48,17 +48,7 @@ namespace focr {
 namespace {
 
 constexpr int RD = TREE_DIM, RW = TREE_RING;
-constexpr int COLS = 16;                        // columns of a CTA: the rows of one MMA tile
-constexpr int BLK = 64;                         // keys of a block
 constexpr int WARPS = 8, PAIRS = WARPS / 2, PT = 32 * WARPS;   // two warps work on a block
-constexpr int PAD = RD + 8;                     // floats per row of a pair's partial output: no bank conflicts
-
-template <bool INT4>
-struct Stage {   // a pair's part of shared memory: one block of keys; later its partial output
-    static constexpr int ROW = INT4 ? RD / 2 : RD;
-    static constexpr int V = BLK * ROW, KS = 2 * BLK * ROW, VS = KS + 4 * BLK, LOADS = VS + 4 * BLK;
-    static constexpr int BYTES = LOADS > COLS * PAD * 4 ? LOADS : COLS * PAD * 4;
-};
 
 struct Shared {
     uint4 qf[4 * 3][32];               // query digits as A fragments: [k-step * 3 + digit][lane]
@@ -72,46 +62,6 @@ struct Shared {
     unsigned long long line[TREE_MAX];
     int par[TREE_MAX];
 };
-
-// d = a (16 x 32) * b (32 x 8) + c.  A_S8: a is signed like b (the query's top digit); else a holds unsigned digits.
-template <bool A_S8>
-__device__ __forceinline__ void mma(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, int c0, int c1, int c2, int c3) {
-    if (A_S8)
-        asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-            : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
-    else
-        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-            : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
-}
-// the same, with the accumulator started (FIRST) at the pattern that reads as MAGIC + sum
-template <bool A_S8, bool FIRST>
-__device__ __forceinline__ void mma(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if (FIRST)
-        mma<A_S8>(d, a, b0, b1, MAGIC_BITS, MAGIC_BITS, MAGIC_BITS, MAGIC_BITS);
-    else
-        mma<A_S8>(d, a, b0, b1, d[0], d[1], d[2], d[3]);
-}
-// bytes of four words, transposed: o[i] = byte i of a, b, c, d
-__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&o)[4]) {
-    const uint32_t t0 = __byte_perm(a, b, 0x5140), t1 = __byte_perm(c, d, 0x5140);
-    const uint32_t t2 = __byte_perm(a, b, 0x7362), t3 = __byte_perm(c, d, 0x7362);
-    o[0] = __byte_perm(t0, t1, 0x5410), o[1] = __byte_perm(t0, t1, 0x7632);
-    o[2] = __byte_perm(t2, t3, 0x5410), o[3] = __byte_perm(t2, t3, 0x7632);
-}
-
-// Shared-memory offset of 16-byte chunk j of row r; the swizzles spread the chunks that eight lanes read together
-// (K: rows 2i and 2i + 1; V: rows 0, 2, 4, 6) over all banks.
-template <bool INT4>
-__device__ __forceinline__ int k_off(int r, int j) {
-    return INT4 ? r * 64 + j * 16 : r * 128 + ((j ^ ((r & 1) << 2)) << 4);
-}
-template <bool INT4>
-__device__ __forceinline__ int v_off(int r, int j) {
-    const int x = ((r >> 1) & 3) << 1;
-    return INT4 ? (r >> 1) * 128 + ((((r & 1) << 2 | j) ^ x) << 4) : r * 128 + ((j ^ x) << 4);
-}
 
 // Starts the copies of a warp's 32 rows of a block's codes; a whole block's addresses are one base and constants.
 template <bool INT4>
@@ -226,26 +176,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
     for (int i = 0; i < MINE; ++i) {
         const int col = warp + i * WARPS;
         const float4 x = q[i];
-        float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        a = fmaxf(a, TINY);
-        const float inv = Q_TOP / a;
-        const int f[4] = {__float2int_rn(x.x * inv), __float2int_rn(x.y * inv), __float2int_rn(x.z * inv), __float2int_rn(x.w * inv)};
-        const int tl = (col & 7) * 4, hi = col >> 3;
-#pragma unroll
-        for (int d = 0; d < 3; ++d) {
-            const uint32_t v0 = (f[0] >> 8 * d) & 255, v1 = (f[1] >> 8 * d) & 255, v2 = (f[2] >> 8 * d) & 255, v3 = (f[3] >> 8 * d) & 255;
-            if (INT4) {   // dims 32 c + 8 s + 2 i in the first word of a k-step, + 1 in the second
-                const int s = (lane >> 1) & 3, cc = lane >> 3;
-                uint16_t* w = reinterpret_cast<uint16_t*>(&sh.qf[s * 3 + d][tl + cc]);
-                w[2 * hi + (lane & 1)] = (uint16_t)(v0 | v2 << 8);
-                w[2 * (2 + hi) + (lane & 1)] = (uint16_t)(v1 | v3 << 8);
-            } else {      // dims 64 (s / 2) + 16 c + 8 (s % 2) + i, + 4 in the second
-                const int s = 2 * (lane >> 4) + ((lane >> 1) & 1), cc = (lane >> 2) & 3;
-                reinterpret_cast<uint32_t*>(&sh.qf[s * 3 + d][tl + cc])[2 * (lane & 1) + hi] = v0 | v1 << 8 | v2 << 16 | v3 << 24;
-            }
-        }
+        const float a = query_digits<INT4>(x, col, lane, sh.qf);
         if (lane == 0) sh.step[col] = a / Q_TOP * (SCORE_SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
         const DraftPart a4 = draft_attend(p, b, h, lane, x, line[i], kk[i], vv[i]);
         reinterpret_cast<float4*>(sh.part[col])[lane] = a4.o;
@@ -538,7 +469,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
 // per SM) with at most two blocks a pair, else the many-units kernel.
 struct TreePlan {
     int groups, S;
-    bool wide;
+    bool ranges;
 };
 TreePlan tree_plan(int B, int N, int heads_q, int heads, int cap) {
     const int sms = device_sms() > 0 ? device_sms() : 148;
@@ -549,7 +480,7 @@ TreePlan tree_plan(int B, int N, int heads_q, int heads, int cap) {
     pl.S = 1;
     while (pl.S < 8 && pl.S * PAIRS < blocks) pl.S *= 2;
     while (pl.S > 1 && units * pl.S > 2 * sms) pl.S /= 2;
-    pl.wide = blocks > 2 * pl.S * PAIRS;
+    pl.ranges = blocks > 2 * pl.S * PAIRS;
     return pl;
 }
 
@@ -574,7 +505,7 @@ extern "C" size_t focr_rswa_tree_workspace_bytes(int32_t B, int32_t N, int32_t h
     if (B < 1 || N < 1 || heads < 1 || heads_q < heads || heads_q > FOCR_HEADS_MAX || B > FOCR_RSWA_B_MAX ||
         ref_cap > FOCR_RSWA_RCAP_MAX || N > TREE_MAX)
         return 0;
-    return tree_plan(B, N, heads_q, heads, ref_cap).wide ? wide_part_bytes() : 0;
+    return tree_plan(B, N, heads_q, heads, ref_cap).ranges ? ranges_part_bytes() : 0;
 }
 
 extern "C" focr_status focr_rswa_tree(const float* q, const float* k_new, const float* v_new, int32_t B, int32_t N,
@@ -615,8 +546,8 @@ extern "C" focr_status focr_rswa_tree(const float* q, const float* k_new, const 
     p.part = reinterpret_cast<float*>(workspace);
     const bool wide = N * G > 8, int4 = ref->type == FOCR_W_INT4;
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = pl.wide ? launch_wide(p, int4, st)
-                          : int4  ? (wide ? launch_tree<true, true>(p, pl, st) : launch_tree<true, false>(p, pl, st))
+    const cudaError_t e = pl.ranges ? (p.groups = pl.groups, launch_ranges(p, int4, st))
+                            : int4  ? (wide ? launch_tree<true, true>(p, pl, st) : launch_tree<true, false>(p, pl, st))
                                   : (wide ? launch_tree<false, true>(p, pl, st) : launch_tree<false, false>(p, pl, st));
     return report_launch(e, "rswa_tree_kernel");
 }

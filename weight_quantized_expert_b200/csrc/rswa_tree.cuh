@@ -1,4 +1,4 @@
-// What the two kernels of the tree attention share (rswa_tree.cu, rswa_wide.cu).
+// What the two kernels of the tree attention share (rswa_tree.cu, rswa_ranges.cu).
 #pragma once
 
 #include "common.cuh"
@@ -8,6 +8,9 @@ namespace focr {
 
 constexpr int TREE_DIM = FOCR_RSWA_DIM, TREE_RING = FOCR_RSWA_RING;
 constexpr int TREE_MAX = FOCR_TREE_NODES_MAX;
+constexpr int COLS = 16;                        // columns of a unit: the rows of one MMA tile
+constexpr int BLK = 64;                         // keys of a block
+constexpr int PAD = TREE_DIM + 8;               // floats per row of a warp's partial output: no bank conflicts
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float SCORE_SCALE = 0.08838834764831845f;   // 1 / sqrt(128)
 constexpr float Q_TOP = 8323072.f;              // 127 * 2^16: the largest fixed-point query value
@@ -17,12 +20,19 @@ constexpr int MAGIC_BITS = 0x4B400000;
 constexpr float NONE = -1e30f;                  // running maximum of a column that has seen no key
 constexpr float TINY = 1e-30f;                  // magnitudes below this share its step
 
+template <bool INT4>
+struct Stage {   // where a block of keys lies in shared memory: one block of keys; later its partial output
+    static constexpr int ROW = INT4 ? TREE_DIM / 2 : TREE_DIM;
+    static constexpr int V = BLK * ROW, KS = 2 * BLK * ROW, VS = KS + 4 * BLK, LOADS = VS + 4 * BLK;
+    static constexpr int BYTES = LOADS > COLS * PAD * 4 ? LOADS : COLS * PAD * 4;
+};
+
 struct TreeParams {
     const float *q, *k_new, *v_new;
     KvView ref, ring;
     const int32_t *ref_len, *n_gen, *parent, *n_nodes;
     float* out;
-    int B, N, hq, hk, G, S, groups;   // clusters: S CTAs each, groups of 16 columns per kv head
+    int B, N, hq, hk, G, S, groups;   // groups of 16 columns per kv head; clusters: S CTAs each
     float* part;                      // ranges: two partial results per CTA
 };
 
@@ -50,6 +60,73 @@ __device__ __forceinline__ float lower(int d1, int d0) {
     return fmaf(__int_as_float(d1), 256.f, -257.f * MAGIC) + __int_as_float(d0);
 }
 __device__ __forceinline__ float upper(int d2) { return fmaf(__int_as_float(d2), 65536.f, -65536.f * MAGIC); }
+
+// d = a (16 x 32) * b (32 x 8) + c.  A_S8: a is signed like b (the query's top digit); else a holds unsigned digits.
+template <bool A_S8>
+__device__ __forceinline__ void mma(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, int c0, int c1, int c2, int c3) {
+    if (A_S8)
+        asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
+    else
+        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
+}
+// the same, with the accumulator started (FIRST) at the pattern that reads as MAGIC + sum
+template <bool A_S8, bool FIRST>
+__device__ __forceinline__ void mma(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (FIRST)
+        mma<A_S8>(d, a, b0, b1, MAGIC_BITS, MAGIC_BITS, MAGIC_BITS, MAGIC_BITS);
+    else
+        mma<A_S8>(d, a, b0, b1, d[0], d[1], d[2], d[3]);
+}
+// bytes of four words, transposed: o[i] = byte i of a, b, c, d
+__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&o)[4]) {
+    const uint32_t t0 = __byte_perm(a, b, 0x5140), t1 = __byte_perm(c, d, 0x5140);
+    const uint32_t t2 = __byte_perm(a, b, 0x7362), t3 = __byte_perm(c, d, 0x7362);
+    o[0] = __byte_perm(t0, t1, 0x5410), o[1] = __byte_perm(t0, t1, 0x7632);
+    o[2] = __byte_perm(t2, t3, 0x5410), o[3] = __byte_perm(t2, t3, 0x7632);
+}
+
+// Shared-memory offset of 16-byte chunk j of row r; the swizzles spread the chunks that eight lanes read together
+// (K: rows 2i and 2i + 1; V: rows 0, 2, 4, 6) over all banks.
+template <bool INT4>
+__device__ __forceinline__ int k_off(int r, int j) {
+    return INT4 ? r * 64 + j * 16 : r * 128 + ((j ^ ((r & 1) << 2)) << 4);
+}
+template <bool INT4>
+__device__ __forceinline__ int v_off(int r, int j) {
+    const int x = ((r >> 1) & 3) << 1;
+    return INT4 ? (r >> 1) * 128 + ((((r & 1) << 2 | j) ^ x) << 4) : r * 128 + ((j ^ x) << 4);
+}
+
+// Writes a query row (four dims a lane) as digits of column `col` into the A fragments qf[k-step * 3 + digit][lane], and
+// returns the row's largest magnitude.
+template <bool INT4>
+__device__ __forceinline__ float query_digits(float4 x, int col, int lane, uint4 (*qf)[32]) {
+    float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    a = fmaxf(a, TINY);
+    const float inv = Q_TOP / a;
+    const int f[4] = {__float2int_rn(x.x * inv), __float2int_rn(x.y * inv), __float2int_rn(x.z * inv), __float2int_rn(x.w * inv)};
+    const int tl = (col & 7) * 4, hi = col >> 3;
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+        const uint32_t v0 = (f[0] >> 8 * d) & 255, v1 = (f[1] >> 8 * d) & 255, v2 = (f[2] >> 8 * d) & 255, v3 = (f[3] >> 8 * d) & 255;
+        if (INT4) {   // dims 32 c + 8 s + 2 i in the first word of a k-step, + 1 in the second
+            const int s = (lane >> 1) & 3, cc = lane >> 3;
+            uint16_t* w = reinterpret_cast<uint16_t*>(&qf[s * 3 + d][tl + cc]);
+            w[2 * hi + (lane & 1)] = (uint16_t)(v0 | v2 << 8);
+            w[2 * (2 + hi) + (lane & 1)] = (uint16_t)(v1 | v3 << 8);
+        } else {      // dims 64 (s / 2) + 16 c + 8 (s % 2) + i, + 4 in the second
+            const int s = 2 * (lane >> 4) + ((lane >> 1) & 1), cc = (lane >> 2) & 3;
+            reinterpret_cast<uint32_t*>(&qf[s * 3 + d][tl + cc])[2 * (lane & 1) + hi] = v0 | v1 << 8 | v2 << 16 | v3 << 24;
+        }
+    }
+    return a;
+}
 
 // Four drafted rows of a line (`rest`: bits of its nodes, the four lowest are taken), four dims a lane.
 __device__ __forceinline__ void draft_load(const TreeParams& p, int b, int h, int lane, unsigned long long& rest, float4 (&k4)[4],
@@ -109,9 +186,8 @@ __device__ __forceinline__ DraftPart draft_attend(const TreeParams& p, int b, in
     return a;
 }
 
-// The many-units kernel (rswa_wide.cu): its CTAs, its partial results' bytes, its launch.
-int wide_ctas();
-size_t wide_part_bytes();
-cudaError_t launch_wide(TreeParams& p, bool int4, cudaStream_t st);
+// The many-units kernel (rswa_ranges.cu): its partial results' bytes, its launch.
+size_t ranges_part_bytes();
+cudaError_t launch_ranges(TreeParams& p, bool int4, cudaStream_t st);
 
 }  // namespace focr
