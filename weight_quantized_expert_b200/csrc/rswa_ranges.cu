@@ -344,16 +344,17 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
             tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
             tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
             const bool any = tm != -INFINITY;
-            const float mb = any ? tm * step[e] : 0.f;
+            // a little above the largest score, so that no rounding makes a weight larger than 1
+            const float mb = any ? fmaf(fabsf(tm * step[e]), 2.4e-7f, tm * step[e]) : 0.f;
             float sum = 0.f;
             uint32_t u[8][2];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float w = ex2(fminf(fmaf(T[j][2 * e + i], step[e], -mb), 0.f));
+                    const float w = ex2(fmaf(T[j][2 * e + i], step[e], -mb));
                     sum += w;
-                    u[j][i] = __float2uint_rn(w * vs[j][i]);
+                    u[j][i] = __float_as_uint(fmaf(w, vs[j][i], P_MAGIC));
                 }
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)

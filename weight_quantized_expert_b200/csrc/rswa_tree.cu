@@ -19,7 +19,7 @@
 //             follow in fp32.
 //   softmax   online over blocks of 64 keys, base 2, per warp.
 //   values    out needs sum_j e_j vs_j vc_j.  The weights of a block, relative to the block's largest score and
-//             largest value scale, are written as three unsigned digits (step 2^-24); the three integer sums over the
+//             largest value scale, are written as three unsigned digits (step 2^-23); the three integer sums over the
 //             64 keys are exact, join in fp32 and are added to the fp32 accumulator with the block's factor.
 //   No sum can wrap or leave a float's exact integers: |sum| <= 128 * 128 * 255 < 2^22, so accumulators start at the
 //   bit pattern of 1.5 * 2^23 and are read back as floats by one subtraction.
@@ -295,16 +295,17 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         for (int e = 0; e < HALVES; ++e) {
             tm[e] = fmaxf(tm[e], sh.mx[pair][half ^ 1][gr + 8 * e]);
             const bool any = tm[e] != -INFINITY;
-            const float mb = any ? tm[e] * step[e] : 0.f;
+            // a little above the largest score, so that no rounding makes a weight larger than 1
+            const float mb = any ? fmaf(fabsf(tm[e] * step[e]), 2.4e-7f, tm[e] * step[e]) : 0.f;
             float sum = 0.f;
             uint32_t u[4][2];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float w = ex2(fminf(fmaf(T[j][2 * e + i], step[e], -mb), 0.f));
+                    const float w = ex2(fmaf(T[j][2 * e + i], step[e], -mb));
                     sum += w;
-                    u[j][i] = __float2uint_rn(w * vs[j][i]);
+                    u[j][i] = __float_as_uint(fmaf(w, vs[j][i], P_MAGIC));
                 }
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
