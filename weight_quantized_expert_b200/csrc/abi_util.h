@@ -35,6 +35,23 @@ inline bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
     return (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
 }
 
+// A caller's buffer.
+struct Span {
+    const void* at;
+    size_t bytes;
+};
+// Whether one of `n` outputs shares a byte with another one or with one of `m` inputs (NULL buffers share none).
+inline bool outputs_overlap(const Span* out, int n, const Span* in, int m) {
+    for (int i = 0; i < n; ++i) {
+        if (!out[i].at) continue;
+        for (int j = i + 1; j < n; ++j)
+            if (out[j].at && ranges_overlap(out[i].at, out[i].bytes, out[j].at, out[j].bytes)) return true;
+        for (int j = 0; j < m; ++j)
+            if (in[j].at && ranges_overlap(out[i].at, out[i].bytes, in[j].at, in[j].bytes)) return true;
+    }
+    return false;
+}
+
 // Launch with programmatic stream serialisation; cluster > 1 sets the cluster's x extent.
 inline cudaError_t launch_kernel(const void* fn, dim3 grid, dim3 block, size_t smem, int cluster, void** args,
                                  cudaStream_t st) {

@@ -16,10 +16,22 @@
 // values are exact or nearly so); sums run in a fixed order.
 //
 // Both are bound by memory (one row of V floats read and written; one row of p and q read per rejection), and by
-// latency for few rows.  A row belongs to a cluster of up to eight CTAs, which exchange one pair of numbers through
-// distributed shared memory; token_probs keeps its part of the row in shared memory, so the row is read once.  The
-// verification looks up p and q of all drafted tokens at once before it walks, so an accepted node costs no memory
-// latency; a rejection is one pass over the rows, spread over the cluster's warps.
+// latency for few rows.  A row belongs to a cluster of up to eight CTAs, whose sums meet in distributed shared memory.
+//
+// token_probs: as many clusters as stay resident take rows in turn.  A row is read once, by asynchronous copies that
+// are in flight while the row before is worked on, and stays in registers (KEPT groups of four values a thread; what a
+// row has beyond that is read again).  The CTAs send each other maximum and sum by st.async on a barrier in shared
+// memory; a cluster barrier would wait for the stores of the row's probabilities as well.  A wait that runs out (it
+// needs a CTA of the cluster to stop) gives NaN.  289 rows of 129280: 68 us, 4.4 TB/s (a cluster per
+// row, without copies ahead: 87 us; taking rows in turn with a cluster barrier: 104 us); one row of 129280: 6.1 us.  Each row has one
+// serial exchange through the cluster between its loads and its stores; that is what is left.
+//
+// spec_verify: p and q of all drafted tokens are looked up at once before the walk, so an accepted node costs no memory
+// latency; a rejection is one pass over the rows, spread over the cluster's warps.  The tiles' sums stay in shared
+// memory and lead to the next token's tile without a second pass over the rows.  One tree of 4 nodes: 9.0 us; 32 trees
+// of 16 nodes, V = 129280: 25 us (with the warps' tiles summed a second time and the answer agreed on by two more
+// cluster barriers: 12.3 and 25.4 us).  What is left is the chain of passes: up to one per rejected sibling, each a
+// cluster-wide sum.
 #include <math.h>
 
 #include "abi_util.h"
@@ -31,7 +43,7 @@ namespace focr {
 namespace {
 
 constexpr int TREE_MAX = FOCR_TREE_NODES_MAX;
-constexpr int VT = 512, VWARPS = VT / 32;
+constexpr int VT = 512, VWARPS = VT / 32;   // threads of the verification
 constexpr int CLUSTER_MAX = 8;
 
 // ------------------------------------------------------------------ probabilities
@@ -253,11 +265,14 @@ struct VerifyParams {
     int N, V, C, vec;
 };
 
+constexpr int TILE = 128;   // tokens a warp takes at a time
+constexpr int BATCH = 4;    // tiles in flight
+constexpr int TILES_MAX = (FOCR_V_MAX / TILE + CLUSTER_MAX - 1) / CLUSTER_MAX + VWARPS;   // of a CTA
+
 struct VerifyShared {
     double p[TREE_MAX], q[TREE_MAX], u[TREE_MAX + 1];   // of each node's token behind its parent
     int par[TREE_MAX], tok[TREE_MAX], gone[TREE_MAX];
-    double warp_sum[VWARPS], cta_sum[2];
-    int bad, next, last, cta_next, cta_last;
+    double tile_sum[TILES_MAX], warp_sum[VWARPS], cta_sum[2];
 };
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -286,9 +301,6 @@ struct Residual {
         return is_gone(t) ? 0. : (double)__ldg(p + t);
     }
 };
-
-constexpr int TILE = 128;   // tokens a warp takes at a time
-constexpr int BATCH = 4;    // tiles in flight
 
 // The lane's share of one tile's sum of W.  vec: four neighbours of an aligned row, else four tokens 32 apart.
 __device__ __forceinline__ void tile_load(const float* x, int tile, int lane, int V, bool vec, float (&o)[4]) {
@@ -328,8 +340,8 @@ __device__ __forceinline__ void batch_sums(const Residual& w, int t0, int t1, in
     }
 }
 
-// sum of W in every thread of the cluster; the warp's and the CTAs' parts stay in shared memory
-__device__ double row_sum(const Residual& w, const VerifyParams& p, VerifyShared& sh, int rank, int t0, int t1, int& turn) {
+// Sum of W in every thread of the cluster; the tiles', warps' and CTAs' parts stay in shared memory.
+__device__ double row_sum(const Residual& w, const VerifyParams& p, VerifyShared& sh, int t0, int t1, int mine0, int& turn) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bool any_gone = false;
     if (!w.q)
@@ -339,9 +351,13 @@ __device__ double row_sum(const Residual& w, const VerifyParams& p, VerifyShared
         double part[BATCH];
         batch_sums(w, t, t1, lane, p.V, p.vec, any_gone, part);
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) s += part[i];
+        for (int i = 0; i < BATCH; ++i) part[i] = warp_sum(part[i]);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            s += part[i];
+            if (lane == 0 && t + i < t1) sh.tile_sum[mine0 + t - t0 + i] = part[i];
+        }
     }
-    s = warp_sum(s);
     __syncthreads();   // the sums of the pass before have been read
     if (lane == 0) sh.warp_sum[warp] = s;
     __syncthreads();
@@ -358,49 +374,45 @@ __device__ double row_sum(const Residual& w, const VerifyParams& p, VerifyShared
     return total;
 }
 
-__global__ void __launch_bounds__(VT, 2) spec_verify_kernel(VerifyParams p) {
+__global__ void __launch_bounds__(VT, 2) spec_verify_kernel(const __grid_constant__ VerifyParams p) {
     __shared__ VerifyShared sh;
     const int rank = p.C > 1 ? (int)cluster_rank() : 0, b = blockIdx.x / p.C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, N = p.N, V = p.V;
     const float *P = p.target + (size_t)b * (N + 1) * V, *Q = p.draft ? p.draft + (size_t)b * N * V : nullptr;
     pdl_wait();
+    // every node's parent, token and uniform at once, then p and q of its token behind its parent
     const int L = p.n_nodes ? __ldg(p.n_nodes + b) : N;
-    if (tid == 0) {
-        sh.bad = L < 0 || L > N;
-        sh.next = V;
-        sh.last = -1;
-    }
-    __syncthreads();
-    if (tid < min(L, N)) {
+    bool wrong = L < 0 || L > N;
+    if (tid < N) {
         const int par = p.parent ? __ldg(p.parent + (size_t)b * N + tid) : tid - 1;
         const int x = __ldg(p.tokens + (size_t)b * N + tid);
-        if (par < -1 || par >= tid || x < 0 || x >= V) {
-            sh.bad = 1;
-        } else {
-            const size_t at = (size_t)(par + 1) * V + x;
-            sh.par[tid] = par;
-            sh.tok[tid] = x;
-            sh.p[tid] = (double)__ldg(P + at);
-            sh.q[tid] = Q ? (double)__ldg(Q + at) : 1.;
-            sh.u[tid] = (double)__ldg(p.u + (size_t)b * (N + 1) + tid);
+        const float u = __ldg(p.u + (size_t)b * (N + 1) + tid);
+        if (tid < L) {
+            if (par < -1 || par >= tid || x < 0 || x >= V) {
+                wrong = true;
+            } else {
+                const size_t at = (size_t)(par + 1) * V + x;
+                const float pv = __ldg(P + at), qv = Q ? __ldg(Q + at) : 1.f;
+                sh.par[tid] = par, sh.tok[tid] = x;
+                sh.p[tid] = (double)pv, sh.q[tid] = (double)qv, sh.u[tid] = (double)u;
+            }
         }
     }
     if (tid == TREE_MAX) sh.u[TREE_MAX] = (double)__ldg(p.u + (size_t)b * (N + 1) + N);
-    __syncthreads();
     int32_t* path = p.path + (size_t)b * N;
-    if (sh.bad) {   // the whole cluster sees the same
+    if (__syncthreads_or(wrong)) {   // the whole cluster sees the same
         if (rank == 0) {
             if (tid < N) path[tid] = -1;
             if (tid == 0) p.n_accept[b] = p.next[b] = -1;
         }
         return;
     }
-    // this warp's tiles
+    // this warp's tiles, and the place of its first one's sum
     const int tiles = (V + TILE - 1) / TILE, per = (tiles + p.C * VWARPS - 1) / (p.C * VWARPS);
-    const int t0 = min(tiles, (rank * VWARPS + warp) * per), t1 = min(tiles, t0 + per);
+    const int t0 = min(tiles, (rank * VWARPS + warp) * per), t1 = min(tiles, t0 + per), mine0 = warp * per;
     int cur = -1, taken = 0, turn = 0;
     double M = 1.;
-    bool summed = false;   // M is the sum of W, and the warps' parts of it are in shared memory
+    bool summed = false;   // M is the sum of W, and its parts are in shared memory
     Residual w{P, nullptr, 0., sh.gone, 0};
     for (int i = 0; i < L; ++i) {
         if (sh.par[i] != cur) continue;
@@ -418,7 +430,7 @@ __global__ void __launch_bounds__(VT, 2) spec_verify_kernel(VerifyParams p) {
         } else if (Q) {
             w.c += M;
             w.q = Q + (size_t)(cur + 1) * V;
-            M = row_sum(w, p, sh, rank, t0, t1, turn);
+            M = row_sum(w, p, sh, t0, t1, mine0, turn);
             summed = true;
         } else if (left > 0.) {
             __syncthreads();
@@ -428,76 +440,76 @@ __global__ void __launch_bounds__(VT, 2) spec_verify_kernel(VerifyParams p) {
             __syncthreads();
         }
     }
-    double total = summed ? M : row_sum(w, p, sh, rank, t0, t1, turn);
+    if (rank == 0) {
+        if (tid == 0) p.n_accept[b] = taken;
+        if (tid >= taken && tid < N) path[tid] = -1;
+    }
+    double total = summed ? M : row_sum(w, p, sh, t0, t1, mine0, turn);
     if (!(total > 0.)) {   // nothing is left (a draft that equals the target, rejected by rounding): the target itself
         w.q = nullptr;
         w.n_gone = 0;
-        total = row_sum(w, p, sh, rank, t0, t1, turn);
+        total = row_sum(w, p, sh, t0, t1, mine0, turn);
     }
-    // the warp whose tiles hold the border looks for it
+    // The warp whose tiles hold the border looks for it.  Every warp forms the borders between warps from the same sums
+    // in the same order, so exactly one warp finds itself: the last one, should rounding put the border behind all sums;
+    // the first one, should there be no border (rows that hold no mass, or none that is finite).
     const double want = sh.u[TREE_MAX] * total;
-    double before = 0.;
-    if (p.C > 1)
-        for (int r = 0; r < rank; ++r) before += ld_cluster(&sh.cta_sum[turn], r);
-    for (int i = 0; i < warp; ++i) before += sh.warp_sum[i];
-    const double mine = sh.warp_sum[warp];
-    if (mine > 0.) {
-        int found = V;
-        const bool border = before + mine > want;
-        for (int t = t0; t < t1 && found == V && border; t += BATCH) {
-            double part[BATCH];
-            batch_sums(w, t, t1, lane, V, p.vec, w.n_gone > 0, part);
+    const bool none = !(total > 0. && want == want);
+    double before = 0., after;
+    {
+        double base = 0., sum = 0.;
+        if (p.C > 1) {
+            for (int r = 0; r < rank; ++r) base += ld_cluster(&sh.cta_sum[turn], r);
+            cluster_arrive();   // waited for before the CTA leaves
+        }
+        for (int i = 0; i < warp; ++i) sum += sh.warp_sum[i];
+        before = base + sum, after = base + (sum + sh.warp_sum[warp]);
+    }
+    const bool first = rank == 0 && warp == 0, last = rank == p.C - 1 && warp == VWARPS - 1;
+    if (none ? first : (first || before <= want) && (last || want < after)) {
+        int found = -1;
+        for (int c = t0; c < t1 && found < 0; c += 32) {   // 32 tiles' sums at a time, in order
+            double s = c + lane < t1 ? sh.tile_sum[mine0 + c - t0 + lane] : 0.;
+            const bool some = s > 0.;
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                const double tile = warp_sum(part[i]);
-                if (found == V && tile > 0. && before + tile > want) {
-                    double at = before;
-                    for (int j = 0; j < TILE / 32 && found == V; ++j) {   // token by token, in order
-                        const int tok = (t + i) * TILE + 32 * j + lane;
-                        const double v = tok < V ? w.at(tok) : 0.;
-                        double s = v;
-#pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const double up = __shfl_up_sync(0xffffffffu, s, o);
-                            if (lane >= o) s += up;
-                        }
-                        const unsigned hit = __ballot_sync(0xffffffffu, v > 0. && at + s > want);
-                        if (hit) found = (t + i) * TILE + 32 * j + __ffs(hit) - 1;
-                        at += __shfl_sync(0xffffffffu, s, 31);
-                    }
-                }
-                before += tile;
+            for (int o = 1; o < 32; o <<= 1) {
+                const double up = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += up;
             }
+            unsigned hit = __ballot_sync(0xffffffffu, some && before + s > want);
+            while (hit && found < 0) {   // the first such tile; the next one should rounding leave it without a token
+                const int k = __ffs(hit) - 1, tile = c + k;
+                hit &= hit - 1;
+                double sum = before + (k > 0 ? __shfl_sync(0xffffffffu, s, k > 0 ? k - 1 : 0) : 0.);
+                double v[TILE / 32];
+#pragma unroll
+                for (int j = 0; j < TILE / 32; ++j) {
+                    const int tok = tile * TILE + 32 * j + lane;
+                    v[j] = tok < V ? w.at(tok) : 0.;
+                }
+#pragma unroll
+                for (int j = 0; j < TILE / 32; ++j) {   // token by token, in order
+                    double a = v[j];
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const double up = __shfl_up_sync(0xffffffffu, a, o);
+                        if (lane >= o) a += up;
+                    }
+                    const unsigned at = __ballot_sync(0xffffffffu, v[j] > 0. && sum + a > want);
+                    if (at && found < 0) found = tile * TILE + 32 * j + __ffs(at) - 1;
+                    sum += __shfl_sync(0xffffffffu, a, 31);
+                }
+            }
+            before += __shfl_sync(0xffffffffu, s, 31);
         }
-        if (lane == 0 && found < V) atomicMin(&sh.next, found);
-    }
-    __syncthreads();
-    int next = sh.next;
-    if (p.C > 1) {
-        if (tid == 0) sh.cta_next = next;
-        cluster_sync();
-        if (rank == 0 && tid < p.C) {
-            int o;
-            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(o) : "r"(mapa_shared(&sh.cta_next, tid)) : "memory");
-            atomicMin(&sh.next, o);
+        // rounding left the border behind the last sum: the last token up to here with any mass (anywhere, if none has)
+        for (int t = min(V, t1 * TILE) - 1; t >= 0 && found < 0; t -= 32) {
+            const unsigned hit = __ballot_sync(0xffffffffu, t >= lane && w.at(max(0, t - lane)) > 0.);
+            if (hit) found = t - __ffs(hit) + 1;
         }
-        cluster_sync();
-        next = sh.next;
+        if (lane == 0) p.next[b] = found < 0 ? V - 1 : found;
     }
-    if (rank != 0) return;
-    if (next == V && warp == 0) {   // rounding left the border behind the last sum: the last token with any mass
-        int last = -1;
-        for (int t = (V - 1) / 32 * 32; t >= 0 && last < 0; t -= 32) {
-            const unsigned hit = __ballot_sync(0xffffffffu, t + lane < V && w.at(t + lane) > 0.);
-            if (hit) last = t + 31 - __clz(hit);
-        }
-        next = last < 0 ? V - 1 : last;
-    }
-    if (tid == 0) {
-        p.next[b] = next;
-        p.n_accept[b] = taken;
-    }
-    if (tid >= taken && tid < N) path[tid] = -1;
+    if (p.C > 1) cluster_wait();
 }
 
 // CTAs of a row of V values: at most `most` values each, and smaller parts while the device is not full
@@ -552,6 +564,12 @@ focr_status focr_spec_verify(const float* target, const float* draft, int32_t V,
     const void* all[] = {target, draft, tokens, parent, n_nodes, u, n_accept, path, next_token};
     for (const void* x : all)
         if (misaligned(x, 4)) return report_error(FOCR_ERR_INVALID_ARG, "misaligned argument");
+    // the CTAs of a tree read while one of them already answers
+    const size_t rows = 4ull * B * N, row = 4ull * V;
+    const Span out[] = {{n_accept, 4ull * B}, {path, rows}, {next_token, 4ull * B}};
+    const Span in[] = {{target, row * B * (N + 1)}, {draft, row * B * N}, {tokens, rows}, {parent, rows}, {n_nodes, 4ull * B},
+                       {u, 4ull * B * (N + 1)}};
+    if (outputs_overlap(out, 3, in, 6)) return report_error(FOCR_ERR_INVALID_ARG, "an output overlaps another argument");
     VerifyParams p{target, draft, u, tokens, parent, n_nodes, n_accept, path, next_token, N, V,
                    row_cluster(B, V, VWARPS * TILE * BATCH, VWARPS * TILE),
                    V % 4 == 0 && !misaligned(target, 16) && !misaligned(draft, 16)};
