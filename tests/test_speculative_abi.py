@@ -143,3 +143,39 @@ def test_the_binding_refuses_cpu_tensors_and_wrong_shapes():
                  lambda: api.new_kv_cache(1, 1, 1, api.W_BF16, device="cpu")):
         with pytest.raises(api.FocrError):
             call()
+
+
+SMALL = dict(heads=1, cap=8)    # 1 KB of codes, 32 B of scales: the default addresses are apart
+
+
+@pytest.mark.parametrize("c,bad", [
+    (dict(ks=at(0) + 512), {}), (dict(v=at(0) + 1008), {}), (dict(vs=at(1) + 28), {}), ({}, dict(k=at(0))), ({}, dict(v=at(3) - 512)),
+    ({}, dict(count=at(1))), ({}, dict(start=at(0) + 1020)), ({}, dict(index=at(2))), ({}, dict(row0=at(3))),
+])
+def test_write_refuses_overlapping_buffers(c, bad):
+    assert write(cache(**SMALL, **c), **bad) == INVALID and "overlap" in api.focr_last_error()
+
+
+@pytest.mark.parametrize("args", [(at(4), at(0), at(6)), (at(4), at(5), at(3) - 16), (at(5) + 16, at(5), at(6)), (at(4), at(5), at(0) + 1008)])
+def test_read_refuses_overlapping_buffers(args):
+    c = cache(**SMALL)
+    assert api.lib().focr_kv_read(ctypes.byref(c), *args, None) == INVALID and "overlap" in api.focr_last_error()
+
+
+@pytest.mark.parametrize("bad", [
+    dict(out=at(4)), dict(out=at(5)), dict(out=at(0)), dict(out=at(6), parent=at(7)), dict(out=at(6), n_nodes=at(6) + 64),
+    dict(ref=dict(cap=32768), ws=at(8), ws_bytes=1 << 30), dict(ref=dict(cap=32768), ws=at(14), ws_bytes=1 << 30),
+])
+def test_tree_refuses_overlapping_buffers(bad):
+    assert tree(**bad) == INVALID and "overlap" in api.focr_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(qo=at(1)), dict(ko=at(1)), dict(gq=at(3)), dict(gk=at(11))])
+def test_rope_refuses_outputs_over_positions_and_weights(bad):
+    assert rope(**bad) == INVALID and "overlap" in api.focr_last_error()
+
+
+@pytest.mark.parametrize("bad", [dict(path=at(4)), dict(next=at(8)), dict(n_accept=at(9) + 12), dict(n_accept=at(7) + 16),
+                                 dict(path=at(0) + 144), dict(next=at(2)), dict(path=at(5)), dict(next=at(6))])
+def test_verify_refuses_overlapping_buffers(bad):
+    assert api.lib().focr_spec_verify(*dict(VERIFY, **bad).values(), None) == INVALID and "overlap" in api.focr_last_error()

@@ -89,6 +89,15 @@ def test_rope_of_zero_rows_with_norm():
     assert (got[0].cpu().numpy() == 0).all() and (got[1].cpu().numpy() == 0).all()
 
 
+@pytest.mark.parametrize("inter,rot", [(True, 126), (True, 64), (True, 2), (False, 64)])
+def test_rope_passes_infinities_behind_the_rotated_dims(inter, rot):
+    x = f32(np.random.default_rng(rot), 2, 3, 128)
+    x[:, :, 127], x[:, :, rot] = np.inf, -np.inf
+    got = api.focr_qk_norm_rope(dev(x), None, ints([1, 70000]), rot_dim=rot, interleaved=inter)[0].cpu().numpy()
+    np.testing.assert_array_equal(got[..., rot:], x[..., rot:])
+    assert np.isfinite(got[..., :rot]).all()
+
+
 # ---------------------------------------------------------------- cache writes and reads
 
 def np_cache(rng, B, heads, cap, int4):
@@ -340,6 +349,29 @@ def test_invalid_sequences_get_nan_and_spare_the_others():
     got = out.cpu().numpy()
     assert np.isnan(got[[0, 2, 3, 4]]).all() and np.isnan(got[1, :2]).all() and (got[1, 2] == 7.0).all()
     assert np.isfinite(got[5]).all()
+
+
+@pytest.mark.parametrize("cap", [300, 4300])      # one launch; ranges
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("what", [np.nan, np.inf])
+@pytest.mark.parametrize("which", [1, 3])         # key scales, value scales
+def test_a_scale_that_is_no_number_reaches_those_who_see_it_alone(cap, int4, what, which):
+    # a chain of three behind n = 200 tokens: token 72 is in the ring and seen by none, token 73 by the first node alone
+    rng = np.random.default_rng(48)
+    B, N, n = 3, 3, 200
+    q, k, v = (f32(rng, B, N, 2, 128) for _ in range(3))
+    ref, ring = np_cache(rng, B, 2, cap, int4), np_cache(rng, B, 2, 128, int4)
+    ring[which][0, :, 72] = ring[which][1, :, 73] = ref[which][2, 0, 10] = what
+    got = api.focr_rswa_tree(dev(q), dev(k), dev(v), dev_cache(ref), ints([cap] * B), dev_cache(ring), ints([n] * B)).cpu().numpy()
+    ref[which][2, 0, 10] = 0
+    ring[which][0, :, 72] = ring[which][1, :, 73] = 0
+    val = lambda c: (sp.values(c[0], c[1]), sp.values(c[2], c[3]))  # noqa: E731
+    want = sp.rswa_tree(q, k, v, val(ref), [cap] * B, val(ring), [n] * B)
+    ok = np.ones(got.shape, bool)
+    ok[1, 0] = ok[2, :, 0] = False
+    assert np.abs(got - want)[ok].max() <= TOL_TREE * max(np.abs(val(ref)[1]).max(), np.abs(val(ring)[1]).max(), np.abs(v).max())
+    if which == 3 or np.isnan(what):      # (an infinite key's score may be that of a masked one)
+        assert not np.isfinite(got[1, 0]).any() and not np.isfinite(got[2, :, 0]).any()
 
 
 # ---------------------------------------------------------------- probabilities

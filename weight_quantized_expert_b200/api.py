@@ -473,7 +473,7 @@ def _device_of(t, what: str) -> int:
 def _call(fn, dev: int, stream, *args):
     """fn(*args, stream) with device `dev` current; stream None: the current stream of `dev`."""
     st = _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-    if _torch.cuda.current_device() == dev:
+    if _torch._C._cuda_getDevice() == dev:
         status = fn(*args, st)
     else:
         with _torch.cuda.device(dev):

@@ -173,6 +173,12 @@ focr_status focr_kv_write(const focr_kv_cache* c, const float* k, int64_t ldk, c
     if (misaligned(k, 16) || misaligned(v, 16)) return report_error(FOCR_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
     if (misaligned(count, 4) || misaligned(start, 4) || misaligned(row0, 4) || misaligned(index, 4))
         return report_error(FOCR_ERR_INVALID_ARG, "misaligned row tables");
+    Span out[4];
+    cache_spans(c, out);
+    const size_t tab = 4ull * c->B;
+    const Span in[] = {{k, 4 * (size_t)((n_rows - 1) * ldk + w)}, {v, 4 * (size_t)((n_rows - 1) * ldv + w)}, {row0, tab},
+                       {count, tab}, {index, tab * n_max}, {start, tab}};
+    if (outputs_overlap(out, 4, in, 6)) return report_error(FOCR_ERR_INVALID_ARG, "the cache's buffers overlap one another or an input");
     p.k = k, p.v = v, p.row0 = row0, p.count = count, p.index = index, p.start = start;
     p.ldk = ldk, p.ldv = ldv, p.n_rows = n_rows, p.n_max = n_max, p.wrap = flags & FOCR_KV_WRAP;
     void* args[] = {&p};
@@ -192,7 +198,11 @@ focr_status focr_kv_read(const focr_kv_cache* c, const int32_t* len, float* k_ou
     if (misaligned(k_out, 16) || misaligned(v_out, 16) || misaligned(len, 4))
         return report_error(FOCR_ERR_INVALID_ARG, "misaligned outputs or lengths");
     const size_t bytes = 4ull * c->B * c->heads * c->cap * RD;
-    if (ranges_overlap(k_out, bytes, v_out, bytes)) return report_error(FOCR_ERR_INVALID_ARG, "k_out and v_out overlap");
+    const Span out[] = {{k_out, bytes}, {v_out, bytes}};
+    Span in[5] = {{}, {}, {}, {}, {len, 4ull * c->B}}, own[4];
+    cache_spans(c, own);
+    for (int i = 0; i < 4; ++i) in[i] = own[i];
+    if (outputs_overlap(out, 2, in, 5)) return report_error(FOCR_ERR_INVALID_ARG, "the outputs overlap one another or an input");
     p.len = len, p.k_out = k_out, p.v_out = v_out;
     void* args[] = {&p};
     const dim3 grid((c->cap + CROWS - 1) / CROWS, c->heads, c->B);

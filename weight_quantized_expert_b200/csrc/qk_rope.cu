@@ -86,6 +86,12 @@ __global__ void __launch_bounds__(32 * RWARPS, 3) qk_rope_kernel(const __grid_co
         if (HOW == 0) {
             x = make_float4(a.x * t0.x - a.y * t0.y, a.y * t0.x + a.x * t0.y, a.z * t0.z - a.w * t0.w, a.w * t0.z + a.z * t0.w);
             y = make_float4(b.x * t1.x - b.y * t1.y, b.y * t1.x + b.x * t1.y, b.z * t1.z - b.w * t1.w, b.w * t1.z + b.z * t1.w);
+            if (p.rot < RD) {   // the others pass as they are, infinities too
+                if (2 * l >= half) x.x = a.x, x.y = a.y;
+                if (2 * l + 1 >= half) x.z = a.z, x.w = a.w;
+                if (32 + 2 * l >= half) y.x = b.x, y.y = b.y;
+                if (33 + 2 * l >= half) y.z = b.z, y.w = b.w;
+            }
         } else if (HOW == 1) {
             x = make_float4(a.x * t0.x - b.x * t0.y, a.y * t0.z - b.y * t0.w, a.z * t1.x - b.z * t1.y, a.w * t1.z - b.w * t1.w);
             y = make_float4(b.x * t0.x + a.x * t0.y, b.y * t0.z + a.y * t0.w, b.z * t1.x + a.z * t1.y, b.w * t1.z + a.w * t1.w);
@@ -164,7 +170,10 @@ extern "C" focr_status focr_qk_norm_rope(const float* q, int64_t ldq, int32_t he
         bad = bad || (!(k_out == k && ldko == ldk) && rows_overlap(k_out, ldko, wk, k, ldk, wk, T)) ||
               rows_overlap(q_out, ldqo, wq, k, ldk, wk, T) || rows_overlap(k_out, ldko, wk, q, ldq, wq, T) ||
               rows_overlap(q_out, ldqo, wq, k_out, ldko, wk, T);
-    if (bad) return report_error(FOCR_ERR_INVALID_ARG, "outputs overlap other rows");
+    const Span out[] = {{q_out, 4 * (size_t)((T - 1) * ldqo + wq)}}, out_k[] = {{k_out, 4 * (size_t)((T - 1) * ldko + wk)}};
+    const Span in[] = {{pos, 4ull * T}, {gamma_q, 4ull * RD}, {gamma_k, 4ull * RD}};
+    if (bad || outputs_overlap(out, 1, in, 3) || outputs_overlap(out_k, 1, in, 3))
+        return report_error(FOCR_ERR_INVALID_ARG, "outputs overlap other rows, the positions or the weights");
     RopeParams p;
     p.q = q, p.k = k, p.q_out = q_out, p.k_out = k_out, p.gamma_q = gamma_q, p.gamma_k = gamma_k, p.pos = pos;
     p.ldq = ldq, p.ldk = ldk, p.ldqo = ldqo, p.ldko = ldko;

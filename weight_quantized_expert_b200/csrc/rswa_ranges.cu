@@ -247,6 +247,8 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
     }
     for (; blk < end; blk += WARPS) {
         cp_wait<1>();
+        check_scale(stage + St::KS, stage + St::VS, lane);
+        check_scale(stage + St::KS, stage + St::VS, lane + 32);
         __syncwarp();
         // scores, without the column's step: T[j][..] for keys 8 j + 2 c, + 1
         float T[8][W16 ? 4 : 2], vs[8][2];

@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
     }
     for (; blk < nblk; blk += stride) {
         cp_wait<1>();
+        check_scale(stage + St::KS, stage + St::VS, 32 * half + lane);
         __syncwarp();
         // scores of the warp's own keys, without the column's step: T[j][..] for keys 8 j + 2 c, + 1 of its 32
         float T[4][VALS], vs[4][2];
@@ -535,14 +536,19 @@ extern "C" focr_status focr_rswa_tree(const float* q, const float* k_new, const 
         if (misaligned(ptr, 16)) return report_error(FOCR_ERR_INVALID_ARG, "float buffers must be 16-byte aligned");
     if (misaligned(ref_len, 4) || misaligned(n_gen, 4) || misaligned(parent, 4) || misaligned(n_nodes, 4))
         return report_error(FOCR_ERR_INVALID_ARG, "misaligned lengths or tree");
-    const size_t qb = 4ull * B * N * heads_q * RD, kb = 4ull * B * N * ref->heads * RD;
-    if (ranges_overlap(out, qb, q, qb) || ranges_overlap(out, qb, k_new, kb) || ranges_overlap(out, qb, v_new, kb))
-        return report_error(FOCR_ERR_INVALID_ARG, "out overlaps an input");
     p.q = q, p.k_new = k_new, p.v_new = v_new, p.ref_len = ref_len, p.n_gen = n_gen, p.parent = parent, p.n_nodes = n_nodes;
     const TreePlan pl = tree_plan(B, N, heads_q, ref->heads, ref->cap);
     const size_t need = focr_rswa_tree_workspace_bytes(B, N, heads_q, ref->heads, ref->cap);
     if (need && (!workspace || misaligned(workspace, 256) || ws_bytes < need))
         return reportf(FOCR_ERR_INVALID_ARG, "workspace of %zu bytes (256-byte aligned) is needed, got %zu", need, ws_bytes);
+    const size_t qb = 4ull * B * N * heads_q * RD, kb = 4ull * B * N * ref->heads * RD, tab = 4ull * B;
+    const Span outs[] = {{out, qb}, {need ? workspace : nullptr, need}};
+    Span a[4], b[4];
+    cache_spans(ref, a);
+    cache_spans(ring, b);
+    const Span in[] = {{q, qb}, {k_new, kb}, {v_new, kb}, {ref_len, tab}, {n_gen, tab}, {parent, tab * N}, {n_nodes, tab},
+                       a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    if (outputs_overlap(outs, 2, in, 15)) return report_error(FOCR_ERR_INVALID_ARG, "out or workspace overlaps another argument");
     p.out = out, p.B = B, p.N = N, p.hq = heads_q, p.hk = ref->heads, p.G = G;
     p.part = reinterpret_cast<float*>(workspace);
     const bool wide = N * G > 8, int4 = ref->type == FOCR_W_INT4;

@@ -54,6 +54,13 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
+// A value scale that is no number becomes the key scale's, so that it reaches those who see the key and nobody else
+// (0 times NaN would reach all).  By the lane that copied key r's scales.
+__device__ __forceinline__ void check_scale(uint8_t* ks, uint8_t* vs, int r) {
+    float* v = reinterpret_cast<float*>(vs) + r;
+    if (!(fabsf(*v) < INFINITY)) *v = 0.f, reinterpret_cast<float*>(ks)[r] = __int_as_float(0x7fc00000);
+}
+
 // 65536 d2 + 256 d1 + d0 of three integer accumulators that started at MAGIC_BITS (so they read as MAGIC + sum), as two
 // parts: lower() + upper().  The products with the constants are exact (multiples of 256 and 65536 below 2^24 of them),
 // the sums round once each.
