@@ -18,8 +18,8 @@ namespace focr {
 namespace {
 
 constexpr int RD = TREE_DIM, RW = TREE_RING;
-constexpr int WARPS = 4, PT = 32 * WARPS, MINE = (COLS + WARPS - 1) / WARPS;   // MINE: columns a warp prepares
-constexpr int JT = 128;                         // threads of the joining kernel
+constexpr int WARPS = 4, PT = 32 * WARPS, TPC = PT / COLS;   // TPC: threads that prepare a column
+constexpr int JT = 128, JCOLS = 4;              // threads and columns of a CTA of the joining kernel
 
 // A partial result: 16 columns' maxima, sums and unnormalised outputs.
 constexpr int PART_L = COLS, PART_O = 2 * COLS, PART_FLOATS = 2 * COLS + COLS * RD;
@@ -39,14 +39,16 @@ struct Shared {
     int scan[WARPS + 4];
 };
 
-// Blocks of a sequence (one at least: the drafted keys need a CTA too).
-__device__ __forceinline__ int sequence_blocks(const TreeParams& p, int b) {
+// A unit's length in the row: what it costs to begin it, in blocks, and its blocks (one at least: the drafted keys need a
+// CTA too).
+constexpr int BEGIN = 6;
+__device__ __forceinline__ int unit_length(const TreeParams& p, int b) {
     const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b);
-    if (R < 0 || R > p.ref.cap || n < 0) return 1;
-    return max(1, (R + BLK - 1) / BLK + (min(n, RW) + BLK - 1) / BLK);
+    if (R < 0 || R > p.ref.cap || n < 0) return BEGIN + 1;
+    return BEGIN + max(1, (R + BLK - 1) / BLK + (min(n, RW) + BLK - 1) / BLK);
 }
-struct Place {   // a block in the row of all units' blocks
-    int b, unit, block;   // sequence, unit of the sequence, block of the unit
+struct Place {   // in the row of all units
+    int b, unit, at;   // sequence, unit of the sequence, place in the unit
 };
 // Sums over all threads of the CTA; the threads' inclusive prefix in `mine`.
 template <int NW>
@@ -68,18 +70,18 @@ __device__ __forceinline__ int cta_scan(int& mine, int* scan) {
     }
     return total;
 }
-// All blocks of the call.
-__device__ int all_blocks(const TreeParams& p, int* scan) {
+// The row's length.
+__device__ int row_length(const TreeParams& p, int* scan) {
     int mine = 0;
-    for (int b = threadIdx.x; b < p.B; b += PT) mine += sequence_blocks(p, b);
+    for (int b = threadIdx.x; b < p.B; b += PT) mine += unit_length(p, b);
     return cta_scan<WARPS>(mine, scan) * p.hk * p.groups;
 }
-// Where block `at` of the row is.
-__device__ Place find_block(const TreeParams& p, int at, int* scan) {
+// What is at place `at` of the row.
+__device__ Place find_place(const TreeParams& p, int at, int* scan) {
     const int per = p.hk * p.groups;
     int before = 0;
     for (int b0 = 0; b0 < p.B; b0 += PT) {
-        const int b = b0 + threadIdx.x, own = b < p.B ? sequence_blocks(p, b) : 0;
+        const int b = b0 + threadIdx.x, own = b < p.B ? unit_length(p, b) : 0;
         int sum = own;
         const int total = cta_scan<WARPS>(sum, scan);
         if ((int64_t)(before + total) * per > at) {
@@ -137,38 +139,49 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
     uint8_t* stage = smem + warp * St::BYTES;
     const uint32_t st = smem_u32(stage);
     pdl_wait();
-    const int all = all_blocks(p, sh.scan), per = (all + gridDim.x - 1) / gridDim.x;
+    pdl_launch_dependents();
+    const int all = row_length(p, sh.scan), per = (all + gridDim.x - 1) / gridDim.x;
     const int from = (int)min((int64_t)blockIdx.x * per, (int64_t)all);
-    int left = min(per, all - from);   // blocks of this CTA's range
+    int left = min(per, all - from);   // of this CTA's range
     if (left == 0) return;
-    Place at = find_block(p, from, sh.scan);
+    Place at = find_place(p, from, sh.scan);
+    int R = 0, n = 0, L = 0, whole = 0, seq = -1;   // of sequence seq
+    bool bad = false;
     while (left > 0) {
     const int b = at.b, h = at.unit / p.groups, col0 = at.unit % p.groups * COLS, cols = min(COLS, p.N * p.G - col0);
-    // ---- everything that depends on nothing, at once: lengths, parents, queries
-    const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b), L = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
-    const int par = tid < p.N && p.parent ? __ldg(p.parent + (size_t)b * p.N + tid) : tid - 1;
-    float4 q[MINE];
-#pragma unroll
-    for (int i = 0; i < MINE; ++i) {
-        const int col = warp + i * WARPS, node = (col0 + col) / p.G, x = h * p.G + (col0 + col) % p.G;
-        q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (col < cols) q[i] = __ldg(reinterpret_cast<const float4*>(p.q + (((size_t)b * p.N + node) * p.hq + x) * RD) + lane);
+    // ---- the query, and what belongs to the sequence if it is another one: lengths and lines of the tree
+    const int col = tid / TPC, j = tid % TPC, node = (col0 + col) / p.G;
+    RowPart<TPC> q;
+    q.zero();
+    if (col < cols) q.load(p.q + (((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD, j);
+    if (b != seq) {
+        seq = b;
+        const int par = tid < p.N && p.parent ? __ldg(p.parent + (size_t)b * p.N + tid) : tid - 1;
+        R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b), L = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
+        whole = unit_length(p, b);
+        const bool lengths = R >= 0 && R <= p.ref.cap && n >= 0 && L >= 0 && L <= p.N;
+        if (tid < p.N) sh.par[tid] = par;
+        bad = __syncthreads_or(!lengths || (tid < L && (par < -1 || par >= tid)));
+        if (tid < L && !bad) {
+            unsigned long long line = 0;
+            for (int i = tid; i >= 0; i = sh.par[i]) line |= 1ull << i;
+            sh.line[tid] = line;
+        }
+        __syncthreads();
     }
-    const bool lengths = R >= 0 && R <= p.ref.cap && n >= 0 && L >= 0 && L <= p.N;
-    if (tid < p.N) sh.par[tid] = par;
-    const bool bad = __syncthreads_or(!lengths || (tid < L && (par < -1 || par >= tid)));
     // ---- this CTA's blocks of the unit; its first ones are on their way while the query is prepared
     const int nref = bad ? 0 : (R + BLK - 1) / BLK, nring = bad ? 0 : (min(n, RW) + BLK - 1) / BLK, nblk = nref + nring;
-    const int whole = sequence_blocks(p, b);   // of the unit, as the ranges count it
-    const int first = at.block, last = min(whole, first + min(left, whole));
-    const bool head = first == 0, complete = head && last == whole;
+    const int take = min(left, whole - at.at);
+    const int first = max(0, at.at - BEGIN), last = max(0, at.at + take - BEGIN);
+    if (last > first) {
+    const bool head = first == 0, complete = head && last == whole - BEGIN;
     const bool dead = bad || col0 / p.G >= L;   // nothing to compute
     if (bad && head) {
         const int live = L < 0 || L > p.N ? p.N : L;
-        for (int col = 0; col < cols; ++col) {
-            const int node = (col0 + col) / p.G;
-            if (node < live && tid < RD)
-                p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = __int_as_float(0x7fc00000);
+        for (int c = 0; c < cols; ++c) {
+            const int x = (col0 + c) / p.G;
+            if (x < live && tid < RD)
+                p.out[(((size_t)b * p.N + x) * p.hq + h * p.G + (col0 + c) % p.G) * RD + tid] = __int_as_float(0x7fc00000);
         }
     }
     if (!dead) {
@@ -197,37 +210,22 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
     if (blk < end) load_codes<INT4>(st + St::V, cur.v, cur.rows, true, lane);
     cp_commit();
 
-    // ---- lines of the tree
-    if (tid < L) {
-        unsigned long long line = 0;
-        for (int j = tid; j >= 0; j = sh.par[j]) line |= 1ull << j;
-        sh.line[tid] = line;
-    }
-    __syncthreads();
-    // ---- query digits, per-column constants, and the drafted keys' part (the CTA that has the unit's first block has them):
-    // four keys at a time, the first four of all columns loaded at once
-    unsigned long long line[MINE];
-    float4 kk[MINE][4], vv[MINE][4];
-#pragma unroll
-    for (int i = 0; i < MINE; ++i) {
-        const int col = warp + i * WARPS, node = (col0 + col) / p.G;
+    // ---- query digits, per-column constants, and the drafted keys' part (the CTA that has the unit's first block has them)
+    {
         const bool live = col < cols && node < L;
-        if (!live) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        line[i] = live && head ? sh.line[node] : 0ull;
-        unsigned long long rest = line[i];
-        draft_load(p, b, h, lane, rest, kk[i], vv[i]);
-        if (lane == 0 && col < COLS) sh.ages[col] = live ? min(n, RW - __popcll(sh.line[node])) : 0;
-    }
+        if (!live) q.zero();
+        const unsigned long long line = live && head ? sh.line[node] : 0ull;
+        DraftPart<TPC> d;
+        d.load(p, b, h, j, line);
+        const float a = query_digits<INT4>(q, col, j, sh.qf);
+        if (j == 0) {
+            sh.ages[col] = live ? min(n, RW - __popcll(sh.line[node])) : 0;
+            sh.step[col] = a / Q_TOP * (SCORE_SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
+        }
+        d.attend(p, b, h, j, q, line);
 #pragma unroll
-    for (int i = 0; i < MINE; ++i) {
-        const int col = warp + i * WARPS;
-        if (col >= COLS) break;
-        const float4 x = q[i];
-        const float a = query_digits<INT4>(x, col, lane, sh.qf);
-        if (lane == 0) sh.step[col] = a / Q_TOP * (SCORE_SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
-        const DraftPart a4 = draft_attend(p, b, h, lane, x, line[i], kk[i], vv[i]);
-        reinterpret_cast<float4*>(sh.part[col])[lane] = a4.o;
-        if (lane == 0) sh.part_m[col] = a4.m, sh.part_l[col] = a4.l;
+        for (int i = 0; i < q.N; ++i) reinterpret_cast<float4*>(sh.part[col])[j + TPC * i] = d.o.x[i];
+        if (j == 0) sh.part_m[col] = d.m, sh.part_l[col] = d.l;
     }
     __syncthreads();
 
@@ -500,48 +498,60 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
         }
     }
     }
+    }
     // ---- the range's next unit
-    left -= last - first;
-    at.block = 0;
+    left -= take;
+    at.at = 0;
     if (++at.unit == p.hk * p.groups) at.unit = 0, ++at.b;
     __syncthreads();
     }
 }
 
-// Joins the partial results of the units that the ranges' cuts divide.
+// Joins the partial results of the units that the ranges' cuts divide, JCOLS columns a CTA.  Everything but the partial
+// results themselves was there before the kernel in front of this one began, so it is read ahead of the wait.
 __global__ void __launch_bounds__(JT) rswa_ranges_join_kernel(const __grid_constant__ TreeParams p, int ctas) {
     __shared__ int scan[JT / 32 + 4];
     const int tid = threadIdx.x, per_b = p.hk * p.groups, b = blockIdx.x / per_b, unit = blockIdx.x % per_b;
-    pdl_wait();
-    // the unit's blocks in the row of all blocks, and the CTAs that had them
     int all = 0, before = 0;
     for (int i = tid; i < p.B; i += JT) {
-        const int own = sequence_blocks(p, i);
+        const int own = unit_length(p, i);
         all += own;
         if (i < b) before += own;
     }
-    all = cta_scan<JT / 32>(all, scan) * per_b;
-    before = cta_scan<JT / 32>(before, scan);
-    const int own = sequence_blocks(p, b), per = (all + ctas - 1) / ctas;
-    const int64_t from = (int64_t)before * per_b + (int64_t)unit * own;
-    const int c0 = (int)(from / per), c1 = (int)((from + own - 1) / per);
     const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b), L = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
     const int par = tid < p.N && p.parent ? __ldg(p.parent + (size_t)b * p.N + tid) : tid - 1;
+    // the unit's blocks in the row, and the CTAs that had them
+    const int own = unit_length(p, b);
+    all = cta_scan<JT / 32>(all, scan) * per_b;
+    before = cta_scan<JT / 32>(before, scan);
+    const int per = (all + ctas - 1) / ctas;
+    const int64_t from = (int64_t)before * per_b + (int64_t)unit * own;
+    const int c0 = (int)((from + BEGIN) / per), c1 = (int)((from + own - 1) / per);
     const bool bad = __syncthreads_or(R < 0 || R > p.ref.cap || n < 0 || L < 0 || L > p.N || (tid < L && (par < -1 || par >= tid)));
+    pdl_wait();
     if (bad || c0 == c1) return;
-    const int h = unit / p.groups, col0 = unit % p.groups * COLS, cols = min(COLS, p.N * p.G - col0);
-    for (int col = blockIdx.y; col < cols; col += gridDim.y) {
-        const int node = (col0 + col) / p.G;
-        if (node >= L) return;
-        float M = NONE, l = 0.f, o = 0.f;
-        for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(p.part + ((size_t)c * 2 + (c == c0)) * PART_FLOATS + col));
-        for (int c = c0; c <= c1; ++c) {
-            const float* part = p.part + ((size_t)c * 2 + (c == c0)) * PART_FLOATS;
-            const float f = ex2(__ldcg(part + col) - M);
-            l = fmaf(f, __ldcg(part + PART_L + col), l);
-            o = fmaf(f, __ldcg(part + PART_O + col * RD + tid), o);
+    const int h = unit / p.groups, col0 = unit % p.groups * COLS, first = blockIdx.y * JCOLS;
+    float M[JCOLS], l[JCOLS], o[JCOLS];
+#pragma unroll
+    for (int j = 0; j < JCOLS; ++j) M[j] = NONE, l[j] = o[j] = 0.f;
+#pragma unroll 2
+    for (int c = c0; c <= c1; ++c) {
+        const float* part = p.part + ((size_t)c * 2 + (c == c0)) * PART_FLOATS;
+        float m[JCOLS], lp[JCOLS], op[JCOLS];   // (columns behind the unit's last hold anything, and go nowhere)
+#pragma unroll
+        for (int j = 0; j < JCOLS; ++j)
+            m[j] = __ldcg(part + first + j), lp[j] = __ldcg(part + PART_L + first + j), op[j] = __ldcg(part + PART_O + (first + j) * RD + tid);
+#pragma unroll
+        for (int j = 0; j < JCOLS; ++j) {
+            const float mn = fmaxf(M[j], m[j]), f = ex2(M[j] - mn), g = ex2(m[j] - mn);
+            M[j] = mn, l[j] = fmaf(g, lp[j], f * l[j]), o[j] = fmaf(g, op[j], f * o[j]);
         }
-        p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = o / l;
+    }
+#pragma unroll
+    for (int j = 0; j < JCOLS; ++j) {
+        const int col = col0 + first + j, node = col / p.G;
+        if (first + j < COLS && col < p.N * p.G && node < L)
+            p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + col % p.G) * RD + tid] = o[j] / l[j];
     }
 }
 
@@ -559,7 +569,7 @@ cudaError_t launch_as(TreeParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     void* more[] = {&p, &ctas};
     const int cols = p.N * p.G < COLS ? p.N * p.G : COLS;
-    return launch_kernel((const void*)rswa_ranges_join_kernel, dim3((unsigned)p.B * p.hk * p.groups, cols < 4 ? cols : 4), dim3(JT), 0, 1,
+    return launch_kernel((const void*)rswa_ranges_join_kernel, dim3((unsigned)p.B * p.hk * p.groups, (cols + JCOLS - 1) / JCOLS), dim3(JT), 0, 1,
                          more, st);
 }
 

@@ -93,7 +93,7 @@ template <bool INT4, bool W16>
 __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant__ TreeParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     using St = Stage<INT4>;
-    constexpr int MINE = COLS / WARPS;   // columns a warp prepares
+    constexpr int TPC = PT / COLS;   // threads that prepare a column
     Shared& sh = *reinterpret_cast<Shared*>(smem + PAIRS * St::BYTES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, c = lane & 3;
     const int rank = p.S > 1 ? (int)cluster_rank() : 0;
@@ -106,13 +106,10 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
     // ---- everything that depends on nothing, at once: lengths, parents, queries
     const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b), L = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
     const int par = tid < p.N && p.parent ? __ldg(p.parent + (size_t)b * p.N + tid) : tid - 1;
-    float4 q[MINE];
-#pragma unroll
-    for (int i = 0; i < MINE; ++i) {
-        const int col = warp + i * WARPS, node = (col0 + col) / p.G, x = h * p.G + (col0 + col) % p.G;
-        q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (col < cols) q[i] = __ldg(reinterpret_cast<const float4*>(p.q + (((size_t)b * p.N + node) * p.hq + x) * RD) + lane);
-    }
+    const int col = tid / TPC, j = tid % TPC, node = (col0 + col) / p.G;
+    RowPart<TPC> q;
+    q.zero();
+    if (col < cols) q.load(p.q + (((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD, j);
     const bool lengths = R >= 0 && R <= p.ref.cap && n >= 0 && L >= 0 && L <= p.N;
     if (tid < p.N) sh.par[tid] = par;
     const bool bad = __syncthreads_or(!lengths || (tid < L && (par < -1 || par >= tid)));
@@ -120,10 +117,10 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
     const int nref = bad ? 0 : (R + BLK - 1) / BLK, nring = bad ? 0 : (min(n, RW) + BLK - 1) / BLK, nblk = nref + nring;
     if (bad) {
         const int live = L < 0 || L > p.N ? p.N : L;
-        for (int col = rank; col < cols; col += p.S) {
-            const int node = (col0 + col) / p.G;
-            if (node < live && tid < RD)
-                p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + tid] = __int_as_float(0x7fc00000);
+        for (int c = rank; c < cols; c += p.S) {
+            const int x = (col0 + c) / p.G;
+            if (x < live && tid < RD)
+                p.out[(((size_t)b * p.N + x) * p.hq + h * p.G + (col0 + c) % p.G) * RD + tid] = __int_as_float(0x7fc00000);
         }
         return;
     }
@@ -158,29 +155,22 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         sh.line[tid] = line;
     }
     __syncthreads();
-    // ---- query digits, per-column constants, and the drafted keys' part (a CTA of the cluster takes every S-th column's):
-    // four keys at a time, the first four of all columns loaded at once
-    unsigned long long line[MINE];
-    float4 kk[MINE][4], vv[MINE][4];
-#pragma unroll
-    for (int i = 0; i < MINE; ++i) {
-        const int col = warp + i * WARPS, node = (col0 + col) / p.G;
+    // ---- query digits, per-column constants, and the drafted keys' part (a CTA of the cluster takes every S-th column's)
+    {
         const bool live = col < cols && node < L;
-        if (!live) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        line[i] = live && col % p.S == rank ? sh.line[node] : 0ull;
-        unsigned long long rest = line[i];
-        draft_load(p, b, h, lane, rest, kk[i], vv[i]);
-        if (lane == 0) sh.ages[col] = live ? min(n, RW - __popcll(sh.line[node])) : 0;
-    }
+        if (!live) q.zero();
+        const unsigned long long line = live && col % p.S == rank ? sh.line[node] : 0ull;
+        DraftPart<TPC> d;
+        d.load(p, b, h, j, line);
+        const float a = query_digits<INT4>(q, col, j, sh.qf);
+        if (j == 0) {
+            sh.ages[col] = live ? min(n, RW - __popcll(sh.line[node])) : 0;
+            sh.step[col] = a / Q_TOP * (SCORE_SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
+        }
+        d.attend(p, b, h, j, q, line);
 #pragma unroll
-    for (int i = 0; i < MINE; ++i) {
-        const int col = warp + i * WARPS;
-        const float4 x = q[i];
-        const float a = query_digits<INT4>(x, col, lane, sh.qf);
-        if (lane == 0) sh.step[col] = a / Q_TOP * (SCORE_SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
-        const DraftPart a4 = draft_attend(p, b, h, lane, x, line[i], kk[i], vv[i]);
-        reinterpret_cast<float4*>(sh.part[col])[lane] = a4.o;
-        if (lane == 0) sh.part_m[col] = a4.m, sh.part_l[col] = a4.l;
+        for (int i = 0; i < q.N; ++i) reinterpret_cast<float4*>(sh.part[col])[j + TPC * i] = d.o.x[i];
+        if (j == 0) sh.part_m[col] = d.m, sh.part_l[col] = d.l;
     }
     __syncthreads();
 

@@ -109,90 +109,118 @@ __device__ __forceinline__ int v_off(int r, int j) {
     return INT4 ? (r >> 1) * 128 + ((((r & 1) << 2 | j) ^ x) << 4) : r * 128 + ((j ^ x) << 4);
 }
 
-// Writes a query row (four dims a lane) as digits of column `col` into the A fragments qf[k-step * 3 + digit][lane], and
-// returns the row's largest magnitude.
-template <bool INT4>
-__device__ __forceinline__ float query_digits(float4 x, int col, int lane, uint4 (*qf)[32]) {
-    float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+// Before the blocks all columns of a unit are worked on at once, by TPC neighbouring threads each: thread j of a column has
+// the 16-byte chunks j, j + TPC, ... of its rows.  (One column a warp, several in turn: 5 us a unit instead of 2.)
+template <int TPC>
+struct RowPart {
+    static constexpr int N = TREE_DIM / 4 / TPC;
+    float4 x[N];
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    a = fmaxf(a, TINY);
+        for (int i = 0; i < N; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ void load(const float* row, int j) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = __ldg(reinterpret_cast<const float4*>(row) + j + TPC * i);
+    }
+};
+
+// Writes a query row as digits of column `col` into the A fragments qf[k-step * 3 + digit][lane], and returns the row's
+// largest magnitude.
+template <bool INT4, int TPC>
+__device__ __forceinline__ float query_digits(const RowPart<TPC>& q, int col, int j, uint4 (*qf)[32]) {
+    float a = TINY;
+#pragma unroll
+    for (int i = 0; i < q.N; ++i)
+        a = fmaxf(a, fmaxf(fmaxf(fabsf(q.x[i].x), fabsf(q.x[i].y)), fmaxf(fabsf(q.x[i].z), fabsf(q.x[i].w))));
+#pragma unroll
+    for (int o = TPC / 2; o >= 1; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     const float inv = Q_TOP / a;
-    const int f[4] = {__float2int_rn(x.x * inv), __float2int_rn(x.y * inv), __float2int_rn(x.z * inv), __float2int_rn(x.w * inv)};
     const int tl = (col & 7) * 4, hi = col >> 3;
 #pragma unroll
-    for (int d = 0; d < 3; ++d) {
-        const uint32_t v0 = (f[0] >> 8 * d) & 255, v1 = (f[1] >> 8 * d) & 255, v2 = (f[2] >> 8 * d) & 255, v3 = (f[3] >> 8 * d) & 255;
-        if (INT4) {   // dims 32 c + 8 s + 2 i in the first word of a k-step, + 1 in the second
-            const int s = (lane >> 1) & 3, cc = lane >> 3;
-            uint16_t* w = reinterpret_cast<uint16_t*>(&qf[s * 3 + d][tl + cc]);
-            w[2 * hi + (lane & 1)] = (uint16_t)(v0 | v2 << 8);
-            w[2 * (2 + hi) + (lane & 1)] = (uint16_t)(v1 | v3 << 8);
-        } else {      // dims 64 (s / 2) + 16 c + 8 (s % 2) + i, + 4 in the second
-            const int s = 2 * (lane >> 4) + ((lane >> 1) & 1), cc = (lane >> 2) & 3;
-            reinterpret_cast<uint32_t*>(&qf[s * 3 + d][tl + cc])[2 * (lane & 1) + hi] = v0 | v1 << 8 | v2 << 16 | v3 << 24;
+    for (int i = 0; i < q.N; ++i) {
+        const float4 x = q.x[i];
+        const int ch = j + TPC * i;
+        const int f[4] = {__float2int_rn(x.x * inv), __float2int_rn(x.y * inv), __float2int_rn(x.z * inv), __float2int_rn(x.w * inv)};
+#pragma unroll
+        for (int d = 0; d < 3; ++d) {
+            const uint32_t v0 = (f[0] >> 8 * d) & 255, v1 = (f[1] >> 8 * d) & 255, v2 = (f[2] >> 8 * d) & 255, v3 = (f[3] >> 8 * d) & 255;
+            if (INT4) {   // dims 32 c + 8 s + 2 i in the first word of a k-step, + 1 in the second
+                const int s = (ch >> 1) & 3, cc = ch >> 3;
+                uint16_t* w = reinterpret_cast<uint16_t*>(&qf[s * 3 + d][tl + cc]);
+                w[2 * hi + (ch & 1)] = (uint16_t)(v0 | v2 << 8);
+                w[2 * (2 + hi) + (ch & 1)] = (uint16_t)(v1 | v3 << 8);
+            } else {      // dims 64 (s / 2) + 16 c + 8 (s % 2) + i, + 4 in the second
+                const int s = 2 * (ch >> 4) + ((ch >> 1) & 1), cc = (ch >> 2) & 3;
+                reinterpret_cast<uint32_t*>(&qf[s * 3 + d][tl + cc])[2 * (ch & 1) + hi] = v0 | v1 << 8 | v2 << 16 | v3 << 24;
+            }
         }
     }
     return a;
 }
 
-// Four drafted rows of a line (`rest`: bits of its nodes, the four lowest are taken), four dims a lane.
-__device__ __forceinline__ void draft_load(const TreeParams& p, int b, int h, int lane, unsigned long long& rest, float4 (&k4)[4],
-                                           float4 (&v4)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        k4[j] = v4[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (rest) {
-            const size_t r = (((size_t)b * p.N + __ffsll(rest) - 1) * p.hk + h) * (TREE_DIM / 4) + lane;
-            k4[j] = __ldg(reinterpret_cast<const float4*>(p.k_new) + r);
-            v4[j] = __ldg(reinterpret_cast<const float4*>(p.v_new) + r);
-        }
-        rest &= rest - 1;
-    }
-}
-// Attention of one query over its line's drafted keys, fp32, by a warp; k4, v4 hold the line's first four rows.
+// Attention of one query over its line's drafted keys (`line`: bits of its nodes), fp32, four keys at a time.  load()
+// starts the first four rows' loads; attend() is called by whole warps.
+template <int TPC>
 struct DraftPart {
+    RowPart<TPC> k[4], v[4], o;
     float m, l;
-    float4 o;
-};
-__device__ __forceinline__ DraftPart draft_attend(const TreeParams& p, int b, int h, int lane, float4 q, unsigned long long line,
-                                                  float4 (&k4)[4], float4 (&v4)[4]) {
-    DraftPart a{NONE, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    const float k2 = SCORE_SCALE * LOG2E;
-    q = make_float4(q.x * k2, q.y * k2, q.z * k2, q.w * k2);
-    for (bool more = line != 0; more;) {
-        float sc[4];
+    __device__ __forceinline__ void load(const TreeParams& p, int b, int h, int j, unsigned long long line) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sc[j] = q.x * k4[j].x + q.y * k4[j].y + q.z * k4[j].z + q.w * k4[j].w;
-#pragma unroll
-        for (int e = 16; e >= 1; e >>= 1)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sc[j] += __shfl_xor_sync(0xffffffffu, sc[j], e);
-        float mn = a.m;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (!line) sc[j] = -INFINITY;
+        for (int n = 0; n < 4; ++n) {
+            if (line) {
+                const size_t r = (((size_t)b * p.N + __ffsll(line) - 1) * p.hk + h) * TREE_DIM;
+                k[n].load(p.k_new + r, j), v[n].load(p.v_new + r, j);
+            } else {
+                k[n].zero(), v[n].zero();
+            }
             line &= line - 1;
-            mn = fmaxf(mn, sc[j]);
-        }
-        const float al = ex2(a.m - mn);
-        a.l *= al, a.o.x *= al, a.o.y *= al, a.o.z *= al, a.o.w *= al;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float w = ex2(sc[j] - mn);
-            a.l += w;
-            a.o.x = fmaf(w, v4[j].x, a.o.x), a.o.y = fmaf(w, v4[j].y, a.o.y);
-            a.o.z = fmaf(w, v4[j].z, a.o.z), a.o.w = fmaf(w, v4[j].w, a.o.w);
-        }
-        a.m = mn;
-        more = line != 0;
-        if (more) {
-            unsigned long long rest = line;
-            draft_load(p, b, h, lane, rest, k4, v4);
         }
     }
-    return a;
-}
+    __device__ __forceinline__ void attend(const TreeParams& p, int b, int h, int j, const RowPart<TPC>& q, unsigned long long line) {
+        constexpr float k2 = SCORE_SCALE * LOG2E;
+        m = NONE, l = 0.f;
+        o.zero();
+        while (__any_sync(0xffffffffu, line != 0)) {
+            float sc[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                sc[n] = 0.f;
+#pragma unroll
+                for (int i = 0; i < q.N; ++i)
+                    sc[n] += (q.x[i].x * k2) * k[n].x[i].x + (q.x[i].y * k2) * k[n].x[i].y + (q.x[i].z * k2) * k[n].x[i].z +
+                             (q.x[i].w * k2) * k[n].x[i].w;
+            }
+#pragma unroll
+            for (int e = TPC / 2; e >= 1; e >>= 1)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) sc[n] += __shfl_xor_sync(0xffffffffu, sc[n], e);
+            float mn = m;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                if (!line) sc[n] = -INFINITY;
+                line &= line - 1;
+                mn = fmaxf(mn, sc[n]);
+            }
+            float f = ex2(m - mn);
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < q.N; ++i) o.x[i].x *= f, o.x[i].y *= f, o.x[i].z *= f, o.x[i].w *= f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                f = ex2(sc[n] - mn);
+                l += f;
+#pragma unroll
+                for (int i = 0; i < q.N; ++i) {
+                    o.x[i].x = fmaf(f, v[n].x[i].x, o.x[i].x), o.x[i].y = fmaf(f, v[n].x[i].y, o.x[i].y);
+                    o.x[i].z = fmaf(f, v[n].x[i].z, o.x[i].z), o.x[i].w = fmaf(f, v[n].x[i].w, o.x[i].w);
+                }
+            }
+            m = mn;
+            if (__any_sync(0xffffffffu, line != 0)) load(p, b, h, j, line);
+        }
+    }
+};
 
 // The many-units kernel (rswa_ranges.cu): its partial results' bytes, its launch.
 size_t ranges_part_bytes();
