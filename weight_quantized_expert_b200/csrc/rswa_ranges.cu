@@ -33,6 +33,7 @@ struct Shared {
     float part_m[COLS], part_l[COLS];
     float warp_m[WARPS][COLS], warp_l[WARPS][COLS], warp_f[WARPS + 1][COLS];   // f: a part's factor (the last: drafted keys)
     float step[COLS];                  // a score in units of log2 is (integer dot) * key scale * step
+    int row[COLS];                     // a column's row of the output, -1 without a live node
     int ages[COLS];                    // ring slots younger than this are seen (0 for a column without a node)
     unsigned long long line[TREE_MAX];
     int par[TREE_MAX];
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
         d.load(p, b, h, j, line);
         const float a = query_digits<INT4>(q, col, j, sh.qf);
         if (j == 0) {
+            sh.row[col] = live ? node * p.hq + h * p.G + (col0 + col) % p.G : -1;
             sh.ages[col] = live ? min(n, RW - __popcll(sh.line[node])) : 0;
             sh.step[col] = a / Q_TOP * (SCORE_SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
         }
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
         }
         cur = nxt;
     }
-    // ---- join the warps: partial outputs at [column][t * 8 + dim / 16], dim = 16 * (dim / 16) + t
+    // ---- join the warps
     cp_wait<0>();
     __syncwarp();
     {
@@ -458,7 +460,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
         for (int t = 0; t < 16; ++t)
 #pragma unroll
             for (int e = 0; e < HALVES; ++e)
-                *reinterpret_cast<float2*>(po + (gr + 8 * e) * PAD + t * 8 + 2 * c) = make_float2(O[t][2 * e], O[t][2 * e + 1]);
+                po[part_at(gr + 8 * e, 32 * c + t)] = O[t][2 * e], po[part_at(gr + 8 * e, 32 * c + 16 + t)] = O[t][2 * e + 1];
         if (c == 0) {
 #pragma unroll
             for (int e = 0; e < HALVES; ++e) sh.warp_m[warp][gr + 8 * e] = run_m[e], sh.warp_l[warp][gr + 8 * e] = run_l[e];
@@ -484,17 +486,19 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
         if (!complete) mine[col] = M, mine[PART_L + col] = l;
     }
     __syncthreads();
-    for (int i = tid; i < cols * RD; i += PT) {
-        const int col = i / RD, d = i % RD;
+    static_assert(PT == RD, "a thread has one dim of every column");
+    float* out = p.out + (size_t)b * p.N * p.hq * RD + tid;
+#pragma unroll 4
+    for (int col = 0; col < cols; ++col) {
+        const int d = tid;
         float o = sh.warp_f[WARPS][col] * sh.part[col][d];
 #pragma unroll
         for (int w = 0; w < WARPS; ++w)
-            o = fmaf(sh.warp_f[w][col], reinterpret_cast<const float*>(smem + w * St::BYTES)[col * PAD + (d & 15) * 8 + (d >> 4)], o);
+            o = fmaf(sh.warp_f[w][col], reinterpret_cast<const float*>(smem + w * St::BYTES)[part_at(col, d)], o);
         if (complete) {
-            const int node = (col0 + col) / p.G;
-            if (node < L) p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + d] = o / sh.part_l[col];
+            if (sh.row[col] >= 0) out[sh.row[col] * RD] = o / sh.part_l[col];
         } else {
-            mine[PART_O + i] = o;
+            mine[PART_O + col * RD + d] = o;
         }
     }
     }

@@ -58,6 +58,7 @@ struct Shared {
     float mx[PAIRS][2][COLS + 4];      // each warp's largest scores of a block, and its largest value scale
     float pair_m[PAIRS][COLS], warp_l[WARPS][COLS], pair_f[PAIRS + 1][COLS];   // f: a part's factor (the last: drafted keys)
     float step[COLS];                  // a score in units of log2 is (integer dot) * key scale * step
+    int row[COLS];                     // a column's row of the output, -1 without a live node
     int ages[COLS];                    // ring slots younger than this are seen (0 for a column without a node)
     unsigned long long line[TREE_MAX];
     int par[TREE_MAX];
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         d.load(p, b, h, j, line);
         const float a = query_digits<INT4>(q, col, j, sh.qf);
         if (j == 0) {
+            sh.row[col] = live ? node * p.hq + h * p.G + (col0 + col) % p.G : -1;
             sh.ages[col] = live ? min(n, RW - __popcll(sh.line[node])) : 0;
             sh.step[col] = a / Q_TOP * (SCORE_SCALE * LOG2E * (INT4 ? 1.f / 16.f : 1.f));
         }
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
                 O[t][i] = fmaf(upper(acc[2][i]), gain[i >> 1], fmaf(lower(acc[1][i], acc[0][i]), gain[i >> 1], O[t][i]));
         }
     }
-    // ---- join the pairs: partial outputs at [column][t * 8 + dim / 16], dim = 16 * (dim / 16) + t
+    // ---- join the pairs
     cp_wait<0>();
     named_bar_sync(1 + pair, 64);
     {
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         for (int t = 0; t < 8; ++t)
 #pragma unroll
             for (int e = 0; e < HALVES; ++e)
-                *reinterpret_cast<float2*>(po + (gr + 8 * e) * PAD + (8 * half + t) * 8 + 2 * c) = make_float2(O[t][2 * e], O[t][2 * e + 1]);
+                po[part_at(gr + 8 * e, 32 * c + 8 * half + t)] = O[t][2 * e], po[part_at(gr + 8 * e, 32 * c + 16 + 8 * half + t)] = O[t][2 * e + 1];
         if (c == 0) {
 #pragma unroll
             for (int e = 0; e < HALVES; ++e) {
@@ -420,25 +422,26 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         sh.part_m[col] = M, sh.part_l[col] = l;
     }
     __syncthreads();
-    for (int i = tid; i < cols * RD; i += PT) {
-        const int col = i / RD, d = i % RD;
+    float* out = p.out + (size_t)b * p.N * p.hq * RD + tid % RD;
+#pragma unroll 4
+    for (int col = tid / RD; col < cols; col += PT / RD) {
+        const int d = tid % RD;
         float o = sh.pair_f[PAIRS][col] * sh.part[col][d];
 #pragma unroll
         for (int w = 0; w < PAIRS; ++w)
-            o = fmaf(sh.pair_f[w][col], reinterpret_cast<const float*>(smem + w * St::BYTES)[col * PAD + (d & 15) * 8 + (d >> 4)], o);
+            o = fmaf(sh.pair_f[w][col], reinterpret_cast<const float*>(smem + w * St::BYTES)[part_at(col, d)], o);
         if (p.S > 1) {
             sh.part[col][d] = o;
         } else {
-            const int node = (col0 + col) / p.G;
-            if (node < L) p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + d] = o / sh.part_l[col];
+            if (sh.row[col] >= 0) out[sh.row[col] * RD] = o / sh.part_l[col];
         }
     }
     if (p.S > 1) {
         // ---- join the CTAs of the cluster: each takes every S-th column
         cluster_sync();
-        for (int i = tid; i < (cols - rank + p.S - 1) / p.S * RD; i += PT) {
-            const int col = rank + i / RD * p.S, d = i % RD, node = (col0 + col) / p.G;
-            if (node >= L) continue;
+        for (int col = rank + tid / RD * p.S; col < cols; col += PT / RD * p.S) {
+            const int d = tid % RD;
+            if (sh.row[col] < 0) continue;
             float m[8], M = NONE, l = 0.f, o = 0.f;
 #pragma unroll
             for (int r = 0; r < 8; ++r) m[r] = r < p.S ? ld_cluster(&sh.part_m[col], r) : NONE;
@@ -451,7 +454,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
                     l = fmaf(f, ld_cluster(&sh.part_l[col], r), l);
                     o = fmaf(f, ld_cluster(&sh.part[col][d], r), o);
                 }
-            p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + (col0 + col) % p.G) * RD + d] = o / l;
+            out[sh.row[col] * RD] = o / l;
         }
         cluster_sync();   // no CTA leaves while another reads its shared memory
     }

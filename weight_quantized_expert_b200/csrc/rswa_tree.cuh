@@ -10,7 +10,10 @@ constexpr int TREE_DIM = FOCR_RSWA_DIM, TREE_RING = FOCR_RSWA_RING;
 constexpr int TREE_MAX = FOCR_TREE_NODES_MAX;
 constexpr int COLS = 16;                        // columns of a unit: the rows of one MMA tile
 constexpr int BLK = 64;                         // keys of a block
-constexpr int PAD = TREE_DIM + 8;               // floats per row of a warp's partial output: no bank conflicts
+// A column's partial output in shared memory: its 128 dims with a gap behind each 16, PAD floats, so that neither a warp's
+// stores (columns gr, dims 32 c + t) nor its loads (neighbouring dims) meet in a bank.
+constexpr int PAD = TREE_DIM + 33;
+__device__ __forceinline__ int part_at(int col, int dim) { return col * PAD + dim + 4 * (dim >> 4); }
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float SCORE_SCALE = 0.08838834764831845f;   // 1 / sqrt(128)
 constexpr float Q_TOP = 8323072.f;              // 127 * 2^16: the largest fixed-point query value
