@@ -27,5 +27,9 @@ __device__ __forceinline__ double ld_cluster(const double* p, uint32_t rank) {
     asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(p, rank)) : "memory");
     return v;
 }
+// writes the same variable in the shared memory of the cluster's CTA `rank`
+__device__ __forceinline__ void st_cluster(float* p, uint32_t rank, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(p, rank)), "f"(v) : "memory");
+}
 
 }  // namespace focr

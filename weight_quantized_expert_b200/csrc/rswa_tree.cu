@@ -52,7 +52,9 @@ constexpr int WARPS = 8, PAIRS = WARPS / 2, PT = 32 * WARPS;   // two warps work
 
 struct Shared {
     uint4 qf[4 * 3][32];               // query digits as A fragments: [k-step * 3 + digit][lane]
-    float part[COLS][RD];              // the drafted keys' part, then the CTA's
+    float part[COLS][RD];              // the drafted keys' part
+    float got[COLS][RD];               // from rank r of the cluster, the i-th column this CTA answers for: [r * (COLS / S) + i]
+    float got_m[COLS], got_l[COLS];
     float part_m[COLS], part_l[COLS];
     uint4 px[PAIRS][2][3][32];         // a pair's weight digits as A fragments: [32 keys][digit][lane]
     float mx[PAIRS][2][COLS + 4];      // each warp's largest scores of a block, and its largest value scale
@@ -126,6 +128,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         return;
     }
     if (col0 / p.G >= L) return;   // no live node in this group, in any CTA of the cluster
+    if (p.S > 1) cluster_arrive();
     const size_t ref0 = ((size_t)b * p.hk + h) * p.ref.cap, ring0 = ((size_t)b * p.hk + h) * RW;
     // Rows of block i that hold a key (later ones are read from the last such row and masked), and its copies' start.
     auto rows_of = [&](int i) { return min(BLK, i >= nref ? min(n, RW) - (i - nref) * BLK : R - i * BLK); };
@@ -405,6 +408,8 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         }
     }
     __syncthreads();
+    const int slog = 31 - __clz(p.S);
+    if (p.S > 1) cluster_wait();   // every CTA of the cluster runs: its shared memory may be written
     if (tid < cols) {   // a column's maximum, the parts' factors, its sum
         const int col = tid;
         const float pm = sh.part_m[col];
@@ -420,6 +425,11 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
             l = fmaf(f, sh.warp_l[2 * w][col] + sh.warp_l[2 * w + 1][col], l);
         }
         sh.part_m[col] = M, sh.part_l[col] = l;
+        if (p.S > 1) {
+            const int at = rank * (COLS >> slog) + (col >> slog);
+            st_cluster(&sh.got_m[at], col & (p.S - 1), M);
+            st_cluster(&sh.got_l[at], col & (p.S - 1), l);
+        }
     }
     __syncthreads();
     float* out = p.out + (size_t)b * p.N * p.hq * RD + tid % RD;
@@ -431,32 +441,25 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         for (int w = 0; w < PAIRS; ++w)
             o = fmaf(sh.pair_f[w][col], reinterpret_cast<const float*>(smem + w * St::BYTES)[part_at(col, d)], o);
         if (p.S > 1) {
-            sh.part[col][d] = o;
+            st_cluster(&sh.got[rank * (COLS >> slog) + (col >> slog)][d], col & (p.S - 1), o);
         } else {
             if (sh.row[col] >= 0) out[sh.row[col] * RD] = o / sh.part_l[col];
         }
     }
     if (p.S > 1) {
-        // ---- join the CTAs of the cluster: each takes every S-th column
+        // ---- join the CTAs of the cluster: a column's parts have been stored in the CTA that answers for it
         cluster_sync();
         for (int col = rank + tid / RD * p.S; col < cols; col += PT / RD * p.S) {
-            const int d = tid % RD;
-            if (sh.row[col] < 0) continue;
-            float m[8], M = NONE, l = 0.f, o = 0.f;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) m[r] = r < p.S ? ld_cluster(&sh.part_m[col], r) : NONE;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) M = fmaxf(M, m[r]);
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (r < p.S) {
-                    const float f = ex2(m[r] - M);
-                    l = fmaf(f, ld_cluster(&sh.part_l[col], r), l);
-                    o = fmaf(f, ld_cluster(&sh.part[col][d], r), o);
-                }
-            out[sh.row[col] * RD] = o / l;
+            const int at = col >> slog, step = COLS >> slog;
+            float M = NONE, l = 0.f, o = 0.f;
+            for (int r = 0; r < p.S; ++r) M = fmaxf(M, sh.got_m[r * step + at]);
+            for (int r = 0; r < p.S; ++r) {
+                const float f = ex2(sh.got_m[r * step + at] - M);
+                l = fmaf(f, sh.got_l[r * step + at], l);
+                o = fmaf(f, sh.got[r * step + at][tid % RD], o);
+            }
+            if (sh.row[col] >= 0) out[sh.row[col] * RD] = o / l;
         }
-        cluster_sync();   // no CTA leaves while another reads its shared memory
     }
 }
 
