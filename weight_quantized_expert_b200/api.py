@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 import typing
 
@@ -125,10 +126,10 @@ def lib():
                 "focr_rswa_decode": (i32, [P, P, P, P, P, P, i32, P, P, P, i32, P, P, sz, P]),
                 "focr_qk_norm_rope": (i32, [P, i64, i32, P, i64, i32, P, i32, P, P, ctypes.c_float, ctypes.c_double,
                                             i32, i32, P, i64, P, i64, P]),
-                "focr_kv_write": (i32, [ctypes.POINTER(KVCacheDesc), P, i64, P, i64, i64, P, P, P, i32, P, i32, P]),
-                "focr_kv_read": (i32, [ctypes.POINTER(KVCacheDesc), P, P, P, P]),
-                "focr_rswa_tree": (i32, [P, P, P, i32, i32, i32, ctypes.POINTER(KVCacheDesc), P,
-                                         ctypes.POINTER(KVCacheDesc), P, P, P, P, P, sz, P]),
+                "focr_kv_write": (i32, [P, P, i64, P, i64, i64, P, P, P, i32, P, i32, P]),
+                "focr_kv_read": (i32, [P, P, P, P, P]),
+                "focr_rswa_tree": (i32, [P, P, P, i32, i32, i32, P, P,
+                                         P, P, P, P, P, P, sz, P]),
                 "focr_rswa_tree_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
                 "focr_token_probs": (i32, [P, i32, i32, ctypes.c_float, P, P]),
                 "focr_spec_verify": (i32, [P, P, i32, P, P, P, P, i32, i32, P, P, P, P]),
@@ -543,16 +544,21 @@ def new_kv_cache(B: int, heads: int, cap: int, wtype: int = W_INT8, device="cuda
     return KVCache(k, torch.zeros(shape[:3], device=device), v, torch.zeros(shape[:3], device=device))
 
 
-def _kv_desc(cache, dev: int, name: str = "cache") -> KVCacheDesc:
+_pack_cache = struct.Struct("PPPPiiii").pack   # a KVCacheDesc, in a quarter of its constructor's time
+
+
+def _kv_desc(cache, dev: int, name: str = "cache"):
+    """(descriptor, B, heads, cap)"""
     k, ks, v, vs = cache
-    shape, int8 = k.shape, k.dtype is _torch.int8
-    _need(len(shape) == 4 and shape[3] == (RSWA_DIM if int8 else RSWA_DIM // 2),
-          f"{name}: codes are [B, heads, cap, 128] int8 or [B, heads, cap, 64] uint8")
-    dtype = _torch.int8 if int8 else _torch.uint8
-    B, heads, cap = rows = shape[:3]
-    return KVCacheDesc(_need_tensor(name, k, dev, dtype, shape), _need_tensor(name, ks, dev, _torch.float32, rows),
-                       _need_tensor(name, v, dev, dtype, shape), _need_tensor(name, vs, dev, _torch.float32, rows),
-                       W_INT8 if int8 else W_INT4, B, heads, cap)
+    shape, dtype = k.shape, k.dtype
+    int8 = dtype is _torch.int8
+    if len(shape) != 4 or shape[3] != (RSWA_DIM if int8 else RSWA_DIM // 2) or not (int8 or dtype is _torch.uint8):
+        raise FocrError(1, f"{name}: codes are [B, heads, cap, 128] int8 or [B, heads, cap, 64] uint8")
+    B, heads, cap, _ = shape
+    rows, f32 = (B, heads, cap), _torch.float32
+    return _pack_cache(_need_tensor(name, k, dev, dtype, shape), _need_tensor(name, ks, dev, f32, rows),
+                       _need_tensor(name, v, dev, dtype, shape), _need_tensor(name, vs, dev, f32, rows),
+                       W_INT8 if int8 else W_INT4, B, heads, cap), B, heads, cap
 
 
 def focr_kv_write(cache, k, v, count, start, row0=None, index=None, n_max: int | None = None, wrap: bool = False,
@@ -562,14 +568,14 @@ def focr_kv_write(cache, k, v, count, start, row0=None, index=None, n_max: int |
     tokens of a sequence (default: the columns of index, else rows // B)."""
     torch, L = _tensor_lib()
     dev = _device_of(k, "k")
-    desc = _kv_desc(cache, dev)
-    B, shape, i32 = desc.B, k.shape, torch.int32
-    _need(len(shape) == 3 and shape[1] == desc.heads, "k and v must be [rows, heads, 128] with the cache's heads")
+    desc, B, heads, _ = _kv_desc(cache, dev)
+    shape, i32 = k.shape, torch.int32
+    _need(len(shape) == 3 and shape[1] == heads, "k and v must be [rows, heads, 128] with the cache's heads")
     kp, ldk = _need_rows("k", k, dev, shape)
     vp, ldv = _need_rows("v", v, dev, shape)
     if n_max is None:
         n_max = index.shape[1] if index is not None else max(1, shape[0] // B)
-    _call(L.focr_kv_write, dev, stream, ctypes.byref(desc), kp, ldk, vp, ldv, shape[0],
+    _call(L.focr_kv_write, dev, stream, desc, kp, ldk, vp, ldv, shape[0],
           None if row0 is None else _need_tensor("row0", row0, dev, i32, (B,)), _need_tensor("count", count, dev, i32, (B,)),
           None if index is None else _need_tensor("index", index, dev, i32, (B, n_max)), n_max,
           _need_tensor("start", start, dev, i32, (B,)), KV_WRAP if wrap else 0)
@@ -581,13 +587,13 @@ def focr_kv_read(cache, length, k_out=None, v_out=None, stream=None):
     (zero where they are made here)."""
     torch, L = _tensor_lib()
     dev = _device_of(cache[0], "the cache")
-    desc = _kv_desc(cache, dev)
-    shape = (desc.B, desc.heads, desc.cap, RSWA_DIM)
+    desc, B, heads, cap = _kv_desc(cache, dev)
+    shape = (B, heads, cap, RSWA_DIM)
     if k_out is None:
         k_out = _new(dev, stream, shape, zero=True)
     if v_out is None:
         v_out = _new(dev, stream, shape, zero=True)
-    _call(L.focr_kv_read, dev, stream, ctypes.byref(desc), _need_tensor("length", length, dev, torch.int32, (desc.B,)),
+    _call(L.focr_kv_read, dev, stream, desc, _need_tensor("length", length, dev, torch.int32, (B,)),
           _need_tensor("k_out", k_out, dev, torch.float32, shape), _need_tensor("v_out", v_out, dev, torch.float32, shape))
     return k_out, v_out
 
@@ -606,17 +612,18 @@ def focr_rswa_tree(q, k_new, v_new, ref, ref_len, ring, n_gen, parent=None, n_no
     shape, f32, i32 = q.shape, torch.float32, torch.int32
     _need(len(shape) == 4 and shape[3] == RSWA_DIM, "q must be [B, N, heads_q, 128]")
     B, N, hq, _ = shape
-    dref, dring = _kv_desc(ref, dev, "ref"), _kv_desc(ring, dev, "ring")
+    dref, _, heads, cap = _kv_desc(ref, dev, "ref")
+    dring = _kv_desc(ring, dev, "ring")[0]
     if out is None:
         out = _new(dev, stream, shape, zero=True)
     if workspace is None:
-        need = L.focr_rswa_tree_workspace_bytes(B, N, hq, dref.heads, dref.cap)
+        need = L.focr_rswa_tree_workspace_bytes(B, N, hq, heads, cap)
         workspace = _new(dev, stream, (need,), torch.uint8) if need else None
     ws_bytes = 0 if workspace is None else workspace.numel()
-    new = (B, N, dref.heads, RSWA_DIM)
+    new = (B, N, heads, RSWA_DIM)
     _call(L.focr_rswa_tree, dev, stream, _need_tensor("q", q, dev, f32, shape), _need_tensor("k_new", k_new, dev, f32, new),
-          _need_tensor("v_new", v_new, dev, f32, new), B, N, hq, ctypes.byref(dref),
-          _need_tensor("ref_len", ref_len, dev, i32, (B,)), ctypes.byref(dring), _need_tensor("n_gen", n_gen, dev, i32, (B,)),
+          _need_tensor("v_new", v_new, dev, f32, new), B, N, hq, dref,
+          _need_tensor("ref_len", ref_len, dev, i32, (B,)), dring, _need_tensor("n_gen", n_gen, dev, i32, (B,)),
           None if parent is None else _need_tensor("parent", parent, dev, i32, (B, N)),
           None if n_nodes is None else _need_tensor("n_nodes", n_nodes, dev, i32, (B,)),
           _need_tensor("out", out, dev, f32, shape),
