@@ -195,7 +195,21 @@ def random_tree(rng, N):
     return [int(rng.integers(max(-1, i - 5), i)) for i in range(N)]
 
 
-def check_tree(seed, B, N, hq, hk, Rcap, ref_len, n_gen, int4=False, parent="random", n_nodes=None, qscale=1.0):
+MANY = 25000     # a capacity that even a small call splits into ranges
+
+
+def wide_cache(cache, cap=MANY):
+    """On the device with more rows, which hold scales that would show."""
+    import torch
+    out = []
+    for x in dev_cache(cache):
+        y = torch.full((*x.shape[:2], cap, *x.shape[3:]), float("nan") if x.ndim == 3 else 77, dtype=x.dtype, device="cuda")
+        y[:, :, :x.shape[2]] = x
+        out.append(y)
+    return out
+
+
+def check_tree(seed, B, N, hq, hk, Rcap, ref_len, n_gen, int4=False, parent="random", n_nodes=None, qscale=1.0, wide=None):
     import torch
     rng = np.random.default_rng(seed)
     q, k, v = f32(rng, B, N, hq, 128) * np.float32(qscale), f32(rng, B, N, hk, 128), f32(rng, B, N, hk, 128)
@@ -213,7 +227,9 @@ def check_tree(seed, B, N, hq, hk, Rcap, ref_len, n_gen, int4=False, parent="ran
             for x in (q, k, v):
                 x[b, max(0, n_nodes[b]):] = np.nan
     out = torch.full((B, N, hq, 128), 7.0, device="cuda")
-    api.focr_rswa_tree(dev(q), dev(k), dev(v), dev_cache(ref), ints(ref_len), dev_cache(ring), ints(n_gen), ints(parent),
+    dref = wide_cache(ref, wide) if wide else dev_cache(ref)
+    assert bool(wide) == bool(api.focr_rswa_tree_workspace_bytes(B, N, hq, hk, dref[1].shape[2]))     # the kernel meant
+    api.focr_rswa_tree(dev(q), dev(k), dev(v), dref, ints(ref_len), dev_cache(ring), ints(n_gen), ints(parent),
                        ints(n_nodes), out=out)
     ref, ring = (tuple(np.nan_to_num(sp.values(c[i], c[i + 1])) for i in (0, 2)) for c in (ref, ring))
     want = sp.rswa_tree(q, k, v, ref, ref_len, ring, n_gen, parent, n_nodes)
@@ -267,7 +283,7 @@ def test_long_reference_block(int4):
 @pytest.mark.parametrize("N,hq,hk", [(1, 2, 2), (3, 4, 1), (16, 2, 2), (17, 1, 1), (16, 4, 2), (21, 2, 1), (33, 1, 1), (64, 1, 1), (16, 8, 2)])
 def test_many_units_kernel_head_layouts(N, hq, hk, int4):
     # few units but a capacity that splits into ranges; lengths around its tiles of 128
-    check_tree(400 + N, 3, N, hq, hk, 4300, [4300, 257, 128], [600, 127, 1], int4)
+    check_tree(400 + N, 3, N, hq, hk, 4300, [4300, 257, 128], [600, 127, 1], int4, wide=MANY)
 
 
 @pytest.mark.parametrize("int4", [False, True])
@@ -280,7 +296,7 @@ def test_many_units_kernel_on_a_ragged_batch(int4):
     gen[:4] = [0, 0, 1, 5]
     nodes = [int(x) for x in rng.integers(0, 4, B)]
     nodes[:4] = [3, 1, 0, 2]
-    check_tree(45, B, 3, 2, 2, 520, lens, gen, int4, n_nodes=nodes)
+    check_tree(45, B, 3, 2, 2, 520, lens, gen, int4, n_nodes=nodes, wide=1100)
 
 
 def test_many_units_kernel_when_the_scores_keep_rising():
@@ -295,7 +311,7 @@ def test_many_units_kernel_when_the_scores_keep_rising():
         ref = [x for y in (k, v) for x in sp.quantise(y, int4)]
         ring = np_cache(rng, 1, 2, 128, int4)
         kn, vn = f32(rng, 1, N, 2, 128), f32(rng, 1, N, 2, 128)
-        got = api.focr_rswa_tree(dev(q), dev(kn), dev(vn), dev_cache(ref), ints([R]), dev_cache(ring), ints([40])).cpu().numpy()
+        got = api.focr_rswa_tree(dev(q), dev(kn), dev(vn), wide_cache(ref), ints([R]), dev_cache(ring), ints([40])).cpu().numpy()
         val = lambda c: (sp.values(c[0], c[1]), sp.values(c[2], c[3]))  # noqa: E731
         want = sp.rswa_tree(q, kn, vn, val(ref), [R], val(ring), [40])
         assert np.abs(got - want).max() <= TOL_TREE * np.abs(v).max()
@@ -307,10 +323,10 @@ def test_many_units_kernel_marks_invalid_sequences():
     B, N, cap = 6, 3, 4300
     q, k = f32(rng, B, N, 2, 128), f32(rng, B, N, 2, 128)
     ref, ring = np_cache(rng, B, 2, cap, False), np_cache(rng, B, 2, 128, False)
-    ref_len, n_gen, n_nodes = [cap + 1, -1, 900, 4300, 4300, 1200], [5, 5, -1, 5, 5, 5], [3, 2, 3, 4, 3, 3]
+    ref_len, n_gen, n_nodes = [MANY + 1, -1, 900, 4300, 4300, 1200], [5, 5, -1, 5, 5, 5], [3, 2, 3, 4, 3, 3]
     parent = [[-1, 0, 1]] * 4 + [[-1, 1, 0]] + [[-1, 0, -1]]
     out = torch.full((B, N, 2, 128), 7.0, device="cuda")
-    api.focr_rswa_tree(dev(q), dev(k), dev(k), dev_cache(ref), ints(ref_len), dev_cache(ring), ints(n_gen), ints(parent),
+    api.focr_rswa_tree(dev(q), dev(k), dev(k), wide_cache(ref), ints(ref_len), dev_cache(ring), ints(n_gen), ints(parent),
                        ints(n_nodes), out=out)
     got = out.cpu().numpy()
     assert np.isnan(got[[0, 2, 3, 4]]).all() and np.isnan(got[1, :2]).all() and (got[1, 2] == 7.0).all()
@@ -351,7 +367,7 @@ def test_invalid_sequences_get_nan_and_spare_the_others():
     assert np.isfinite(got[5]).all()
 
 
-@pytest.mark.parametrize("cap", [300, 4300])      # one launch; ranges
+@pytest.mark.parametrize("cap", [300, MANY])      # one launch; ranges
 @pytest.mark.parametrize("int4", [False, True])
 @pytest.mark.parametrize("what", [np.nan, np.inf])
 @pytest.mark.parametrize("which", [1, 3])         # key scales, value scales
@@ -360,13 +376,13 @@ def test_a_scale_that_is_no_number_reaches_those_who_see_it_alone(cap, int4, wha
     rng = np.random.default_rng(48)
     B, N, n = 3, 3, 200
     q, k, v = (f32(rng, B, N, 2, 128) for _ in range(3))
-    ref, ring = np_cache(rng, B, 2, cap, int4), np_cache(rng, B, 2, 128, int4)
+    ref, ring = np_cache(rng, B, 2, 300, int4), np_cache(rng, B, 2, 128, int4)
     ring[which][0, :, 72] = ring[which][1, :, 73] = ref[which][2, 0, 10] = what
-    got = api.focr_rswa_tree(dev(q), dev(k), dev(v), dev_cache(ref), ints([cap] * B), dev_cache(ring), ints([n] * B)).cpu().numpy()
+    got = api.focr_rswa_tree(dev(q), dev(k), dev(v), wide_cache(ref, cap), ints([300] * B), dev_cache(ring), ints([n] * B)).cpu().numpy()
     ref[which][2, 0, 10] = 0
     ring[which][0, :, 72] = ring[which][1, :, 73] = 0
     val = lambda c: (sp.values(c[0], c[1]), sp.values(c[2], c[3]))  # noqa: E731
-    want = sp.rswa_tree(q, k, v, val(ref), [cap] * B, val(ring), [n] * B)
+    want = sp.rswa_tree(q, k, v, val(ref), [300] * B, val(ring), [n] * B)
     ok = np.ones(got.shape, bool)
     ok[1, 0] = ok[2, :, 0] = False
     assert np.abs(got - want)[ok].max() <= TOL_TREE * max(np.abs(val(ref)[1]).max(), np.abs(val(ring)[1]).max(), np.abs(v).max())

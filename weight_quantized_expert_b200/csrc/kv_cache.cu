@@ -5,7 +5,11 @@
 // fp32 scale with its group).  The group is a whole row, the 128 values of one head of one token:
 //   s = fp32(max|x|) / Q as one fp32 division (Q = 127 int8, 7 int4); q = round-half-even(fp32(x / s)) clamped to
 //   [-127, 127] or [-8, 7]; a row with s = 0 has q = 0;  the value read back is fp32(s * q).
-// Both kernels are bound by memory: 512 B of fp32 against 132 B (int8) or 68 B (int4) a row, each moved once.
+// Both kernels are bound by memory: 512 B of fp32 against 132 B (int8) or 68 B (int4) a row, each moved once.  Half a warp
+// has a token of a head, its K and its V row, with all loads issued before the first is used, and a division only where a
+// value lies next to a border of the rounding (a warp a row, all divided: 159 us instead of 112).  8 sequences x 10 heads x
+// ragged 4096 rows, int8, written and read back (659 MB): 112 us, 5.9 TB/s; 8 x 9 tokens into an int4 ring and the ring
+// read back: 5.4 us, two launches.
 #include "abi_util.h"
 #include "common.cuh"
 #include "kv_cache.h"

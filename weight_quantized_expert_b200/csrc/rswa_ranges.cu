@@ -1,11 +1,19 @@
-// The tree attention of rswa_tree.cu for many units or long reference blocks: equal ranges of blocks per CTA.
+// The tree attention of rswa_tree.cu for many or long units: equal ranges of blocks per CTA.
 //
-// The mathematics and the fragments are those of rswa_tree.cu.  All 64-key blocks of all units form one row, cut into
-// equal ranges, one per resident CTA (the lengths are read on the device, so ragged batches stay balanced); units that a
-// cut divides leave partial results in the workspace, and a second kernel joins them.  Here a block is one warp's: with
-// no barrier in the loop and 255 registers it needs a quarter fewer instructions than two warps a block, which pays once
-// the device is full (217 us against 258 us for 8 sequences x 10 heads x 32 nodes over 32768 rows, int8); with few blocks
-// a warp the other form's lower latency wins.
+// The mathematics and the fragments are those of rswa_tree.cu.  All units stand in one row, a unit as long as its 64-key
+// blocks and BEGIN more for what it costs to begin one, and the row is cut into equal ranges, one per resident CTA (the
+// lengths are read on the device, so ragged batches stay balanced).  Units that a cut divides leave partial results in the
+// workspace, and a second kernel joins them.  Here a block is one warp's: with no barrier in the loop and 255 registers it
+// needs a quarter fewer instructions than two warps a block, which pays once the device is full (217 us against 258 us for
+// 8 sequences x 10 heads x 32 nodes over 32768 rows, int8); with few blocks a warp the other form's lower latency wins.
+//
+// Measured: 8 x 10 x 32 nodes over ragged 32768 rows, int8 (549 MB, 85 us at the copy rate): 209 us; 32 x 10 x 14 columns
+// over ragged 4096 rows, int4 (146 MB, 23 us): 73 us.  What bounds it is the work between the products: a block of 16
+// columns x 64 keys takes 192 matrix instructions (1540 cycles of a scheduler's tensor core) and 1550 others (digits taken
+// apart and put together, exponentials, transposed values), 3000 cycles with two warps a scheduler; registers leave no
+// room for a third.  Beginning and ending a unit costs 5 us (13 us with a column a warp at a time and ranges that
+// did not count it: 225 and 87 us).  The tensor-memory form of the same products (kind::i8) came to 224 and 125 us with
+// four times the error: its exponentials wait on tensor-memory loads instead.
 #include <math.h>
 
 #include "abi_util.h"
@@ -41,7 +49,7 @@ struct Shared {
 };
 
 // A unit's length in the row: what it costs to begin it, in blocks, and its blocks (one at least: the drafted keys need a
-// CTA too).
+// CTA too).  BEGIN = 3 / 6 / 9: 76.3 / 73.2 / 74.3 us for the int4 call above.
 constexpr int BEGIN = 6;
 __device__ __forceinline__ int unit_length(const TreeParams& p, int b) {
     const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b);

@@ -17,24 +17,27 @@
 //             + 256 d1 + d0), d2 signed, so it is off by half a step of 2^-23 max|q|.  Three products of the digits
 //             with the key codes give the exact integer dot; the key's scale, the query's step and log2(e) / sqrt(128)
 //             follow in fp32.
-//   softmax   online over blocks of 64 keys, base 2, per warp.
+//   softmax   online over blocks of 64 keys, base 2.
 //   values    out needs sum_j e_j vs_j vc_j.  The weights of a block, relative to the block's largest score and
 //             largest value scale, are written as three unsigned digits (step 2^-23); the three integer sums over the
 //             64 keys are exact, join in fp32 and are added to the fp32 accumulator with the block's factor.
 //   No sum can wrap or leave a float's exact integers: |sum| <= 128 * 128 * 255 < 2^22, so accumulators start at the
 //   bit pattern of 1.5 * 2^23 and are read back as floats by one subtraction.
-// Drafted keys and values stay fp32 and are few: a warp takes a column and walks its line on the CUDA cores.
+// Against 64 bits the result is off by 3e-7 of its norm (fp32 matrix products and softmax: 2e-7 to 3e-6, growing with the
+// number of keys, which this does not).
 //
 // Work split: a unit is one kv head of one sequence with up to 16 columns; its keys are blocks of 64 (reference rows,
-// then the ring), which the four pairs of warps of a CTA take in turn, each with its own copies in flight (cp.async into
-// its part of shared memory: the next block's K loads while P V runs, its V while Q K runs).  In a pair each warp has the
-// scores of half the keys and the values of half the dims, so 128 registers hold its accumulators and four warps per
-// scheduler hide each other's latencies (one warp per block needed 255: two per scheduler, half the issue rate).
-//   few units   a cluster of S CTAs has a unit and joins through distributed shared memory: one launch.
-//   many units  all blocks of all units in one row, cut into equal ranges, one per resident CTA (the lengths are read
-//               on the device, so ragged batches stay balanced); units that a cut divides leave partial results in
-//               the workspace, and a second kernel joins them.
-// Bound by memory: 264 B (int8) or 136 B (int4) a key and head.
+// then the ring).  This kernel gives a unit to a cluster of S CTAs, which take its blocks in turn by pairs of warps, each
+// pair with its own copies in flight (cp.async into its part of shared memory: the next block's K loads while P V runs,
+// its V while Q K runs).  In a pair each warp has the scores of half the keys and the values of half the dims, so 128
+// registers hold its accumulators and a block's latency is halved (a warp a block: 19.3 us instead of 16.9 for 8 sequences
+// x 10 heads x 16 nodes over 289 rows).  Parts are joined through distributed shared memory, each CTA storing into the
+// one that answers for a column (loading them instead: 13.6 instead of 13.0 us).  Drafted keys and values stay fp32 and
+// are few: all columns walk their lines at once on the CUDA cores, before the blocks.  Long or many units go to
+// rswa_ranges.cu.
+// 264 B (int8) or 136 B (int4) a key and head have to be read; for the calls that come here latency is the bound: 1
+// sequence x 10 heads x 1 node over 289 rows 7.1 us, 8 x 10 x 16 nodes 13.0 us.  The chain is lengths -> lines -> drafted
+// rows (2 us), a block's copies and products (2 us), the join of warps and CTAs (2 us).
 #include <math.h>
 
 #include "abi_util.h"
@@ -463,8 +466,13 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
     }
 }
 
-// How a call is split, from its sizes alone: a cluster for each unit while all of them fit the device at once (two CTAs
-// per SM) with at most two blocks a pair, else the many-units kernel.
+// How a call is split, from its sizes alone: a cluster for each unit, of as many CTAs as give every pair of warps a block
+// and the device no more than two CTAs per SM; or ranges (rswa_ranges.cu), which use the whole device whatever the units
+// are, but cost a second kernel and longer beginnings.  Clusters are taken up to 12 blocks a pair while they leave at most
+// one CTA to an SM, else up to 4.  Measured, clusters against ranges (us, int8): 1 sequence x 10 heads x 1 node over 8000
+// / 16000 / 24000 rows (4, 8, 12 blocks a pair) 13.9 / 22.7 / 31.4 against 25.9 / 30.5 / 34.5; 3 x 10 x 4 over 12000
+// rows (12) 25.7 against 30.4; 8 x 10 x 16 over 896 / 1792 rows (2, 4 blocks; 160 CTAs) 16.7 / 22.6 against 20.0 / 23.8;
+// 32 x 10 x 14 over 896 rows (4; 320 CTAs) 34.9 against 34.1.
 struct TreePlan {
     int groups, S;
     bool ranges;
@@ -478,7 +486,7 @@ TreePlan tree_plan(int B, int N, int heads_q, int heads, int cap) {
     pl.S = 1;
     while (pl.S < 8 && pl.S * PAIRS < blocks) pl.S *= 2;
     while (pl.S > 1 && units * pl.S > 2 * sms) pl.S /= 2;
-    pl.ranges = blocks > 2 * pl.S * PAIRS;
+    pl.ranges = blocks > (units * pl.S > sms ? 4 : 12) * pl.S * PAIRS;
     return pl;
 }
 

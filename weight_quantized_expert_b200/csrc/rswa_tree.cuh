@@ -113,7 +113,7 @@ __device__ __forceinline__ int v_off(int r, int j) {
 }
 
 // Before the blocks all columns of a unit are worked on at once, by TPC neighbouring threads each: thread j of a column has
-// the 16-byte chunks j, j + TPC, ... of its rows.  (One column a warp, several in turn: 5 us a unit instead of 2.)
+// the 16-byte chunks j, j + TPC, ... of its rows.  (A column a warp, several in turn: 5 us a unit instead of 2.)
 template <int TPC>
 struct RowPart {
     static constexpr int N = TREE_DIM / 4 / TPC;
