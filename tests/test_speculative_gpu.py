@@ -134,6 +134,30 @@ def test_prefill_write_of_ragged_sequences(int4):
 
 
 @pytest.mark.parametrize("int4", [False, True])
+def test_write_next_to_the_borders_of_the_rounding(int4):
+    import torch
+    # values at (k + 1/2) steps and one or two floats to either side, for steps of all mantissas
+    rng = np.random.default_rng(29)
+    top, rows = (7, 2000) if int4 else (127, 2000)
+    m = (top * np.exp(rng.uniform(-20, 20, rows))).astype(np.float32)
+    m[:4] = top, 2 * top, np.float32(1e-30), np.float32(1e30)
+    step = m / np.float32(top)
+    x = ((rng.integers(-top, top, (rows, 128)) + 0.5) * step[:, None].astype(np.float64)).astype(np.float32)
+    for _ in range(2):
+        x = np.where(rng.random(x.shape) < 0.4, np.nextafter(x, np.where(rng.random(x.shape) < 0.5, np.inf, -np.inf).astype(np.float32)), x)
+    x = np.clip(x, -m[:, None], m[:, None])
+    x[:, 5] = m
+    c = api.new_kv_cache(1, 1, rows, api.W_INT4 if int4 else api.W_INT8)
+    d = dev(x[:, None])
+    api.focr_kv_write(c, d, d, ints([rows]), ints([0]))
+    torch.cuda.synchronize()
+    codes, scales = sp.quantise(x, int4)
+    for got_c, got_s in ((c.k, c.k_scale), (c.v, c.v_scale)):
+        np.testing.assert_array_equal(got_s.cpu().numpy()[0, 0], scales)
+        np.testing.assert_array_equal(got_c.cpu().numpy()[0, 0], codes)
+
+
+@pytest.mark.parametrize("int4", [False, True])
 def test_ring_commit_by_path_with_wrap_and_more_tokens_than_slots(int4):
     rng = np.random.default_rng(12)
     index = np.stack([rng.permutation(150) for _ in range(4)])

@@ -7,9 +7,9 @@
 //   [-127, 127] or [-8, 7]; a row with s = 0 has q = 0;  the value read back is fp32(s * q).
 // Both kernels are bound by memory: 512 B of fp32 against 132 B (int8) or 68 B (int4) a row, each moved once.  Half a warp
 // has a token of a head, its K and its V row, with all loads issued before the first is used, and a division only where a
-// value lies next to a border of the rounding (a warp a row, all divided: 159 us instead of 112).  8 sequences x 10 heads x
-// ragged 4096 rows, int8, written and read back (659 MB): 112 us, 5.9 TB/s; 8 x 9 tokens into an int4 ring and the ring
-// read back: 5.4 us, two launches.
+// value lies next to a border of the rounding.  8 sequences x 10 heads x ragged 4096 rows, int8, written and read back (659
+// MB): 106 us, 6.2 TB/s (a warp a row, all divided: 159 us; values rounded, clamped and packed one by one: 112 us, bound by
+// the write's instructions); 8 x 9 tokens into an int4 ring and the ring read back: 5.2 us, two launches.
 #include "abi_util.h"
 #include "common.cuh"
 #include "kv_cache.h"
@@ -28,12 +28,31 @@ struct WriteParams {
     int n_max, wrap;
 };
 
-// The code of one value: round-half-even(fp32(x / s)).  The product with the reciprocal is within 127 x 2^-21 of the
-// quotient; only where it lies nearer than that to a border of the rounding (or is not a number) is the division done.
-__device__ __forceinline__ int code_of(float x, float s, float inv) {
-    const float t = x * inv, r = rintf(t);
-    if (!(fabsf(t - r) < 0.4999f)) return __float2int_rn(x / s);
-    return (int)r;
+// round-half-even(fp32(x / s)) by the division itself.
+template <bool INT4>
+__device__ __noinline__ uint32_t codes_by_division(float4 x, float s) {
+    const float in[4] = {x.x, x.y, x.z, x.w};
+    uint32_t w = 0u;
+    for (int j = 0; j < 4; ++j) {
+        const int q = __float2int_rn(in[j] / s);
+        w |= ((uint32_t)(INT4 ? max(-8, min(7, q)) : max(-127, min(127, q))) & 255u) << 8 * j;
+    }
+    return w;
+}
+// Codes of four values, one a byte.  x / s is formed with the reciprocal, rounded by adding 1.5 * 2^23 (the code is then the
+// sum's low byte), and its distance from the rounded value returned through `far`.  The reciprocal and the division each
+// round by 2^-24 of at most 127, so the code is the division's unless the distance is within 2^-15 of a half.
+__device__ __forceinline__ uint32_t codes4(float4 x, float inv, float& far) {
+    constexpr float MAGIC = 12582912.f;
+    const float in[4] = {x.x, x.y, x.z, x.w};
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float t = fmaf(in[j], inv, MAGIC);
+        u[j] = __float_as_uint(t);
+        far = fmaxf(far, fabsf(fmaf(in[j], inv, MAGIC - t)));
+    }
+    return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
 }
 // A row of 128 by half a warp: lane l has values 4 l .. 4 l + 3 (a) and 64 + 4 l .. 64 + 4 l + 3 (b).
 template <bool INT4>
@@ -43,16 +62,18 @@ __device__ __forceinline__ void quantise_row(float4 a, float4 b, bool live, uint
 #pragma unroll
     for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float s = m / (INT4 ? 7.f : 127.f), inv = 1.f / s;
-    const float in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t w[2] = {0u, 0u};
     if (s > 0.f) {
+        float far = 0.f;
+        w[0] = codes4(a, inv, far), w[1] = codes4(b, inv, far);
+        // scales near the subnormal numbers (reciprocals that overflow, rounded scales) and what is no number go the same way
+        if (!(far < 0.5f - 3.1e-5f) || !(s > 1e-35f) || !(s < 1e35f)) w[0] = codes_by_division<INT4>(a, s), w[1] = codes_by_division<INT4>(b, s);
+        if (INT4) {   // bytes to nibbles
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int q = code_of(in[j], s, inv);
-            if (INT4)
-                w[j / 4] |= (uint32_t)(max(-8, min(7, q)) & 15) << 4 * (j % 4);
-            else
-                w[j / 4] |= (uint32_t)(max(-127, min(127, q)) & 255) << 8 * (j % 4);
+            for (int i = 0; i < 2; ++i) {
+                w[i] &= 0x0F0F0F0Fu;
+                w[i] = __byte_perm(w[i] | w[i] >> 4, 0u, 0x4420);
+            }
         }
     }
     if (!live) return;

@@ -8,8 +8,8 @@
 // The angle is formed in revolutions in fp64 and reduced to [-1/2, 1/2] before it is rounded to fp32, so far
 // positions lose nothing: the reduced angle is off by at most 2^-25 revolutions plus pos x 2^-53 x a few.
 //
-// Bound by memory: every row is read and written once, 1 KB a row.  8192 tokens x 20 heads with norms (168 MB): 31.5 us, 5.3
-// TB/s; one token: 1.7 us.  A block a token, its rows' loads ahead of the angles, half a warp a row (a warp a row with the
+// Bound by memory: every row is read and written once, 1 KB a row.  8192 tokens x 20 heads with norms (168 MB): 29.2 us, 5.7
+// TB/s (31.6 with 40 registers instead of 32, a few of them spilled); one token: 1.7 us.  A block a token, its rows' loads ahead of the angles, half a warp a row (a warp a row with the
 // angles first: 50 us; blocks that stay and take tokens in turn: 66 us, each waiting for the angles of its next token).
 #include <math.h>
 
@@ -38,7 +38,7 @@ struct RopeParams {
 // HOW: 0 pairs (2i, 2i + 1); 1 pairs (i, i + 64): both in a lane.  2 pairs (i, i + rot / 2), rot < 128, through shared
 // memory.
 template <int HOW, bool NORM>
-__global__ void __launch_bounds__(32 * RWARPS, 3) qk_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(32 * RWARPS, 4) qk_rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) float2 cs[RD / 2];
     __shared__ __align__(16) float row[HOW == 2 ? 2 * RWARPS : 1][RD];
     const int t = blockIdx.x, l = threadIdx.x & 15, h0 = threadIdx.x >> 4, step = blockDim.x >> 4;

@@ -22,8 +22,9 @@
 // are in flight while the row before is worked on, and stays in registers (KEPT groups of four values a thread; what a
 // row has beyond that is read again).  The CTAs send each other maximum and sum by st.async on a barrier in shared
 // memory; a cluster barrier would wait for the stores of the row's probabilities as well.  A wait that runs out (it
-// needs a CTA of the cluster to stop) gives NaN.  289 rows of 129280: 68 us, 4.4 TB/s (a cluster per
-// row, without copies ahead: 87 us; taking rows in turn with a cluster barrier: 104 us); one row of 129280: 6.1 us.  Each row has one
+// needs a CTA of the cluster to stop) gives NaN.  289 rows of 129280: 67.7 us, 4.4 TB/s (a cluster per
+// row, without copies ahead: 87 us; taking rows in turn with a cluster barrier: 104 us); one row of 129280: 6.3 us.
+// Clusters of eight CTAs of which two share an SM stay on 132 of 148 SMs.  Each row has one
 // serial exchange through the cluster between its loads and its stores; that is what is left.
 //
 // spec_verify: p and q of all drafted tokens are looked up at once before the walk, so an accepted node costs no memory
@@ -48,7 +49,7 @@ constexpr int CLUSTER_MAX = 8;
 
 // ------------------------------------------------------------------ probabilities
 
-constexpr int PT = 1024, PWARPS = PT / 32;
+constexpr int PT = 512, PWARPS = PT / 32;
 
 // values of a row per CTA of its cluster
 __host__ __device__ inline int row_share(int V, int C) { return ((V + C - 1) / C + 3) & ~3; }
@@ -142,7 +143,7 @@ __device__ __forceinline__ Part join_lanes(Part a, int width, const ProbsParams&
 // in flight while this row is worked on, its sums come together and its probabilities are written.
 // KEPT: groups of four values a thread keeps; the rest of a long row is read again.
 template <bool VEC, int KEPT>
-__global__ void __launch_bounds__(PT) token_probs_kernel(const __grid_constant__ ProbsParams p) {
+__global__ void __launch_bounds__(PT, 2) token_probs_kernel(const __grid_constant__ ProbsParams p) {
     extern __shared__ __align__(16) float4 held[];   // [KEPT][PT]
     __shared__ float wm[PWARPS];
     __shared__ double ws[PWARPS], parts[2][2 * CLUSTER_MAX];   // parts: every CTA's maximum and sum of a row
