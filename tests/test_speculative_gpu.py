@@ -42,6 +42,7 @@ def f32(rng, *shape):
 @pytest.mark.parametrize("T,hq,hk,rot,inter,norm", [
     (1, 10, 10, 128, False, False), (1, 10, 10, 128, True, True), (3, 20, 5, 64, False, True), (7, 1, 1, 34, False, True),
     (2, 3, 0, 2, True, False), (33, 128, 2, 96, True, True), (130, 11, 7, 126, False, False),
+    (5, 3, 2, 96, False, True), (4, 2, 1, 8, False, False), (9, 40, 8, 120, False, True), (3, 2, 2, 2, False, True),
 ])
 def test_rope(T, hq, hk, rot, inter, norm):
     rng = np.random.default_rng(T * 100 + hq)
@@ -417,7 +418,8 @@ def test_a_scale_that_is_no_number_reaches_those_who_see_it_alone(cap, int4, wha
 # ---------------------------------------------------------------- probabilities
 
 @pytest.mark.parametrize("T,V,temp", [(1, 1, 1.0), (2, 5, 0.5), (3, 1023, 1.0), (1, 4096, 0.7), (5, 32001, 1.3),
-                                      (2, 129280, 0.3), (1, 300007, 1.0), (150, 1000, 1.0)])
+                                      (2, 129280, 0.3), (1, 300007, 1.0), (150, 1000, 1.0), (3, 33333, 1.0), (5, 129281, 0.8),
+                                      (150, 1001, 1.0), (40, 16382, 1.0), (40, 16385, 1.0), (2, 131071, 1.0), (7, 2, 1.0)])
 def test_probs(T, V, temp):
     rng = np.random.default_rng(T + V)
     x = f32(rng, T, V) * 4
@@ -444,6 +446,12 @@ def test_probs_in_place_rows_without_a_finite_maximum_and_alignment():
     flat[1:] = dev(f32(rng, 1500))
     y = api.focr_token_probs(flat[1:].view(3, 500)).cpu().numpy()
     np.testing.assert_allclose(y, sp.token_probs(flat[1:].view(3, 500).cpu().numpy()), rtol=3e-6)
+    for shift in (0, 1, 2, 3):                               # outputs aligned unlike the logits, and nothing beside them written
+        out = torch.full((4 + 3 * 500,), 7.0, device="cuda")
+        api.focr_token_probs(flat[1:].view(3, 500), out=out[shift:shift + 1500].view(3, 500))
+        got = out.cpu().numpy()
+        np.testing.assert_allclose(got[shift:shift + 1500].reshape(3, 500), y, rtol=1e-6)
+        assert (got[:shift] == 7).all() and (got[shift + 1500:] == 7).all()
 
 
 # ---------------------------------------------------------------- verification

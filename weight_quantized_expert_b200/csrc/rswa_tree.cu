@@ -94,7 +94,8 @@ __device__ __forceinline__ void load_scales(uint32_t dst, const float* src, int 
     cp4(dst + 4 * r, src + min(r, rows - 1));
 }
 
-// W16: more than eight columns, so both row halves of the MMA tiles are used.
+// W16: more than eight columns, so both row halves of the MMA tiles are used (8 x 10 x 8 nodes over 289 rows without it 10.7
+// us, with it 11.4; over 32768 rows, in ranges, 98 and 111).
 template <bool INT4, bool W16>
 __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant__ TreeParams p) {
     extern __shared__ __align__(128) uint8_t smem[];

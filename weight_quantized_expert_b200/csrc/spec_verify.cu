@@ -75,51 +75,61 @@ __device__ __forceinline__ float expo(float x, float base, const ProbsParams& p)
     return y;
 }
 
-// Group g of a thread: values 4 g' .. 4 g' + 3 (VEC: rows are 16-byte aligned) or four values PT apart.
-template <bool VEC>
-__device__ __forceinline__ float4 get4(const float* x, int g, int tid, int n, float none) {
-    if (VEC) {
-        const int i = 4 * (g * PT + tid);
-        return i < n ? *reinterpret_cast<const float4*>(x + i) : make_float4(none, none, none, none);
+// How a thread's group of four values lies: FAR, PT values apart (logits and probabilities aligned differently); NEAR, 16
+// aligned bytes, all inside the row's part x[0 .. n - 1] or all outside; SKEW, the same with groups that begin `skew` (0 .. 3)
+// values ahead of the part, so the ones at its ends are taken value by value.  289 x 129281: SKEW 68 us, FAR 106; 289 x
+// 129280: NEAR 67.0, SKEW 69.7.
+enum { FAR, NEAR, SKEW };
+template <int VEC>
+__device__ __forceinline__ int first_of(int g, int tid, int skew) { return VEC == FAR ? 4 * g * PT + tid : 4 * (g * PT + tid) - skew; }
+template <int VEC>
+__device__ __forceinline__ bool whole(int i, int n) { return VEC == NEAR ? i < n : VEC == SKEW && i >= 0 && i + 3 < n; }
+template <int VEC>
+__device__ __forceinline__ float4 get4(const float* x, int g, int tid, int n, int skew, float none) {
+    const int i = first_of<VEC>(g, tid, skew);
+    if (whole<VEC>(i, n)) return *reinterpret_cast<const float4*>(x + i);
+    if (VEC == NEAR) return make_float4(none, none, none, none);
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int at = i + j * (VEC == FAR ? PT : 1);
+        v[j] = at >= 0 && at < n ? x[at] : none;
     }
-    const int i = 4 * g * PT + tid;
-    return make_float4(i < n ? x[i] : none, i + PT < n ? x[i + PT] : none, i + 2 * PT < n ? x[i + 2 * PT] : none,
-                       i + 3 * PT < n ? x[i + 3 * PT] : none);
+    return make_float4(v[0], v[1], v[2], v[3]);
 }
-template <bool VEC>
-__device__ __forceinline__ void put4(float* y, int g, int tid, int n, float4 v) {
-    if (VEC) {
-        const int i = 4 * (g * PT + tid);
-        if (i < n) *reinterpret_cast<float4*>(y + i) = v;
+template <int VEC>
+__device__ __forceinline__ void put4(float* y, int g, int tid, int n, int skew, float4 v) {
+    const int i = first_of<VEC>(g, tid, skew);
+    if (whole<VEC>(i, n)) {
+        *reinterpret_cast<float4*>(y + i) = v;
         return;
     }
-    const int i = 4 * g * PT + tid;
-    if (i < n) y[i] = v.x;
-    if (i + PT < n) y[i + PT] = v.y;
-    if (i + 2 * PT < n) y[i + 2 * PT] = v.z;
-    if (i + 3 * PT < n) y[i + 3 * PT] = v.w;
+    if (VEC == NEAR) return;
+    const float o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int at = i + j * (VEC == FAR ? PT : 1);
+        if (at >= 0 && at < n) y[at] = o[j];
+    }
 }
 __device__ __forceinline__ float max4(float m, float4 v) { return fmaxf(fmaxf(m, fmaxf(v.x, v.y)), fmaxf(v.z, v.w)); }
 
-// Starts the copy of group g into its place in shared memory (values past n become -inf).  A thread reads back only
-// what it copied itself, so waiting for its own copies is enough.
-template <bool VEC>
-__device__ __forceinline__ void fetch4(float4* held, const float* x, int g, int tid, int n) {
+// Starts the copy of group g into its place in shared memory (values outside the part become -inf).  A thread reads back
+// only what it copied itself, so waiting for its own copies is enough.
+template <int VEC>
+__device__ __forceinline__ void fetch4(float4* held, const float* x, int g, int tid, int n, int skew) {
     float4* at = held + g * PT + tid;
     const uint32_t dst = smem_u32(at);
-    if (VEC) {
-        const int i = 4 * (g * PT + tid);
-        if (i < n)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(x + i) : "memory");
-        else
-            *at = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    const int i = first_of<VEC>(g, tid, skew);
+    if (whole<VEC>(i, n)) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(x + i) : "memory");
         return;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int i = (4 * g + j) * PT + tid;
-        if (i < n)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * j), "l"(x + i) : "memory");
+        const int k = i + j * (VEC == FAR ? PT : 1);
+        if (VEC != NEAR && k >= 0 && k < n)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + 4 * j), "l"(x + k) : "memory");
         else
             reinterpret_cast<float*>(at)[j] = -INFINITY;
     }
@@ -142,7 +152,7 @@ __device__ __forceinline__ Part join_lanes(Part a, int width, const ProbsParams&
 // A cluster takes rows in turn: a row's part goes from shared memory to registers, the next row's copies start, and are
 // in flight while this row is worked on, its sums come together and its probabilities are written.
 // KEPT: groups of four values a thread keeps; the rest of a long row is read again.
-template <bool VEC, int KEPT>
+template <int VEC, int KEPT>
 __global__ void __launch_bounds__(PT, 2) token_probs_kernel(const __grid_constant__ ProbsParams p) {
     extern __shared__ __align__(16) float4 held[];   // [KEPT][PT]
     __shared__ float wm[PWARPS];
@@ -151,12 +161,13 @@ __global__ void __launch_bounds__(PT, 2) token_probs_kernel(const __grid_constan
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = p.C > 1 ? (int)cluster_rank() : 0, rows = gridDim.x / p.C;
     const int share = row_share(p.V, p.C), first = min(p.V, rank * share), n = min(share, p.V - first);
-    const int groups = (n + 4 * PT - 1) / (4 * PT);
     int row = blockIdx.x / p.C, turn = 0, phase = 0;
     pdl_wait();
+    auto part = [&](int r) { return p.logits + (size_t)r * p.V + first; };
+    auto skew_of = [](const float* x) { return VEC == SKEW ? (int)((uintptr_t)x / 4 % 4) : 0; };
     auto fetch = [&](int r) {
 #pragma unroll
-        for (int g = 0; g < KEPT; ++g) fetch4<VEC>(held, p.logits + (size_t)r * p.V + first, g, tid, n);
+        for (int g = 0; g < KEPT; ++g) fetch4<VEC>(held, part(r), g, tid, n, skew_of(part(r)));
     };
     fetch(row);
     if (p.C > 1) {
@@ -168,7 +179,8 @@ __global__ void __launch_bounds__(PT, 2) token_probs_kernel(const __grid_constan
         cluster_sync();
     }
     for (; row < p.T; row += rows, phase ^= turn, turn ^= 1) {
-        const float* x = p.logits + (size_t)row * p.V + first;
+        const float* x = part(row);
+        const int skew = skew_of(x), groups = (n + skew + 4 * PT - 1) / (4 * PT);
         float* y = p.probs + (size_t)row * p.V + first;
         asm volatile("cp.async.wait_all;" ::: "memory");
         float4 v[KEPT];
@@ -179,7 +191,7 @@ __global__ void __launch_bounds__(PT, 2) token_probs_kernel(const __grid_constan
         Part a{-INFINITY, 0.};
 #pragma unroll
         for (int g = 0; g < KEPT; ++g) a.m = max4(a.m, v[g]);
-        for (int g = KEPT; g < groups; ++g) a.m = max4(a.m, get4<VEC>(x, g, tid, n, -INFINITY));
+        for (int g = KEPT; g < groups; ++g) a.m = max4(a.m, get4<VEC>(x, g, tid, n, skew, -INFINITY));
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) a.m = fmaxf(a.m, __shfl_xor_sync(0xffffffffu, a.m, o));
         const float base = base_of(a.m);
@@ -189,7 +201,7 @@ __global__ void __launch_bounds__(PT, 2) token_probs_kernel(const __grid_constan
             a.s += (double)((v[g].x + v[g].y) + (v[g].z + v[g].w));
         }
         for (int g = KEPT; g < groups; ++g) {
-            const float4 t = get4<VEC>(x, g, tid, n, -INFINITY);
+            const float4 t = get4<VEC>(x, g, tid, n, skew, -INFINITY);
             a.s += (double)((expo(t.x, base, p) + expo(t.y, base, p)) + (expo(t.z, base, p) + expo(t.w, base, p)));
         }
 #pragma unroll
@@ -222,15 +234,15 @@ __global__ void __launch_bounds__(PT, 2) token_probs_kernel(const __grid_constan
         // a row of -inf alone has no distribution (and a wait that ran out gives no numbers)
         const float f = a.m == -INFINITY || !arrived ? __int_as_float(0x7fc00000) : expo(base, a.m, p) / (float)a.s;
 #pragma unroll
-        for (int g = 0; g < KEPT; ++g) put4<VEC>(y, g, tid, n, make_float4(v[g].x * f, v[g].y * f, v[g].z * f, v[g].w * f));
+        for (int g = 0; g < KEPT; ++g) put4<VEC>(y, g, tid, n, skew, make_float4(v[g].x * f, v[g].y * f, v[g].z * f, v[g].w * f));
         for (int g = KEPT; g < groups; ++g) {
-            const float4 t = get4<VEC>(x, g, tid, n, -INFINITY);
-            put4<VEC>(y, g, tid, n, make_float4(expo(t.x, base, p) * f, expo(t.y, base, p) * f, expo(t.z, base, p) * f, expo(t.w, base, p) * f));
+            const float4 t = get4<VEC>(x, g, tid, n, skew, -INFINITY);
+            put4<VEC>(y, g, tid, n, skew, make_float4(expo(t.x, base, p) * f, expo(t.y, base, p) * f, expo(t.z, base, p) * f, expo(t.w, base, p) * f));
         }
     }
 }
 
-template <bool VEC, int KEPT>
+template <int VEC, int KEPT>
 cudaError_t launch_probs(ProbsParams& p, cudaStream_t st) {
     const void* fn = (const void*)token_probs_kernel<VEC, KEPT>;
     const size_t smem = (size_t)KEPT * PT * 16;
@@ -255,6 +267,11 @@ cudaError_t launch_probs(ProbsParams& p, cudaStream_t st) {
     }
     void* args[] = {&p};
     return launch_kernel(fn, dim3((unsigned)(rows * p.C)), dim3(PT), smem, p.C, args, st);
+}
+
+template <int VEC>
+cudaError_t launch_groups(ProbsParams& p, int groups, cudaStream_t st) {
+    return groups <= 1 ? launch_probs<VEC, 1>(p, st) : groups <= 4 ? launch_probs<VEC, 4>(p, st) : launch_probs<VEC, 8>(p, st);
 }
 
 // ------------------------------------------------------------------ verification
@@ -543,12 +560,11 @@ focr_status focr_token_probs(const float* logits, int32_t T, int32_t V, float te
     p.C = row_cluster(T, V, 4 * PT * 8, 4 * PT);
     const double scale = 1.4426950408889634 / (double)temperature;
     p.scale = (float)scale, p.scale_lo = (float)(scale - (double)p.scale);
-    const bool vec = V % 4 == 0 && !misaligned(logits, 16) && !misaligned(probs, 16);
-    const int groups = (row_share(V, p.C) + 4 * PT - 1) / (4 * PT);
+    const bool even = ((uintptr_t)logits - (uintptr_t)probs) % 16 == 0, aligned = even && V % 4 == 0 && !misaligned(logits, 16);
+    // as few kept groups as hold a row's part: 289 x 2000 with 1 / 8 of them 3.0 / 5.6 us, 289 x 8000 with 4 / 8 5.0 / 6.3
+    const int groups = (row_share(V, p.C) + (even && !aligned ? 3 : 0) + 4 * PT - 1) / (4 * PT);
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = groups <= 1   ? (vec ? launch_probs<true, 1>(p, st) : launch_probs<false, 1>(p, st))
-                          : groups <= 4 ? (vec ? launch_probs<true, 4>(p, st) : launch_probs<false, 4>(p, st))
-                                        : (vec ? launch_probs<true, 8>(p, st) : launch_probs<false, 8>(p, st));
+    const cudaError_t e = aligned ? launch_groups<NEAR>(p, groups, st) : even ? launch_groups<SKEW>(p, groups, st) : launch_groups<FAR>(p, groups, st);
     return report_launch(e, "token_probs_kernel");
 }
 
