@@ -27,7 +27,7 @@ namespace {
 
 constexpr int RD = TREE_DIM, RW = TREE_RING;
 constexpr int WARPS = 4, PT = 32 * WARPS, TPC = PT / COLS;   // TPC: threads that prepare a column
-constexpr int JT = 128, JCOLS = 4;              // threads and columns of a CTA of the joining kernel
+constexpr int JCOLS = 4;                        // columns of a CTA of the joining kernel
 
 // A partial result: 16 columns' maxima, sums and unnormalised outputs.
 constexpr int PART_L = COLS, PART_O = 2 * COLS, PART_FLOATS = 2 * COLS + COLS * RD;
@@ -519,10 +519,15 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
     }
 }
 
-// Joins the partial results of the units that the ranges' cuts divide, JCOLS columns a CTA.  Everything but the partial
-// results themselves was there before the kernel in front of this one began, so it is read ahead of the wait.
-__global__ void __launch_bounds__(JT) rswa_ranges_join_kernel(const __grid_constant__ TreeParams p, int ctas) {
+// Joins the partial results of the units that the ranges' cuts divide, JCOLS columns a CTA; its JG groups of 128 threads
+// take the parts in turn (a unit of a small call may have hundreds: 1 x 10 heads x 1 node over 26000 rows, 296 parts in all,
+// with 1 / 4 groups 34 / 22 us; 320 units of two or three parts 73 / 82 us).  Everything but the partial results themselves was there before the
+// kernel in front of this one began, so it is read ahead of the wait.
+template <int JG>
+__global__ void __launch_bounds__(JG * RD) rswa_ranges_join_kernel(const __grid_constant__ TreeParams p, int ctas) {
+    constexpr int JT = JG * RD;
     __shared__ int scan[JT / 32 + 4];
+    __shared__ float gm[JG][JCOLS], gl[JG][JCOLS], go[JG][JCOLS][RD];
     const int tid = threadIdx.x, per_b = p.hk * p.groups, b = blockIdx.x / per_b, unit = blockIdx.x % per_b;
     int all = 0, before = 0;
     for (int i = tid; i < p.B; i += JT) {
@@ -543,27 +548,42 @@ __global__ void __launch_bounds__(JT) rswa_ranges_join_kernel(const __grid_const
     pdl_wait();
     if (bad || c0 == c1) return;
     const int h = unit / p.groups, col0 = unit % p.groups * COLS, first = blockIdx.y * JCOLS;
+    const int group = tid / RD, d = tid % RD;
     float M[JCOLS], l[JCOLS], o[JCOLS];
 #pragma unroll
     for (int j = 0; j < JCOLS; ++j) M[j] = NONE, l[j] = o[j] = 0.f;
+    auto add = [&](int j, float m, float lp, float op) {
+        const float mn = fmaxf(M[j], m), f = ex2(M[j] - mn), g = ex2(m - mn);
+        M[j] = mn, l[j] = fmaf(g, lp, f * l[j]), o[j] = fmaf(g, op, f * o[j]);
+    };
 #pragma unroll 2
-    for (int c = c0; c <= c1; ++c) {
+    for (int c = c0 + group; c <= c1; c += JG) {
         const float* part = p.part + ((size_t)c * 2 + (c == c0)) * PART_FLOATS;
         float m[JCOLS], lp[JCOLS], op[JCOLS];   // (columns behind the unit's last hold anything, and go nowhere)
 #pragma unroll
         for (int j = 0; j < JCOLS; ++j)
-            m[j] = __ldcg(part + first + j), lp[j] = __ldcg(part + PART_L + first + j), op[j] = __ldcg(part + PART_O + (first + j) * RD + tid);
+            m[j] = __ldcg(part + first + j), lp[j] = __ldcg(part + PART_L + first + j), op[j] = __ldcg(part + PART_O + (first + j) * RD + d);
+#pragma unroll
+        for (int j = 0; j < JCOLS; ++j) add(j, m[j], lp[j], op[j]);
+    }
+    if (JG > 1) {
 #pragma unroll
         for (int j = 0; j < JCOLS; ++j) {
-            const float mn = fmaxf(M[j], m[j]), f = ex2(M[j] - mn), g = ex2(m[j] - mn);
-            M[j] = mn, l[j] = fmaf(g, lp[j], f * l[j]), o[j] = fmaf(g, op[j], f * o[j]);
+            go[group][j][d] = o[j];
+            if (d == 0) gm[group][j] = M[j], gl[group][j] = l[j];
         }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g = 1; g < JG; ++g)
+#pragma unroll
+            for (int j = 0; j < JCOLS; ++j) add(j, gm[g][j], gl[g][j], go[g][j][d]);
     }
 #pragma unroll
     for (int j = 0; j < JCOLS; ++j) {
         const int col = col0 + first + j, node = col / p.G;
         if (first + j < COLS && col < p.N * p.G && node < L)
-            p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + col % p.G) * RD + tid] = o[j] / l[j];
+            p.out[(((size_t)b * p.N + node) * p.hq + h * p.G + col % p.G) * RD + d] = o[j] / l[j];
     }
 }
 
@@ -581,8 +601,10 @@ cudaError_t launch_as(TreeParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     void* more[] = {&p, &ctas};
     const int cols = p.N * p.G < COLS ? p.N * p.G : COLS;
-    return launch_kernel((const void*)rswa_ranges_join_kernel, dim3((unsigned)p.B * p.hk * p.groups, (cols + JCOLS - 1) / JCOLS), dim3(JT), 0, 1,
-                         more, st);
+    const unsigned units = (unsigned)p.B * p.hk * p.groups;
+    const bool few = units < (unsigned)ctas / 4;
+    return launch_kernel(few ? (const void*)rswa_ranges_join_kernel<4> : (const void*)rswa_ranges_join_kernel<1>,
+                         dim3(units, (cols + JCOLS - 1) / JCOLS), dim3(few ? 4 * RD : RD), 0, 1, more, st);
 }
 
 }  // namespace
