@@ -469,11 +469,12 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
 
 // How a call is split, from its sizes alone: a cluster for each unit, of as many CTAs as give every pair of warps a block
 // and the device no more than two CTAs per SM; or ranges (rswa_ranges.cu), which use the whole device whatever the units
-// are, but cost a second kernel and longer beginnings.  Clusters are taken up to 12 blocks a pair while they leave at most
-// one CTA to an SM, else up to 4.  Measured, clusters against ranges (us, int8): 1 sequence x 10 heads x 1 node over 8000
-// / 16000 / 24000 rows (4, 8, 12 blocks a pair) 13.9 / 22.7 / 31.4 against 25.9 / 30.5 / 34.5; 3 x 10 x 4 over 12000
-// rows (12) 25.7 against 30.4; 8 x 10 x 16 over 896 / 1792 rows (2, 4 blocks; 160 CTAs) 16.7 / 22.6 against 20.0 / 23.8;
-// 32 x 10 x 14 over 896 rows (4; 320 CTAs) 34.9 against 34.1.
+// are, but cost a second kernel and longer beginnings.  Clusters are taken up to 6 blocks a pair while they leave at most
+// one CTA to an SM, else up to 4.  Measured, clusters against ranges (us, int8): 1 sequence x 10 heads x 1 node over 3900
+// / 8000 / 12000 rows (2, 4, 6 blocks a pair) 9.5 / 14.0 / 18.3 against 12.7 / 14.8 / 16.5; 1 x 10 x 16 nodes over 8000 /
+// 12000 rows 17.5 / 22.6 against 20.7 / 22.0; 3 x 10 x 4 over 3000 / 8000 rows (3, 8) 13.5 / 20.9 against 14.8 / 20.0;
+// 8 x 10 x 16 over 896 / 1792 rows (2, 4 blocks; 160 CTAs) 16.7 / 22.6 against 20.0 / 23.8; 32 x 10 x 14 over 896 rows
+// (4; 320 CTAs) 34.9 against 34.1.
 struct TreePlan {
     int groups, S;
     bool ranges;
@@ -487,7 +488,7 @@ TreePlan tree_plan(int B, int N, int heads_q, int heads, int cap) {
     pl.S = 1;
     while (pl.S < 8 && pl.S * PAIRS < blocks) pl.S *= 2;
     while (pl.S > 1 && units * pl.S > 2 * sms) pl.S /= 2;
-    pl.ranges = blocks > (units * pl.S > sms ? 4 : 12) * pl.S * PAIRS;
+    pl.ranges = blocks > (units * pl.S > sms ? 4 : 6) * pl.S * PAIRS;
     return pl;
 }
 
