@@ -640,3 +640,37 @@ def test_same_inputs_give_the_same_bits():
     p1, p2 = api.focr_token_probs(x), api.focr_token_probs(x)
     torch.cuda.synchronize()
     assert torch.equal(a, b) and torch.equal(p1, p2)
+
+
+def test_two_calls_of_each_operator_at_once():
+    import torch
+    rng = np.random.default_rng(61)
+    B, N, hk = 40, 3, 4
+
+    def job():
+        q, k, v = (dev(f32(rng, B, N, hk, 128)) for _ in range(3))
+        ref = wide_cache(np_cache(rng, B, hk, 200, False), 1100)        # ranges: a workspace
+        ring = dev_cache(np_cache(rng, B, hk, 128, False))
+        target, draft, tokens, parent, u = verify_case(rng, B, N, 20001)
+        return dict(q=q, k=k, v=v, ref=ref, ring=ring, n=ints(rng.integers(0, 300, B)), r=ints(rng.integers(0, 201, B)),
+                    pos=ints(rng.integers(0, 9999, B * N)), logits=dev(f32(rng, 9, 20001)), target=dev(target), draft=dev(draft),
+                    tokens=ints(tokens), parent=ints(parent), u=dev(u))
+
+    def run(j, stream=None):
+        s = dict(stream=stream)
+        rot = api.focr_qk_norm_rope(j["q"].view(B * N, hk, 128), j["k"].view(B * N, hk, 128), j["pos"], norm=True, **s)
+        out = api.focr_rswa_tree(j["q"], j["k"], j["v"], j["ref"], j["r"], j["ring"], j["n"], j["parent"], **s)
+        p = api.focr_token_probs(j["logits"], 0.9, **s)
+        ver = api.focr_spec_verify(j["target"], j["draft"], j["tokens"], j["parent"], None, j["u"], **s)
+        return [*rot, out, p, *ver]
+
+    jobs = [job() for _ in range(2)]
+    alone = [run(j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(5):
+        both = [run(j, s) for j, s in zip(jobs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
