@@ -1,4 +1,4 @@
-// Thread-block clusters: rank, barrier and reads of another CTA's shared memory.
+// Thread-block clusters: rank, barrier and stores into another CTA's shared memory.
 #pragma once
 
 #include "common.cuh"
@@ -16,20 +16,12 @@ __device__ __forceinline__ void cluster_sync() {
     cluster_arrive();
     cluster_wait();
 }
-// the value of the same variable in the shared memory of the cluster's CTA `rank`
-__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(p, rank)) : "memory");
-    return v;
-}
-__device__ __forceinline__ double ld_cluster(const double* p, uint32_t rank) {
-    double v;
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(mapa_shared(p, rank)) : "memory");
-    return v;
-}
 // writes the same variable in the shared memory of the cluster's CTA `rank`
 __device__ __forceinline__ void st_cluster(float* p, uint32_t rank, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(p, rank)), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster(double* p, uint32_t rank, double v) {
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(mapa_shared(p, rank)), "d"(v) : "memory");
 }
 
 }  // namespace focr

@@ -30,8 +30,8 @@
 // spec_verify: p and q of all drafted tokens are looked up at once before the walk, so an accepted node costs no memory
 // latency; a rejection is one pass over the rows, spread over the cluster's warps.  The tiles' sums stay in shared
 // memory and lead to the next token's tile without a second pass over the rows.  One tree of 4 nodes: 9.0 us; 32 trees
-// of 16 nodes, V = 129280: 25 us (with the warps' tiles summed a second time and the answer agreed on by two more
-// cluster barriers: 12.3 and 25.4 us).  What is left is the chain of passes: up to one per rejected sibling, each a
+// of 16 nodes, V = 129280: 24 us (with the warps' tiles summed a second time, the answer agreed on by two more cluster
+// barriers and sums fetched instead of stored: 12.3 and 25.4 us).  What is left is the chain of passes: up to one per rejected sibling, each a
 // cluster-wide sum.
 #include <math.h>
 
@@ -290,7 +290,7 @@ constexpr int TILES_MAX = (FOCR_V_MAX / TILE + CLUSTER_MAX - 1) / CLUSTER_MAX + 
 struct VerifyShared {
     double p[TREE_MAX], q[TREE_MAX], u[TREE_MAX + 1];   // of each node's token behind its parent
     int par[TREE_MAX], tok[TREE_MAX], gone[TREE_MAX];
-    double tile_sum[TILES_MAX], warp_sum[VWARPS], cta_sum[2];
+    double tile_sum[TILES_MAX], warp_sum[VWARPS], cta_sum[2][CLUSTER_MAX];
 };
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -383,12 +383,12 @@ __device__ double row_sum(const Residual& w, const VerifyParams& p, VerifyShared
 #pragma unroll
     for (int i = 0; i < VWARPS; ++i) total += sh.warp_sum[i];
     if (p.C == 1) return total;
-    // two places in turn: a CTA may write its next sum while another still reads this one
+    // into every CTA of the cluster; two places in turn: a CTA may store its next sum while another still reads this one
     turn ^= 1;
-    if (threadIdx.x == 0) sh.cta_sum[turn] = total;
+    if (threadIdx.x < p.C) st_cluster(&sh.cta_sum[turn][cluster_rank()], threadIdx.x, total);
     cluster_sync();
     total = 0.;
-    for (int r = 0; r < p.C; ++r) total += ld_cluster(&sh.cta_sum[turn], r);
+    for (int r = 0; r < p.C; ++r) total += sh.cta_sum[turn][r];
     return total;
 }
 
@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(VT, 2) spec_verify_kernel(const __grid_constan
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, N = p.N, V = p.V;
     const float *P = p.target + (size_t)b * (N + 1) * V, *Q = p.draft ? p.draft + (size_t)b * N * V : nullptr;
     pdl_wait();
+    if (p.C > 1) cluster_arrive();
     // every node's parent, token and uniform at once, then p and q of its token behind its parent
     const int L = p.n_nodes ? __ldg(p.n_nodes + b) : N;
     bool wrong = L < 0 || L > N;
@@ -418,7 +419,9 @@ __global__ void __launch_bounds__(VT, 2) spec_verify_kernel(const __grid_constan
     }
     if (tid == TREE_MAX) sh.u[TREE_MAX] = (double)__ldg(p.u + (size_t)b * (N + 1) + N);
     int32_t* path = p.path + (size_t)b * N;
-    if (__syncthreads_or(wrong)) {   // the whole cluster sees the same
+    const bool any_wrong = __syncthreads_or(wrong);   // the whole cluster sees the same
+    if (p.C > 1) cluster_wait();                      // every CTA of the cluster runs: its shared memory may be written
+    if (any_wrong) {
         if (rank == 0) {
             if (tid < N) path[tid] = -1;
             if (tid == 0) p.n_accept[b] = p.next[b] = -1;
@@ -476,10 +479,7 @@ __global__ void __launch_bounds__(VT, 2) spec_verify_kernel(const __grid_constan
     double before = 0., after;
     {
         double base = 0., sum = 0.;
-        if (p.C > 1) {
-            for (int r = 0; r < rank; ++r) base += ld_cluster(&sh.cta_sum[turn], r);
-            cluster_arrive();   // waited for before the CTA leaves
-        }
+        for (int r = 0; r < rank; ++r) base += sh.cta_sum[turn][r];
         for (int i = 0; i < warp; ++i) sum += sh.warp_sum[i];
         before = base + sum, after = base + (sum + sh.warp_sum[warp]);
     }
@@ -527,7 +527,6 @@ __global__ void __launch_bounds__(VT, 2) spec_verify_kernel(const __grid_constan
         }
         if (lane == 0) p.next[b] = found < 0 ? V - 1 : found;
     }
-    if (p.C > 1) cluster_wait();
 }
 
 // CTAs of a row of V values: at most `most` values each, and smaller parts while the device is not full
