@@ -469,7 +469,7 @@ focr_status focr_qk_norm_rope(const float* q, int64_t ldq, int32_t heads_q, cons
  *   k, v: DEVICE codes [B][heads][cap][128] int8 (FOCR_W_INT8), or [B][heads][cap][64] bytes of two nibbles
  *     (FOCR_W_INT4; element 2j in bits 0-3, 2j + 1 in bits 4-7), 16-byte aligned;
  *   k_scale, v_scale: DEVICE fp32 [B][heads][cap].
- *   A row's values are scale * code.  1 <= B <= FOCR_RSWA_B_MAX, heads <= FOCR_HEADS_MAX, cap <= FOCR_RSWA_RCAP_MAX.
+ *   A row's values are scale * code; a scale is not negative.  1 <= B <= FOCR_RSWA_B_MAX, heads <= FOCR_HEADS_MAX, cap <= FOCR_RSWA_RCAP_MAX.
  */
 typedef struct focr_kv_cache {
     void* k;
@@ -517,7 +517,8 @@ focr_status focr_kv_read(const focr_kv_cache* c, const int32_t* len, float* k_ou
  *   q, out: DEVICE fp32 [B][N][heads_q][128]; k_new, v_new: DEVICE fp32 [B][N][heads][128] (heads of the caches),
  *   finite for live nodes; 16-byte aligned.  parent: DEVICE int32 [B][N] or NULL (a chain: parent of i is i - 1).
  *   n_nodes: DEVICE int32 [B] or NULL (N each).  ref_len, n_gen: DEVICE int32 [B].
- *   ref and ring: caches of B sequences, the same heads and type; ring->cap = 128.
+ *   ref and ring: caches of B sequences, the same heads and type; ring->cap = 128.  Rows that a node does not see may
+ *   hold anything: a scale that is NaN or infinite reaches the nodes that see its row and no other.
  *   1 <= N, N * heads_q / heads <= FOCR_TREE_NODES_MAX.
  *   Rows of nodes >= n_nodes[b] are left as they were.  A sequence with ref_len outside [0, ref->cap], n_gen < 0,
  *   n_nodes outside [0, N] or a bad parent of a live node gets NaN (in all N rows if n_nodes is the bad value).
