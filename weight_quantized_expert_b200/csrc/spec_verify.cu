@@ -139,12 +139,14 @@ struct Part {   // maximum of some logits and the sum of their exponentials rela
     float m;
     double s;
 };
-__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }   // masked logits alone sum to 0
-// Joins the parts of `width` neighbouring lanes, in every one of them.
+// A part without a finite logit has maximum -inf and sum 0 (NaN, should it hold one), taken relative to 0.
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+// Joins the parts of `width` neighbouring lanes, in every one of them.  A part that sums to 0 adds nothing: its base of 0 may
+// lie so far above the others' maximum that the factor is infinite.
 __device__ __forceinline__ Part join_lanes(Part a, int width, const ProbsParams& p) {
     float M = a.m;
     for (int o = width / 2; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    double s = a.s * (double)expo(base_of(a.m), base_of(M), p);
+    double s = a.s == 0. ? 0. : a.s * (double)expo(base_of(a.m), base_of(M), p);
     for (int o = width / 2; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return {M, s};
 }
@@ -195,6 +197,7 @@ __global__ void __launch_bounds__(PT, 2) token_probs_kernel(const __grid_constan
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) a.m = fmaxf(a.m, __shfl_xor_sync(0xffffffffu, a.m, o));
         const float base = base_of(a.m);
+        const bool masked = a.m == -INFINITY;   // none of the warp's values is finite: all of its exponentials are 0
 #pragma unroll
         for (int g = 0; g < KEPT; ++g) {
             v[g] = make_float4(expo(v[g].x, base, p), expo(v[g].y, base, p), expo(v[g].z, base, p), expo(v[g].w, base, p));
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(PT, 2) token_probs_kernel(const __grid_constan
         const int from = 2 * (lane & (p.C - 1));
         a = join_lanes({(float)parts[turn][from], parts[turn][from + 1]}, p.C, p);
         // a row of -inf alone has no distribution (and a wait that ran out gives no numbers)
-        const float f = a.m == -INFINITY || !arrived ? __int_as_float(0x7fc00000) : expo(base, a.m, p) / (float)a.s;
+        const float f = a.m == -INFINITY || !arrived ? __int_as_float(0x7fc00000) : expo(masked ? a.m : base, a.m, p) / (float)a.s;
 #pragma unroll
         for (int g = 0; g < KEPT; ++g) put4<VEC>(y, g, tid, n, skew, make_float4(v[g].x * f, v[g].y * f, v[g].z * f, v[g].w * f));
         for (int g = KEPT; g < groups; ++g) {
