@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from oracle import speculative as sp
-from test_speculative_gpu import U, dev, f32
+from test_speculative_gpu import MANY, TOL_TREE, U, dev, dev_cache, f32, ints, np_cache, wide_cache
 from weight_quantized_expert_b200 import api
 
 pytestmark = pytest.mark.gpu
@@ -63,3 +63,99 @@ def test_probs_stay_nan_where_a_row_has_no_distribution():
         x[3, 1] = np.nan
         got = api.focr_token_probs(dev(x), 0.5).cpu().numpy()
         assert np.isnan(got[[0, 1, 3]]).all() and np.isnan(got[2]).any()
+
+
+# ---------------------------------------------------------------- tree attention: what the weights are rounded against
+# check_tree's bar, with the largest value among the rows that a node itself sees: |err| <= TOL_TREE max|v seen|.
+
+def values_of(c):
+    return sp.values(c[0], c[1]), sp.values(c[2], c[3])
+
+
+CAPS = [300, MANY]                      # one launch; ranges
+LAYOUTS = [(2, 2), (8, 2)]              # up to eight columns of a unit, and more
+
+
+@pytest.mark.parametrize("hq,hk", LAYOUTS)
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("factor", [1e4, 1e8, 1e20, 1e30])
+def test_a_large_scale_reaches_the_nodes_that_see_its_row_alone(factor, int4, cap, hq, hk):
+    # a chain of three behind n = 200 tokens: token 72 is in the ring and seen by none, token 73 by the first node alone
+    rng = np.random.default_rng(71)
+    B, N, n, R = 3, 3, 200, 300
+    q, k, v = f32(rng, B, N, hq, 128), f32(rng, B, N, hk, 128), f32(rng, B, N, hk, 128)
+    ref, ring = np_cache(rng, B, hk, R, int4), np_cache(rng, B, hk, 128, int4)
+    ring[3][0, :, 72] *= np.float32(factor)
+    ring[3][1, :, 73] *= np.float32(factor)
+    ring[1][2, :, 72] *= np.float32(factor)
+    got = api.focr_rswa_tree(dev(q), dev(k), dev(v), wide_cache(ref, cap), ints([R] * B), dev_cache(ring), ints([n] * B)).cpu().numpy()
+    r, g = values_of(ref), values_of(ring)
+    want = sp.rswa_tree(q, k, v, r, [R] * B, g, [n] * B)
+    for b in range(B):
+        for i in range(N):
+            seen = [t % 128 for t in range(n + i - 127, n)]
+            vmax = max(np.abs(r[1][b]).max(), np.abs(g[1][b][:, seen]).max(), np.abs(v[b, :i + 1]).max())
+            assert np.abs(got[b, i] - want[b, i]).max() <= TOL_TREE * vmax, (b, i)
+
+
+@pytest.mark.parametrize("hq,hk", LAYOUTS)
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("factor", [1e4, 1e8])
+def test_a_large_value_of_no_weight_spares_the_others(factor, int4, cap, hq, hk):
+    # all queries lie near one direction, and row 10 against it: its score is about -68, its weight below e^-60
+    rng = np.random.default_rng(72)
+    B, N, n, R = 2, 3, 50, 300
+    way = f32(rng, 128)
+    q = way + 0.1 * f32(rng, B, N, hq, 128)
+    k, v = f32(rng, B, N, hk, 128), f32(rng, B, N, hk, 128)
+    rk, rv = f32(rng, B, hk, R, 128), f32(rng, B, hk, R, 128)
+    rk[:, :, 10] = -6 * way
+    ref = [*sp.quantise(rk, int4), *sp.quantise(rv, int4)]
+    ref[3][:, :, 10] *= np.float32(factor)
+    ring = np_cache(rng, B, hk, 128, int4)
+    got = api.focr_rswa_tree(dev(q.astype(np.float32)), dev(k), dev(v), wide_cache(ref, cap), ints([R] * B), dev_cache(ring), ints([n] * B)).cpu().numpy()
+    r, g = values_of(ref), values_of(ring)
+    want = sp.rswa_tree(q.astype(np.float32), k, v, r, [R] * B, g, [n] * B)
+    vmax = max(np.abs(np.delete(r[1], 10, 2)).max(), np.abs(g[1]).max(), np.abs(v).max())
+    assert np.abs(got - want).max() <= TOL_TREE * vmax
+
+
+@pytest.mark.parametrize("hq,hk", LAYOUTS)
+@pytest.mark.parametrize("R,cap", [(289, 300), (289, MANY), (4096, MANY)])
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("share,size", [(0.86, 0.1), (0.9, 0.1), (0.9, 0.01), (0.997, 0.003)])
+def test_a_key_with_most_of_the_weight_and_a_small_value(share, size, int4, R, cap, hq, hk):
+    """A sink.  All other keys have the same score, and all scores are whole numbers, so the bar, relative to an output's norm, is
+      digits   each product of a block is off by 0.29 steps of 2^-23 of the largest one (rms), and 64 of them by 8 times that:
+               2.8e-7 where the largest one carries the output (the sink's does here);
+      scores   the others' common weight is off, relative to the sink's, by the score in log2 x 4 roundings x ln 2 + 2^-22,
+               which moves the output by that times (the others' part of it + their share of the weight);
+      sums     fp32 roundings of the output and of the weights' sum: 14, and two for each of the blocks that a group of four
+               warps (or of the threads that join parts) adds in turn."""
+    rng = np.random.default_rng(73)
+    B, N, n, top = 1, 3, 64, 7 if int4 else 127
+    few = np.arange(16)                  # the dims in which the queries live: all keys but the sink are zero there
+    one = np.zeros(128, np.float32)
+    one[few] = rng.integers(-126, 127, 16)
+    one[3] = 127
+    q = np.broadcast_to(one, (B, N, hq, 128)).copy()
+    k, v = f32(rng, B, N, hk, 128), f32(rng, B, N, hk, 128)
+    k[..., few] = 0
+    rk, rv, gk, gv = (f32(rng, B, hk, rows, 128) for rows in (R, R, 128, 128))
+    rk[..., few] = gk[..., few] = 0
+    sink = R // 3
+    rk[:, :, sink] = top * np.sign(one)                # codes of +-top: the row's scale is set below
+    ref = [*sp.quantise(rk, int4), *sp.quantise(rv, int4)]
+    others = R - 1 + n + 2
+    ref[1][:, :, sink] = np.log(share / (1 - share) * others) * np.sqrt(128) / (top * np.abs(one).sum())
+    ref[3][:, :, sink] *= np.float32(size)
+    ring = [*sp.quantise(gk, int4), *sp.quantise(gv, int4)]
+    got = api.focr_rswa_tree(dev(q), dev(k), dev(v), wide_cache(ref, cap), ints([R] * B), dev_cache(ring), ints([n] * B)).cpu().numpy()
+    want = sp.rswa_tree(q, k, v, values_of(ref), [R] * B, values_of(ring), [n] * B)
+    norm = np.linalg.norm(want, axis=-1)
+    rest = np.linalg.norm(want - share * np.repeat(values_of(ref)[1][:, :, sink], hq // hk, 1)[:, None], axis=-1) / norm + 1 - share
+    score = np.log2(share / (1 - share) * others) * 4 * U * np.log(2) + 2.0**-22
+    bar = 2.8e-7 + score * rest + (14 + 2 * -(-(R + n) // 256)) * U
+    assert (np.linalg.norm(got - want, axis=-1) <= bar * norm).all(), (np.linalg.norm(got - want, axis=-1) / norm / bar).max()

@@ -314,7 +314,6 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const bool in = key + i < cur.rows;
-                        if (!in) vs[jj][i] = 0.f;
 #pragma unroll
                         for (int e = 0; e < HALVES; ++e) {
                             const bool seen = in && (cur.ring_slot < 0 || ((n - 1 - cur.ring_slot - key - i) & (RW - 1)) < ages[e]);
@@ -335,17 +334,9 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
             load_scales(st + St::VS, nxt.vs, nxt.rows, lane);
         }
         cp_commit();
-        // softmax of the block: weights relative to its largest score and value scale, as digits
-        float vmax = TINY;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) vmax = fmaxf(vmax, fmaxf(vs[j][0], vs[j][1]));
-        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-        const float vinv = P_TOP / vmax;
+        // softmax of the block; the products of weight and value scale as digits, relative to a column's largest one
         float alpha[HALVES], gain[HALVES];
         uint32_t pd[2][3][4];   // digits as A fragments: [32 keys][digit]
-#pragma unroll
-        for (int j = 0; j < 8; ++j) vs[j][0] *= vinv, vs[j][1] *= vinv;
 #pragma unroll
         for (int e = 0; e < HALVES; ++e) {
             float tm = T[0][2 * e];
@@ -354,18 +345,25 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
             tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
             tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
             const bool any = tm != -INFINITY;
-            // a little above the largest score, so that no rounding makes a weight larger than 1
-            const float mb = any ? fmaf(fabsf(tm * step[e]), 2.4e-7f, tm * step[e]) : 0.f;
-            float sum = 0.f;
-            uint32_t u[8][2];
+            const float mb = any ? tm * step[e] : 0.f;
+            float sum = 0.f, top = TINY;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float w = ex2(fmaf(T[j][2 * e + i], step[e], -mb));
                     sum += w;
-                    u[j][i] = __float_as_uint(fmaf(w, vs[j][i], P_MAGIC));
+                    T[j][2 * e + i] = w * vs[j][i];   // 0 for a key that the column does not see
+                    top = fmaxf(top, T[j][2 * e + i]);
                 }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float inv = P_TOP / top;
+            uint32_t u[8][2];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) u[j][i] = __float_as_uint(fmaf(T[j][2 * e + i], inv, P_MAGIC));
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
@@ -384,7 +382,7 @@ __global__ void __launch_bounds__(PT, 2) rswa_ranges_kernel(const __grid_constan
             alpha[e] = ex2(run_m[e] - mn);
             const float beta = any ? ex2(mb - mn) : 0.f;
             run_l[e] = run_l[e] * alpha[e] + beta * sum;
-            gain[e] = beta * vmax * ((INT4 ? 1.f / 16.f : 1.f) / P_TOP);
+            gain[e] = beta * top * ((INT4 ? 1.f / 16.f : 1.f) / P_TOP);
             run_m[e] = mn;
         }
         if (!W16) {

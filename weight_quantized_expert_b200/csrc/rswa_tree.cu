@@ -18,13 +18,17 @@
 //             with the key codes give the exact integer dot; the key's scale, the query's step and log2(e) / sqrt(128)
 //             follow in fp32.
 //   softmax   online over blocks of 64 keys, base 2.
-//   values    out needs sum_j e_j vs_j vc_j.  The weights of a block, relative to the block's largest score and
-//             largest value scale, are written as three unsigned digits (step 2^-23); the three integer sums over the
-//             64 keys are exact, join in fp32 and are added to the fp32 accumulator with the block's factor.
+//   values    out needs sum_j e_j vs_j vc_j.  A block's products of weight and value scale, e_j vs_j, are formed in fp32 and
+//             written as three unsigned digits relative to the column's largest one of the block (step 2^-23 of it), so
+//             keys that the column does not see, and large values of little weight, cost the others nothing; the three
+//             integer sums over the 64 keys are exact, join in fp32 and are added to the fp32 accumulator with the
+//             block's factor.  (One bound for all columns, largest weight x largest value scale: 1 to 3% faster, and
+//             wrong by any factor where the two belong to different keys.)
 //   No sum can wrap or leave a float's exact integers: |sum| <= 128 * 128 * 255 < 2^22, so accumulators start at the
 //   bit pattern of 1.5 * 2^23 and are read back as floats by one subtraction.
-// Against 64 bits the result is off by 3e-7 of its norm (fp32 matrix products and softmax: 2e-7 to 3e-6, growing with the
-// number of keys, which this does not).
+// Against 64 bits the result is off by 3e-7 of its norm for normal rows (fp32 matrix products and softmax: 2e-7 to 3e-6,
+// growing with the number of keys, which this does not).  Where the values cancel, the error is relative to the largest
+// product in a block, not to what is left of the sum.
 //
 // Work split: a unit is one kv head of one sequence with up to 16 columns; its keys are blocks of 64 (reference rows,
 // then the ring).  This kernel gives a unit to a cluster of S CTAs, which take its blocks in turn by pairs of warps, each
@@ -60,7 +64,7 @@ struct Shared {
     float got_m[COLS], got_l[COLS];
     float part_m[COLS], part_l[COLS];
     uint4 px[PAIRS][2][3][32];         // a pair's weight digits as A fragments: [32 keys][digit][lane]
-    float mx[PAIRS][2][COLS + 4];      // each warp's largest scores of a block, and its largest value scale
+    float2 mx[PAIRS][2][COLS];         // each warp's largest score of a block, and its largest product of weight and value scale
     float pair_m[PAIRS][COLS], warp_l[WARPS][COLS], pair_f[PAIRS + 1][COLS];   // f: a part's factor (the last: drafted keys)
     float step[COLS];                  // a score in units of log2 is (integer dot) * key scale * step
     int row[COLS];                     // a column's row of the output, -1 without a live node
@@ -253,7 +257,6 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const bool in = key + i < rows;
-                        if (!in) vs[jj][i] = 0.f;
 #pragma unroll
                         for (int e = 0; e < HALVES; ++e) {
                             const bool seen = in && (ring_slot < 0 || ((n - 1 - ring_slot - key - i) & (RW - 1)) < ages[e]);
@@ -268,45 +271,52 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
         const int next = blk + stride;
         if (next < nblk) fetch_k(next);
         cp_commit();
-        // softmax of the block: weights relative to its largest score and value scale, over both warps' keys
-        float vmax = TINY, tm[HALVES];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) vmax = fmaxf(vmax, fmaxf(vs[j][0], vs[j][1]));
-        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+        // softmax of the block: each warp's weights relative to its own largest score, then both warps' products of weight and
+        // value scale as digits, relative to a column's largest one of the block
+        float own[HALVES], sum[HALVES], top[HALVES];
 #pragma unroll
         for (int e = 0; e < HALVES; ++e) {
-            tm[e] = fmaxf(T[0][2 * e], T[0][2 * e + 1]);
+            float tm = fmaxf(T[0][2 * e], T[0][2 * e + 1]);
 #pragma unroll
-            for (int j = 1; j < 4; ++j) tm[e] = fmaxf(tm[e], fmaxf(T[j][2 * e], T[j][2 * e + 1]));
-            tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], 1));
-            tm[e] = fmaxf(tm[e], __shfl_xor_sync(0xffffffffu, tm[e], 2));
-            if (c == 0) sh.mx[pair][half][gr + 8 * e] = tm[e];
-        }
-        if (lane == 0) sh.mx[pair][half][COLS] = vmax;
-        named_bar_sync(1 + pair, 64);
-        vmax = fmaxf(vmax, sh.mx[pair][half ^ 1][COLS]);
-        const float vinv = P_TOP / vmax;
-        float alpha[HALVES], gain[HALVES];
-        uint32_t pd[3][4];   // digits of the warp's keys as an A fragment
-#pragma unroll
-        for (int j = 0; j < 4; ++j) vs[j][0] *= vinv, vs[j][1] *= vinv;
-#pragma unroll
-        for (int e = 0; e < HALVES; ++e) {
-            tm[e] = fmaxf(tm[e], sh.mx[pair][half ^ 1][gr + 8 * e]);
-            const bool any = tm[e] != -INFINITY;
-            // a little above the largest score, so that no rounding makes a weight larger than 1
-            const float mb = any ? fmaf(fabsf(tm[e] * step[e]), 2.4e-7f, tm[e] * step[e]) : 0.f;
-            float sum = 0.f;
-            uint32_t u[4][2];
+            for (int j = 1; j < 4; ++j) tm = fmaxf(tm, fmaxf(T[j][2 * e], T[j][2 * e + 1]));
+            tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
+            tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
+            const bool any = tm != -INFINITY;
+            const float mb = any ? tm * step[e] : 0.f;
+            own[e] = any ? mb : -INFINITY, sum[e] = 0.f, top[e] = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float w = ex2(fmaf(T[j][2 * e + i], step[e], -mb));
-                    sum += w;
-                    u[j][i] = __float_as_uint(fmaf(w, vs[j][i], P_MAGIC));
+                    sum[e] += w;
+                    T[j][2 * e + i] = w * vs[j][i];   // 0 for a key that the column does not see
+                    top[e] = fmaxf(top[e], T[j][2 * e + i]);
                 }
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) {
+                sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], o);
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
+            }
+            if (c == 0) sh.mx[pair][half][gr + 8 * e] = make_float2(own[e], top[e]);
+        }
+        named_bar_sync(1 + pair, 64);
+        float alpha[HALVES], gain[HALVES];
+        uint32_t pd[3][4];   // digits of the warp's keys as an A fragment
+#pragma unroll
+        for (int e = 0; e < HALVES; ++e) {
+            const float2 other = sh.mx[pair][half ^ 1][gr + 8 * e];
+            const float both = fmaxf(own[e], other.x);
+            const bool any = both != -INFINITY;
+            const float mb = any ? both : 0.f;
+            const float r = ex2(own[e] - mb);   // 0 for a warp whose keys the column does not see
+            const float most = fmaxf(fmaxf(top[e] * r, other.y * ex2(other.x - mb)), TINY);
+            const float f = r * (P_TOP / most);
+            uint32_t u[4][2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) u[j][i] = __float_as_uint(fmaf(T[j][2 * e + i], f, P_MAGIC));
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 const uint32_t t0 = __byte_perm(u[2 * g][0], u[2 * g][1], 0x5140), t1 = __byte_perm(u[2 * g + 1][0], u[2 * g + 1][1], 0x5140);
@@ -316,13 +326,11 @@ __global__ void __launch_bounds__(PT, 2) rswa_tree_kernel(const __grid_constant_
                 pd[1][2 * g + e] = __byte_perm(t0, t1, 0x7632);
                 pd[2][2 * g + e] = __byte_perm(t2, t3, 0x5410);
             }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             const float mn = any ? fmaxf(run_m[e], mb) : run_m[e];
             alpha[e] = ex2(run_m[e] - mn);
             const float beta = any ? ex2(mb - mn) : 0.f;
-            run_l[e] = run_l[e] * alpha[e] + beta * sum;
-            gain[e] = beta * vmax * ((INT4 ? 1.f / 16.f : 1.f) / P_TOP);
+            run_l[e] = run_l[e] * alpha[e] + beta * (r * sum[e]);
+            gain[e] = beta * most * ((INT4 ? 1.f / 16.f : 1.f) / P_TOP);
             run_m[e] = mn;
         }
 #pragma unroll

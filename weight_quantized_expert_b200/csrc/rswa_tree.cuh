@@ -17,8 +17,8 @@ __device__ __forceinline__ int part_at(int col, int dim) { return col * PAD + di
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float SCORE_SCALE = 0.08838834764831845f;   // 1 / sqrt(128)
 constexpr float Q_TOP = 8323072.f;              // 127 * 2^16: the largest fixed-point query value
-constexpr float P_TOP = 8388607.f;              // 2^23 - 1: the largest fixed-point weight
-constexpr float P_MAGIC = 8388608.f;            // 2^23: a weight added to it is rounded and lies in the low 23 bits
+constexpr float P_TOP = 8388604.f;              // 2^23 - 4: the largest fixed-point weight, before up to three roundings
+constexpr float P_MAGIC = 8388608.f;            // 2^23: a fixed-point weight added to it is rounded and lies in the low 23 bits
 constexpr float MAGIC = 12582912.f;             // 1.5 * 2^23
 constexpr int MAGIC_BITS = 0x4B400000;
 constexpr float NONE = -1e30f;                  // running maximum of a column that has seen no key
