@@ -483,7 +483,8 @@ typedef struct focr_kv_cache {
 /*
  * focr_kv_write -- quantise rows of K and V and write them into a cache.
  *   s = fp32(max|x|) / Q (one fp32 division; Q = 127 int8, 7 int4), q = round-half-even(fp32(x / s)) clamped to
- *   [-127, 127] or [-8, 7]; s = 0: q = 0.  Inputs must be finite.
+ *   [-127, 127] or [-8, 7]; s = 0: q = 0.  Inputs should be finite: a row that holds a NaN or an infinity gets a scale
+ *   of that kind and codes of 0, so it reads as NaN and focr_rswa_tree gives NaN to the nodes that see it.
  *   k, v: DEVICE fp32, row r at ptr + r * ld (ld in floats, >= heads * 128, a multiple of 4), 0 <= r < n_rows.
  *   For sequence b and i < count[b]: source row r = (row0 ? row0[b] : b * n_max) + (index ? index[b * n_max + i] : i)
  *   goes to slot start[b] + i, or (start[b] + i) mod cap with FOCR_KV_WRAP.  With more tokens than slots the last

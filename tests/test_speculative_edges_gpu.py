@@ -159,3 +159,34 @@ def test_a_key_with_most_of_the_weight_and_a_small_value(share, size, int4, R, c
     score = np.log2(share / (1 - share) * others) * 4 * U * np.log(2) + 2.0**-22
     bar = 2.8e-7 + score * rest + (14 + 2 * -(-(R + n) // 256)) * U
     assert (np.linalg.norm(got - want, axis=-1) <= bar * norm).all(), (np.linalg.norm(got - want, axis=-1) / norm / bar).max()
+
+
+# ---------------------------------------------------------------- cache writes
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("what", [np.nan, np.inf, -np.inf])
+def test_a_row_with_what_is_no_number_is_written_as_such(what, int4):
+    import torch
+    rng = np.random.default_rng(81)
+    rows, heads = 40, 2
+    k, v = f32(rng, rows, heads, 128), f32(rng, rows, heads, 128)
+    want = [np.zeros((1, heads, rows, 64 if int4 else 128), np.uint8 if int4 else np.int8), np.zeros((1, heads, rows), np.float32)] * 2
+    want = [x.copy() for x in want]
+    sp.kv_write(want, k, v, [rows], [0], n_max=rows)
+    for i, x, codes, scale in ((3, k, *want[:2]), (17, k, *want[:2]), (17, v, *want[2:]), (39, v, *want[2:])):
+        x[i, 1, (7 * i) % 128] = what
+        codes[0, 1, i], scale[0, 1, i] = 0, abs(what)
+    cache = api.new_kv_cache(1, heads, rows, api.W_INT4 if int4 else api.W_INT8)
+    api.focr_kv_write(cache, dev(k), dev(v), ints([rows]), ints([0]))
+    torch.cuda.synchronize()
+    for got, x in zip(cache, want):
+        np.testing.assert_array_equal(got.cpu().numpy(), x)
+    for got, bad in zip(api.focr_kv_read(cache, ints([rows])), ([3, 17], [17, 39])):
+        nan = np.isnan(got.cpu().numpy()[0])
+        assert nan[1, bad].all() and nan.sum() == 2 * 128
+    # rows 0 .. 2 are fine; row 3 is seen by the second sequence
+    two = [torch.cat((x, x)) for x in cache]
+    q = dev(f32(rng, 2, 1, heads, 128))
+    ring = api.new_kv_cache(2, heads, 128, api.W_INT4 if int4 else api.W_INT8)
+    out = api.focr_rswa_tree(q, q, q, two, ints([3, 4]), ring, ints([0, 0]))
+    assert out[1, 0, 1].isnan().all() and out.isfinite().sum().item() == 3 * 128

@@ -570,5 +570,11 @@ __device__ __forceinline__ void bf16x2_to_f32(uint32_t w, float& a, float& b) {
     b = __uint_as_float(w & 0xFFFF0000u);
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 }  // namespace focr
 #endif

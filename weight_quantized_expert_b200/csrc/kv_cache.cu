@@ -57,16 +57,17 @@ __device__ __forceinline__ uint32_t codes4(float4 x, float inv, float& far) {
 // A row of 128 by half a warp: lane l has values 4 l .. 4 l + 3 (a) and 64 + 4 l .. 64 + 4 l + 3 (b).
 template <bool INT4>
 __device__ __forceinline__ void quantise_row(float4 a, float4 b, bool live, uint8_t* codes, float* scale, int l) {
-    float m = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
-                    fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+    // a NaN in the row becomes the scale, so that it is not taken for a number later (an infinity does the same by itself)
+    float m = max_nan(max_nan(max_nan(fabsf(a.x), fabsf(a.y)), max_nan(fabsf(a.z), fabsf(a.w))),
+                      max_nan(max_nan(fabsf(b.x), fabsf(b.y)), max_nan(fabsf(b.z), fabsf(b.w))));
 #pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 8; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float s = m / (INT4 ? 7.f : 127.f), inv = 1.f / s;
     uint32_t w[2] = {0u, 0u};
     if (s > 0.f) {
         float far = 0.f;
         w[0] = codes4(a, inv, far), w[1] = codes4(b, inv, far);
-        // scales near the subnormal numbers (reciprocals that overflow, rounded scales) and what is no number go the same way
+        // scales near the subnormal numbers (reciprocals that overflow, rounded scales) and infinite ones go the same way
         if (!(far < 0.5f - 3.1e-5f) || !(s > 1e-35f) || !(s < 1e35f)) w[0] = codes_by_division<INT4>(a, s), w[1] = codes_by_division<INT4>(b, s);
         if (INT4) {   // bytes to nibbles
 #pragma unroll

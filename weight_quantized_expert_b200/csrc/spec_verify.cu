@@ -61,11 +61,6 @@ struct ProbsParams {
     float scale, scale_lo;   // log2(e) / temperature, as a sum of two floats
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 // exp((x - base) / temperature).  The exponent's rounding is that of the difference and of one product (the scale
 // carries two floats).  -inf is held at a finite value, whose exponential is 0, so that the sum below stays finite.
 __device__ __forceinline__ float expo(float x, float base, const ProbsParams& p) {
