@@ -190,3 +190,18 @@ def test_a_row_with_what_is_no_number_is_written_as_such(what, int4):
     ring = api.new_kv_cache(2, heads, 128, api.W_INT4 if int4 else api.W_INT8)
     out = api.focr_rswa_tree(q, q, q, two, ints([3, 4]), ring, ints([0, 0]))
     assert out[1, 0, 1].isnan().all() and out.isfinite().sum().item() == 3 * 128
+
+
+def test_a_flat_ragged_prompt_is_written_whole_by_default():
+    # offsets and counts alone: a sequence may have more than its share of the rows
+    import torch
+    rng = np.random.default_rng(82)
+    k, v = f32(rng, 50, 2, 128), f32(rng, 50, 2, 128)
+    want = np_cache(rng, 3, 2, 64, False)
+    cache = dev_cache(want)
+    count, row0 = [40, 1, 9], [0, 40, 41]
+    api.focr_kv_write(cache, dev(k), dev(v), ints(count), ints([0, 5, 55]), row0=ints(row0))
+    sp.kv_write(want, k, v, count, [0, 5, 55], row0, n_max=50)
+    torch.cuda.synchronize()
+    for got, x in zip(cache, want):
+        np.testing.assert_array_equal(got.cpu().numpy(), x)

@@ -429,6 +429,7 @@ def focr_rswa_decode(q, k_new, v_new, k_ref, v_ref, ref_len, k_ring, v_ring, n_g
 # ---------------------------------------------------------------- speculative decode step
 
 QK_NORM, ROPE_INTERLEAVED, KV_WRAP = 1, 2, 1
+KV_N_MAX = 32768
 _torch = None
 
 
@@ -565,7 +566,8 @@ def focr_kv_write(cache, k, v, count, start, row0=None, index=None, n_max: int |
                   stream=None):
     """Quantise rows of k, v [rows, heads, 128] (rows may be strided) into the cache: sequence b's i-th token, source row
     (row0[b] or b * n_max) + (index[b, i] or i), goes to slot start[b] + i (mod cap with wrap=True).  n_max: the most
-    tokens of a sequence (default: the columns of index, else rows // B)."""
+    tokens of a sequence; one with a larger count writes nothing (default: the columns of index; else rows // B, or with
+    row0, where a sequence may have any of the rows, all of them: the true maximum is cheaper)."""
     torch, L = _tensor_lib()
     dev = _device_of(k, "k")
     desc, B, heads, _ = _kv_desc(cache, dev)
@@ -574,7 +576,10 @@ def focr_kv_write(cache, k, v, count, start, row0=None, index=None, n_max: int |
     kp, ldk = _need_rows("k", k, dev, shape)
     vp, ldv = _need_rows("v", v, dev, shape)
     if n_max is None:
-        n_max = index.shape[1] if index is not None else max(1, shape[0] // B)
+        if index is not None:
+            n_max = index.shape[1]
+        else:
+            n_max = max(1, shape[0] // B if row0 is None else min(shape[0], KV_N_MAX))
     _call(L.focr_kv_write, dev, stream, desc, kp, ldk, vp, ldv, shape[0],
           None if row0 is None else _need_tensor("row0", row0, dev, i32, (B,)), _need_tensor("count", count, dev, i32, (B,)),
           None if index is None else _need_tensor("index", index, dev, i32, (B, n_max)), n_max,
