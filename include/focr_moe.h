@@ -437,6 +437,16 @@ focr_status focr_rswa_decode(const float* q, const float* k_new, const float* v_
  * "Four bits, one shared scale" (the codes).  The pages fix none of these formulas; each call states its own.
  * Every call is asynchronous on `stream`, holds no state between calls and gives the same bits for the same inputs.
  * Calls may overlap as long as no buffer that one of them writes (a workspace is one) is used by another.
+ *
+ * How the calls make a step.  A sequence has n committed tokens (n_gen; their rows are in the ring) and one sampled token x
+ * that is not committed yet: it has no row in the ring.  With D drafts behind it (draft i's parent is a draft or, -1, x):
+ *   1. the tree has D + 1 nodes: node 0 is x, with parent -1; node i + 1 is draft i, with the draft's parent + 1.  A node of
+ *      depth d stands at position n + d.  focr_qk_norm_rope, then focr_rswa_tree with n_gen = n;
+ *   2. the D + 1 rows of logits go through focr_token_probs and are focr_spec_verify's target rows as they stand; its
+ *      tokens, parents and n_nodes are the drafts' own, not shifted;
+ *   3. focr_kv_write commits x and the accepted drafts to the ring: index = {0, path[0] + 1, path[1] + 1, ...},
+ *      count = n_accept + 1, start = n, FOCR_KV_WRAP;
+ *   4. n += n_accept + 1, and x = next_token.
  */
 #define FOCR_HEADS_MAX 128          /* most heads (query or kv) of these calls */
 #define FOCR_TREE_NODES_MAX 64      /* most drafted nodes x query heads per kv head */
@@ -514,7 +524,7 @@ focr_status focr_kv_read(const focr_kv_cache* c, const int32_t* len, float* k_ou
  * (positions 0 .. n - 1, token p in ring slot p mod 128) it stands at position n + d and sees the reference rows
  * 0 .. ref_len[b] - 1, the ring's tokens max(0, n - 128, n + d - 127) .. n - 1, its ancestors and itself:
  *     out = sum_j softmax_j(q . k_j / sqrt(128)) v_j;   query head x reads kv head x / (heads_q / heads).
- * The ring is not written: focr_kv_write with FOCR_KV_WRAP commits accepted nodes.
+ * The ring is not written: focr_kv_write with FOCR_KV_WRAP commits node 0 and the accepted ones (see above).
  *   q, out: DEVICE fp32 [B][N][heads_q][128]; k_new, v_new: DEVICE fp32 [B][N][heads][128] (heads of the caches),
  *   finite for live nodes; 16-byte aligned.  parent: DEVICE int32 [B][N] or NULL (a chain: parent of i is i - 1).
  *   n_nodes: DEVICE int32 [B] or NULL (N each).  ref_len, n_gen: DEVICE int32 [B].

@@ -205,3 +205,105 @@ def test_a_flat_ragged_prompt_is_written_whole_by_default():
     torch.cuda.synchronize()
     for got, x in zip(cache, want):
         np.testing.assert_array_equal(got.cpu().numpy(), x)
+
+
+# ---------------------------------------------------------------- consecutive steps
+
+def test_consecutive_steps_attend_over_what_the_ones_before_committed():
+    """Three steps as the header puts them together: the sampled token is node 0 of the next tree, [0, path + 1] is committed,
+    n_gen advances by n_accept + 1.  Each token's attention is checked against the plain formula over the sequence of committed
+    tokens (no tree, no ring): positions P - 127 .. P, the rows of earlier steps as the quantiser leaves them.  Then the same
+    from a captured step, replayed."""
+    import torch
+    rng = np.random.default_rng(91)
+    B, D, heads, V, R, S = 3, 6, 4, 12, 100, 3
+    N, G = D + 1, heads * 128
+    parent = [-1, -1, 0, 0, 1, 2]
+    nodes = [-1] + [p + 1 for p in parent]
+    depth = [len(x) - 1 for x in sp.tree_lines(nodes)]
+    first, ref_len = [126, 0, 300], [100, 0, 37]
+    tables = [dev(f32(rng, V, G)) for _ in range(3)]
+    head = dev(0.3 * f32(rng, G, V))
+    prompt, old = [f32(rng, B * R, heads, 128) for _ in range(2)], [f32(rng, B * 300, heads, 128) for _ in range(2)]
+    drafts = rng.integers(0, V, (S, B, D)).astype(np.int32)
+    u = rng.random((S, B, D + 1), np.float32)
+    u[:, 0, [0, 2]], u[:, 2, :D] = 0.0, 0.999          # the first sequence accepts drafts 0 and 2, the last one few or none
+    x_first = rng.integers(0, V, B).astype(np.int32)
+    ref, ring = api.new_kv_cache(B, heads, R), api.new_kv_cache(B, heads, 128)
+    api.focr_kv_write(ref, dev(prompt[0]), dev(prompt[1]), ints(ref_len), ints([0] * B), n_max=R)
+    api.focr_kv_write(ring, dev(old[0]), dev(old[1]), ints(first), ints([0] * B), n_max=300, wrap=True)
+    start = [x.clone() for x in ring]
+    x, n, d_drafts, d_u = ints(x_first), ints(first), dev(drafts[0]), dev(u[0])
+    d_depth, d_nodes, d_parent, d_len = ints(depth), ints([nodes] * B), ints([parent] * B), ints(ref_len)
+
+    def step():
+        toks = torch.cat((x[:, None], d_drafts), 1)
+        q, k, v = (t[toks.long()].view(B * N, heads, 128) for t in tables)
+        q, k = api.focr_qk_norm_rope(q, k, (n[:, None] + d_depth).view(-1), norm=True)
+        shape = (B, N, heads, 128)
+        out = api.focr_rswa_tree(q.view(shape), k.view(shape), v.view(shape), ref, d_len, ring, n, d_nodes)
+        probs = api.focr_token_probs(out.view(B * N, G) @ head, 0.9).view(B, N, V)
+        taken, path, nxt = api.focr_spec_verify(probs, None, d_drafts, d_parent, None, d_u)
+        index = torch.cat((torch.zeros_like(x)[:, None], path + 1), 1)
+        api.focr_kv_write(ring, k, v, taken + 1, n, index=index, n_max=N, wrap=True)
+        n.add_(taken + 1)
+        x.copy_(nxt)
+        return dict(q=q, k=k, v=v, out=out, probs=probs, taken=taken, path=path, next=nxt, n=n, x=x)
+
+    def steps(one):
+        for t, y in zip(ring, start):
+            t.copy_(y)
+        x.copy_(ints(x_first))
+        n.copy_(ints(first))
+        got = []
+        for s in range(S):
+            d_drafts.copy_(dev(drafts[s]))
+            d_u.copy_(dev(u[s]))
+            got.append({name: t.clone().cpu().numpy() for name, t in one().items()})
+        return got
+
+    got = steps(step)
+    rows = lambda t: sp.values(*sp.quantise(t, False))  # noqa: E731
+    r = [rows(t.reshape(B, R, heads, 128)) for t in prompt]
+    seqs = [[[list(rows(t.reshape(B, 300, heads, 128)[b, :first[b]])) for t in old], int(x_first[b])] for b in range(B)]
+    for s, g in enumerate(got):
+        want = sp.spec_verify(g["probs"], None, drafts[s], np.array([parent] * B), None, u[s])
+        for name, w in zip(("taken", "path", "next"), want):
+            np.testing.assert_array_equal(g[name], w)
+        lines = sp.tree_lines(nodes)
+        for b, seq in enumerate(seqs):
+            kv, tok = seq
+            P = len(kv[0])
+            q, k, v, out = (g[name].reshape(B, N, heads, 128)[b] for name in ("q", "k", "v", "out"))
+            at = sp.qk_norm_rope(tables[1].cpu().numpy()[np.r_[tok, drafts[s, b]]].reshape(N, heads, 128), [P + d for d in depth], norm=True)
+            assert np.abs(k - at).max() <= 2e-5            # the sampled token and the drafts, at their positions
+            for i, line in enumerate(lines):
+                line = line[::-1]
+                keys, vals = ([*np.asarray(c)[:], *y[line]] for c, y in zip(kv, (k, v)))
+                keys, vals = keys[-128:], vals[-128:]
+                for h in range(heads):
+                    kk = np.array([*r[0][b, :ref_len[b], h], *[z[h] for z in keys]], np.float64)
+                    vv = np.array([*r[1][b, :ref_len[b], h], *[z[h] for z in vals]], np.float64)
+                    w = kk @ q[i, h].astype(np.float64) / np.sqrt(128)
+                    w = np.exp(w - w.max())
+                    assert np.abs(out[i, h] - w @ vv / w.sum()).max() <= TOL_TREE * np.abs(vv).max(), (s, b, i, h)
+            done = [0, *(g["path"][b, :g["taken"][b]] + 1)]
+            for c, y in zip(kv, (k, v)):
+                c += list(rows(np.ascontiguousarray(y[done])))
+            seq[1] = int(g["next"][b])
+            assert g["n"][b] == len(kv[0]) and g["x"][b] == seq[1]
+        assert g["taken"][0] >= 2
+    final = [t.clone() for t in ring]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+
+    def replay():
+        graph.replay()
+        return held
+
+    for a, b in zip(got, steps(replay)):
+        for name in a:
+            np.testing.assert_array_equal(a[name], b[name], err_msg=name)
+    for a, b in zip(final, ring):
+        assert torch.equal(a, b)
