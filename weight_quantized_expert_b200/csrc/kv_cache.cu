@@ -8,8 +8,9 @@
 // Both kernels are bound by memory: 512 B of fp32 against 132 B (int8) or 68 B (int4) a row, each moved once.  Half a warp
 // has a token of a head, its K and its V row, with all loads issued before the first is used, and a division only where a
 // value lies next to a border of the rounding.  8 sequences x 10 heads x ragged 4096 rows, int8, written and read back (659
-// MB): 106 us, 6.2 TB/s (a warp a row, all divided: 159 us; values rounded, clamped and packed one by one: 112 us, bound by
-// the write's instructions); 8 x 9 tokens into an int4 ring and the ring read back: 5.2 us, two launches.
+// MB): 106 us from a graph, 6.2 TB/s, and 111 us called on inputs that change (from a graph: a warp a row, all divided 159 us;
+// values rounded, clamped and packed one by one 112 us, bound by the write's instructions); 8 x 9 tokens into an int4 ring 2.3
+// us, the ring read back 3.0.
 #include "abi_util.h"
 #include "common.cuh"
 #include "kv_cache.h"

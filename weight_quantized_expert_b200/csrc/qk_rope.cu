@@ -8,8 +8,9 @@
 // The angle is formed in revolutions in fp64 and reduced to [-1/2, 1/2] before it is rounded to fp32, so far
 // positions lose nothing: the reduced angle is off by at most 2^-25 revolutions plus pos x 2^-53 x a few.
 //
-// Bound by memory: every row is read and written once, 1 KB a row.  8192 tokens x 20 heads with norms (168 MB): 29.2 us, 5.7
-// TB/s (31.6 with 40 registers instead of 32, a few of them spilled); one token: 1.7 us.  A block a token, its rows' loads ahead of the angles, half a warp a row (a warp a row with the
+// Bound by memory: every row is read and written once, 1 KB a row.  8192 tokens x 20 heads with norms (168 MB): 29.3 us from a
+// graph, 5.7 TB/s, and 32.2 us called on inputs that change (31.6 from a graph with 40 registers instead of 32, a few of them
+// spilled); one token: 1.7 us.  A block a token, its rows' loads ahead of the angles, half a warp a row (a warp a row with the
 // angles first: 50 us; blocks that stay and take tokens in turn: 66 us, each waiting for the angles of its next token).
 #include <math.h>
 

@@ -7,13 +7,15 @@
 // needs a quarter fewer instructions than two warps a block, which pays once the device is full (217 us against 258 us for
 // 8 sequences x 10 heads x 32 nodes over 32768 rows, int8); with few blocks a warp the other form's lower latency wins.
 //
-// Measured: 8 x 10 x 32 nodes over ragged 32768 rows, int8 (549 MB, 85 us at the copy rate): 209 us; 32 x 10 x 14 columns
-// over ragged 4096 rows, int4 (146 MB, 23 us): 73 us.  What bounds it is the work between the products: a block of 16
-// columns x 64 keys takes 192 matrix instructions (1540 cycles of a scheduler's tensor core) and 1550 others (digits taken
-// apart and put together, exponentials, transposed values), 3000 cycles with two warps a scheduler; registers leave no
-// room for a third.  Beginning and ending a unit costs 5 us (13 us with a column a warp at a time and ranges that
-// did not count it: 225 and 87 us).  The tensor-memory form of the same products (kind::i8) came to 224 and 125 us with
-// four times the error: its exponentials wait on tensor-memory loads instead.
+// Measured: 8 x 10 x 32 nodes over ragged 32768 rows, int8 (549 MB, 85 us at the copy rate): 210 us from a graph, 239 us called
+// on inputs that change; 32 x 10 x 14 columns over ragged 4096 rows, int4 (146 MB, 23 us): 75 us.  A block of 16 columns x 64
+// keys takes 192 matrix instructions and some 1590 others (digits taken apart and put together, exponentials, transposed
+// values).  No unit is full: over 8192 rows 1.64 of 4 issue slots are used, the tensor pipe 37%, DRAM 34% of the time.  A warp
+// does its products and its softmax one after the other, and the two warps of a scheduler overlap too little; registers
+// leave no room for a third.  More than 16 columns are several units, each of which copies and takes apart all rows (192 MB
+// read for 140 in that profile).  Beginning and ending a unit costs 5 us (13 us with a column a warp at a time and ranges
+// that did not count it).  The tensor-memory form of the same products (kind::i8) came to 224 and 125 us when this one
+// took 217 and 90: its exponentials wait on tensor-memory loads instead.
 #include <math.h>
 
 #include "abi_util.h"
@@ -49,7 +51,7 @@ struct Shared {
 };
 
 // A unit's length in the row: what it costs to begin it, in blocks, and its blocks (one at least: the drafted keys need a
-// CTA too).  BEGIN = 3 / 6 / 9: 76.3 / 73.2 / 74.3 us for the int4 call above.
+// CTA too).  BEGIN = 3 / 6 / 9 made 76.3 / 73.2 / 74.3 us of the int4 call above when it was chosen.
 constexpr int BEGIN = 6;
 __device__ __forceinline__ int unit_length(const TreeParams& p, int b) {
     const int R = __ldg(p.ref_len + b), n = __ldg(p.n_gen + b);

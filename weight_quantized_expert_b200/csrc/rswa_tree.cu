@@ -40,7 +40,7 @@
 // are few: all columns walk their lines at once on the CUDA cores, before the blocks.  Long or many units go to
 // rswa_ranges.cu.
 // 264 B (int8) or 136 B (int4) a key and head have to be read; for the calls that come here latency is the bound: 1
-// sequence x 10 heads x 1 node over 289 rows 7.1 us, 8 x 10 x 16 nodes 13.0 us.  The chain is lengths -> lines -> drafted
+// sequence x 10 heads x 1 node over 289 rows 7.3 us, 8 x 10 x 16 nodes 13.0 us.  The chain is lengths -> lines -> drafted
 // rows (2 us), a block's copies and products (2 us), the join of warps and CTAs (2 us).
 #include <math.h>
 

@@ -22,7 +22,7 @@
 // are in flight while the row before is worked on, and stays in registers (KEPT groups of four values a thread; what a
 // row has beyond that is read again).  The CTAs send each other maximum and sum by st.async on a barrier in shared
 // memory; a cluster barrier would wait for the stores of the row's probabilities as well.  A wait that runs out (it
-// needs a CTA of the cluster to stop) gives NaN.  289 rows of 129280: 67.7 us, 4.4 TB/s (a cluster per
+// needs a CTA of the cluster to stop) gives NaN.  289 rows of 129280: 67 us, 4.4 TB/s (a cluster per
 // row, without copies ahead: 87 us; taking rows in turn with a cluster barrier: 104 us); one row of 129280: 6.3 us.
 // Clusters of eight CTAs of which two share an SM stay on 132 of 148 SMs.  Each row has one
 // serial exchange through the cluster between its loads and its stores; that is what is left.
@@ -31,8 +31,8 @@
 // latency; a rejection is one pass over the rows, spread over the cluster's warps.  The tiles' sums stay in shared
 // memory and lead to the next token's tile without a second pass over the rows.  One tree of 4 nodes: 9.0 us; 32 trees
 // of 16 nodes, V = 129280: 24 us (with the warps' tiles summed a second time, the answer agreed on by two more cluster
-// barriers and sums fetched instead of stored: 12.3 and 25.4 us).  What is left is the chain of passes: up to one per rejected sibling, each a
-// cluster-wide sum.
+// barriers and sums fetched instead of stored: 12.3 and 25.4 us).  What is left is the chain of passes: up to one per rejected
+// sibling, each over the whole row pair with a cluster-wide sum.
 #include <math.h>
 
 #include "abi_util.h"
